@@ -82,7 +82,7 @@ extern "C" {
 /* Status codes. */
 #define MOE_OK 0
 #define MOE_EINVAL -1        /* null pointer, negative or inconsistent size, misalignment */
-#define MOE_EUNSUPPORTED -2  /* H or I not a multiple of 32, k > min(E, 32), E > 1024, S > 8192 */
+#define MOE_EUNSUPPORTED -2  /* H or I not a multiple of 32, k > min(E, 32), E > 1024, S > 8192, or past an entry point's own limits */
 #define MOE_EWORKSPACE -3    /* ws_bytes below moe_workspace_bytes(...) */
 #define MOE_EHIP -4          /* a HIP launch or copy reported an error */
 #define MOE_ESCRATCH -5      /* the batch needs more than the library's own scratch holds */
@@ -573,6 +573,173 @@ int moe_boot_plan(const double* hist, int L, int E, int k, int n_slots, int32_t*
  * makes the resident set follow new traffic faster).  MOE_EINVAL for a null
  * or misaligned pointer (8 bytes) or a factor outside [0, 1]. */
 int moe_history_scale(double* hist, size_t n, double factor, hipStream_t stream);
+
+/*
+ * Rows in the order of the slots: the token rows of a batch copied into the
+ * order of moe_route's bucketing and summed back, with weights and gradients,
+ * for experts that run outside the library (another weight format, a framework's
+ * own products, training) or through moe_int8_matmul.
+ *
+ * Assignment a = t*k + j is pick j of token t; row p of a "rows" array
+ * [T*k][H] belongs to assignment perm[p].  perm and weight are moe_route's perm
+ * and sel_weight (or arrays of that form: perm names every assignment at most
+ * once; entries outside [0, T*k) name none).
+ */
+
+/* Element types (moe_rows_args.dtype, moe_int8_quantize, moe_int8_matmul). */
+#define MOE_DT_BF16 0
+#define MOE_DT_FP16 1
+#define MOE_DT_FP32 2
+
+/*
+ * moe_positions -- the inverse of perm: pos[perm[p]] = p, and pos[a] = -1 for
+ * the assignments that perm does not name (padded picks).  An assignment named
+ * twice gets the larger p.
+ * Input  : perm [T*k] int32.   Output : pos [T][k] int32 (must not alias perm).
+ * Errors : MOE_EINVAL for null or misaligned (4-byte) pointers, T < 0 or
+ *          k <= 0; MOE_EUNSUPPORTED for k > MOE_MAX_K or T*k > 2^31 - 1.
+ *          T = 0 is valid and does nothing.
+ */
+int moe_positions(const int32_t* perm, int T, int k, int32_t* pos, hipStream_t stream);
+
+/*
+ * moe_dispatch -- src [T][H] token rows, dst [T*k][H] rows:
+ *   dst[pos[t,j]] = w[t,j] * src[t]         (w = 1 and a plain copy if weight is NULL)
+ *   dst[p] = 0 where perm[p] names no assignment, if perm is given; with perm
+ *   NULL, the rows that pos does not name are left as they were.
+ * moe_dispatch_backward -- its gradient; src [T*k][H] the gradient of the
+ * rows, dst [T][H] that of the token rows, other [T][H] the forward call's src:
+ *   dst[t] = sum_j w[t,j] * src[pos[t,j]]
+ *   dweight[t,j] = sum_h src[pos[t,j]][h] * other[t][h]
+ * moe_combine -- src [T*k][H] rows, dst [T][H]:
+ *   dst[t] = sum_j w[t,j] * src[pos[t,j]]
+ * moe_combine_backward -- its gradient; src [T][H] the gradient of the output,
+ * dst [T*k][H] that of the rows, other [T*k][H] the forward call's src:
+ *   dst[pos[t,j]] = w[t,j] * src[t], and perm as in moe_dispatch
+ *   dweight[t,j] = sum_h other[pos[t,j]][h] * src[t][h]
+ *
+ * A pick without a row (pos outside [0, T*k)) is skipped: it adds nothing, its
+ * dweight is 0, and a token with no rows at all gets a zero row.  Sums are
+ * float32 over ascending j, dot products float32 in a fixed order; every value
+ * is rounded once to the element type.  Infinities and NaN pass through and
+ * touch only the rows and tokens that they belong to.
+ *
+ * src_stride, dst_stride, other_stride: elements from one row to the next
+ *          (>= H); rows may start at any element.  dst must not overlap an input.
+ * dweight and other are both given or both NULL (the backward calls; NULL in
+ * the others).  perm is nullable and given only to moe_dispatch and
+ * moe_combine_backward.  weight is nullable everywhere (all ones).
+ * Errors : MOE_EINVAL for null or misaligned pointers (the element's size; 4
+ *          bytes for int32 and float), T < 0, H or k <= 0, a stride below H, an
+ *          unknown dtype or an argument given to a call that has no use for it;
+ *          MOE_EUNSUPPORTED for k > MOE_MAX_K, T*k > 2^31 - 1 or H > 2^30.
+ *          T = 0 is valid and does nothing.  No workspace.
+ */
+typedef struct moe_rows_args {
+  int T, H, k, dtype;
+  const int32_t* perm;
+  const int32_t* pos;
+  const float* weight;
+  const void* src;
+  size_t src_stride;
+  void* dst;
+  size_t dst_stride;
+  const void* other;
+  size_t other_stride;
+  float* dweight;
+} moe_rows_args;
+
+int moe_dispatch(const moe_rows_args* args, hipStream_t stream);
+int moe_dispatch_backward(const moe_rows_args* args, hipStream_t stream);
+int moe_combine(const moe_rows_args* args, hipStream_t stream);
+int moe_combine_backward(const moe_rows_args* args, hipStream_t stream);
+
+/*
+ * 8-bit integer rows and products: experts (or any dense layer) whose weights
+ * are 8-bit integers with one float scale for each output channel, on activation
+ * rows quantised to 8-bit integers with one scale for each token.  Next to the
+ * MXFP4 path: moe_route's bucketing, then moe_int8_quantize of the token rows,
+ * moe_int8_matmul with swiglu (rows by index), moe_int8_quantize of the result,
+ * moe_int8_matmul, moe_combine.
+ *
+ * int8 row : K bytes, two's complement, at 16-byte aligned addresses;
+ *            moe_int8_row_bytes(K) (K rounded up to 16) bytes are read or
+ *            written, those past K as zero or ignored.
+ */
+
+/* Bytes of an int8 row of K elements; 0 for K <= 0 or K > 131056 (the largest
+ * contraction whose 32-bit sums cannot overflow). */
+size_t moe_int8_row_bytes(int K);
+
+/*
+ * moe_int8_quantize -- for each row m of x [M][K]:
+ *   scale[m] = max(max_i |x[m][i]| / 127, 2^-126)      (float32 division)
+ *   q[m][i]  = x[m][i] / scale[m], the exact quotient rounded to the nearest
+ *              integer, ties to even (within +-127); bytes K .. up to the row's
+ *              end are zero.
+ * A row of zeros has zeros and scale 2^-126; a row with an infinity or a NaN
+ * has zeros and scale NaN.
+ * Inputs : x of the element type `dtype`, rows x_stride elements apart (>= K),
+ *          at any element.
+ * Outputs: q, 16-byte aligned rows q_stride bytes apart (a multiple of 16, >=
+ *          moe_int8_row_bytes(K)); scale [M] float.
+ * Errors : MOE_EINVAL for null or misaligned pointers, M < 0, K <= 0, a bad
+ *          stride or an unknown dtype; MOE_EUNSUPPORTED for K > 131056.
+ *          M = 0 is valid and does nothing.  No workspace.
+ */
+int moe_int8_quantize(const void* x, int M, int K, size_t x_stride, int dtype, int8_t* q,
+                      size_t q_stride, float* scale, hipStream_t stream);
+
+/*
+ * moe_int8_matmul -- rows p of out [M][N], over the groups of a bucketing or
+ * dense:
+ *   y[p][n] = a_scale[r] * b_scale[g][n] * sum_i a[r][i] * b[g][n][i]
+ *   out[p][n] = y[p][n], or with swiglu (b has 2N rows, N gate rows and then
+ *               N up rows): silu(y[p][n]) * y[p][N+n], silu(v) = v / (1 + exp(-v))
+ * with exact 32-bit integer sums, float32 scaling and one rounding to the
+ * element type out_dtype.
+ *   G > 0 : offsets [G+1] int32 (moe_route's slot_offsets); rows
+ *           [offsets[g], offsets[g+1]) belong to group g.  Rows in no group are
+ *           left as they were.  Offsets are cut to [0, M].
+ *   G = 0 : offsets NULL; all M rows use the one matrix b.
+ *   r = p, or with index: index[p] / index_div (moe_route's perm and k name the
+ *           token of a row).  Rows whose r is outside [0, a_rows) are left as
+ *           they were; nothing is read for them.
+ * Inputs : a [a_rows][K] int8 rows a_stride bytes apart; a_scale [a_rows]; b: N
+ *          (2N with swiglu) int8 rows, b_stride bytes apart, for each group,
+ *          groups b_group_stride bytes apart; b_scale [N (2N)] for each group,
+ *          b_scale_group_stride floats apart (so a group's matrix and scales
+ *          may lie in an arena slot).  int8 rows as above: strides are multiples
+ *          of 16 and >= moe_int8_row_bytes(K).
+ * Output : out, rows out_stride elements apart (>= N), at any element; must not
+ *          overlap an input.
+ * Errors : MOE_EINVAL for null or misaligned pointers (16 bytes for a and b), a
+ *          bad size, stride, dtype or flag, offsets without G or G without
+ *          offsets, index without index_div >= 1, or fewer rows of a than M
+ *          without index; MOE_EUNSUPPORTED for K > 131056, N > 2^24 or G >
+ *          MOE_MAX_S.  M = 0 is valid and does nothing.  No workspace.
+ */
+typedef struct moe_int8_matmul_args {
+  int M, N, K, G;
+  int swiglu;
+  int a_rows;
+  const int8_t* a;
+  size_t a_stride;
+  const float* a_scale;
+  const int32_t* index;
+  int index_div;
+  const int32_t* offsets;
+  const int8_t* b;
+  size_t b_stride;
+  size_t b_group_stride;
+  const float* b_scale;
+  size_t b_scale_group_stride;
+  void* out;
+  size_t out_stride;
+  int out_dtype;
+} moe_int8_matmul_args;
+
+int moe_int8_matmul(const moe_int8_matmul_args* args, hipStream_t stream);
 
 /*
  * moe_test_mxfp4_probe -- test-only: one wave runs one block-scaled MXFP4

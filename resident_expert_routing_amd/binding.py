@@ -33,6 +33,9 @@ MOE_OP_EXPERTS_SHARED = 4
 MOE_OP_ACT_MXFP6 = 0x10
 MOE_ACT_MXFP4 = 0
 MOE_ACT_MXFP6 = 1
+MOE_DT_BF16 = 0
+MOE_DT_FP16 = 1
+MOE_DT_FP32 = 2
 MOE_MAX_E = 1024
 MOE_MAX_K = 32
 MOE_MAX_S = 8192
@@ -45,6 +48,8 @@ EXPORTS = ("moe_status_string", "moe_mxfp4_row_bytes", "moe_act_row_bytes", "moe
            "moe_workspace_bytes", "moe_route", "moe_demand_accumulate", "moe_experts_forward",
            "moe_experts_forward_noalloc", "moe_ring_plan", "moe_ring_install",
            "moe_history_save", "moe_history_load", "moe_boot_plan", "moe_history_scale",
+           "moe_positions", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
+           "moe_combine_backward", "moe_int8_row_bytes", "moe_int8_quantize", "moe_int8_matmul",
            "arena_load_slot", "moe_hot_pick", "moe_hot_install", "moe_replan", "moe_test_mxfp4_probe",
            "moe_test_stream_read", "moe_test_mfma_loop")
 
@@ -80,6 +85,27 @@ class ExpertsArgs(ctypes.Structure):
                 ("stage_events", ctypes.c_void_p), ("defer_slot", ctypes.c_int),
                 ("defer_event", ctypes.c_void_p), ("shared_expert", ctypes.c_void_p),
                 ("act_format", ctypes.c_int)]
+
+
+class RowsArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int), ("k", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("perm", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("src", ctypes.c_void_p),
+                ("src_stride", ctypes.c_size_t), ("dst", ctypes.c_void_p),
+                ("dst_stride", ctypes.c_size_t), ("other", ctypes.c_void_p),
+                ("other_stride", ctypes.c_size_t), ("dweight", ctypes.c_void_p)]
+
+
+class Int8MatmulArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("G", ctypes.c_int), ("swiglu", ctypes.c_int), ("a_rows", ctypes.c_int),
+                ("a", ctypes.c_void_p), ("a_stride", ctypes.c_size_t),
+                ("a_scale", ctypes.c_void_p), ("index", ctypes.c_void_p),
+                ("index_div", ctypes.c_int), ("offsets", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("b_stride", ctypes.c_size_t),
+                ("b_group_stride", ctypes.c_size_t), ("b_scale", ctypes.c_void_p),
+                ("b_scale_group_stride", ctypes.c_size_t), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_size_t), ("out_dtype", ctypes.c_int)]
 
 
 MOE_STAGE_EVENTS = 5
@@ -142,6 +168,17 @@ def load() -> ctypes.CDLL:
     lib.moe_boot_plan.restype = i
     lib.moe_history_scale.argtypes = [vp, sz, ctypes.c_double, vp]
     lib.moe_history_scale.restype = i
+    lib.moe_positions.argtypes = [vp, i, i, vp, vp]
+    lib.moe_positions.restype = i
+    for name in ("moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward"):
+        getattr(lib, name).argtypes = [ctypes.POINTER(RowsArgs), vp]
+        getattr(lib, name).restype = i
+    lib.moe_int8_row_bytes.argtypes = [i]
+    lib.moe_int8_row_bytes.restype = sz
+    lib.moe_int8_quantize.argtypes = [vp, i, i, sz, i, vp, sz, vp, vp]
+    lib.moe_int8_quantize.restype = i
+    lib.moe_int8_matmul.argtypes = [ctypes.POINTER(Int8MatmulArgs), vp]
+    lib.moe_int8_matmul.restype = i
     lib.moe_test_mxfp4_probe.argtypes = [i, vp, vp, vp, vp, vp, vp]
     lib.moe_test_mxfp4_probe.restype = i
     lib.moe_test_stream_read.argtypes = [vp, ctypes.c_size_t, vp, i, vp]
@@ -340,6 +377,65 @@ def moe_boot_plan(hist, L, E, k, n_slots, expert_slot) -> int:
 
 def moe_history_scale(hist, n, factor, stream=None) -> int:
     return int(load().moe_history_scale(_ptr(hist), int(n), float(factor), _stream(stream)))
+
+
+def moe_positions(perm, T, k, pos, stream=None) -> int:
+    return int(load().moe_positions(_ptr(perm), int(T), int(k), _ptr(pos), _stream(stream)))
+
+
+def _rows_args(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight, perm=None,
+               other=None, other_stride=0, dweight=None):
+    return ctypes.byref(RowsArgs(int(T), int(H), int(k), int(dtype), _ptr(perm), _ptr(pos),
+                                 _ptr(weight), _ptr(src), int(src_stride), _ptr(dst),
+                                 int(dst_stride), _ptr(other), int(other_stride),
+                                 _ptr(dweight)))
+
+
+def moe_dispatch(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None, perm=None,
+                 stream=None) -> int:
+    return int(load().moe_dispatch(_rows_args(T, H, k, dtype, pos, src, src_stride, dst,
+                                              dst_stride, weight, perm), _stream(stream)))
+
+
+def moe_dispatch_backward(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None,
+                          other=None, other_stride=0, dweight=None, stream=None) -> int:
+    return int(load().moe_dispatch_backward(
+        _rows_args(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight, None, other,
+                   other_stride, dweight), _stream(stream)))
+
+
+def moe_combine(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None,
+                stream=None) -> int:
+    return int(load().moe_combine(_rows_args(T, H, k, dtype, pos, src, src_stride, dst,
+                                             dst_stride, weight), _stream(stream)))
+
+
+def moe_combine_backward(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None,
+                         perm=None, other=None, other_stride=0, dweight=None,
+                         stream=None) -> int:
+    return int(load().moe_combine_backward(
+        _rows_args(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight, perm, other,
+                   other_stride, dweight), _stream(stream)))
+
+
+def moe_int8_row_bytes(K: int) -> int:
+    return int(load().moe_int8_row_bytes(int(K)))
+
+
+def moe_int8_quantize(x, M, K, x_stride, dtype, q, q_stride, scale, stream=None) -> int:
+    return int(load().moe_int8_quantize(_ptr(x), int(M), int(K), int(x_stride), int(dtype),
+                                        _ptr(q), int(q_stride), _ptr(scale), _stream(stream)))
+
+
+def moe_int8_matmul(M, N, K, G, swiglu, a_rows, a, a_stride, a_scale, index, index_div, offsets,
+                    b, b_stride, b_group_stride, b_scale, b_scale_group_stride, out, out_stride,
+                    out_dtype, stream=None) -> int:
+    args = Int8MatmulArgs(int(M), int(N), int(K), int(G), 1 if swiglu else 0, int(a_rows),
+                          _ptr(a), int(a_stride), _ptr(a_scale), _ptr(index), int(index_div),
+                          _ptr(offsets), _ptr(b), int(b_stride), int(b_group_stride),
+                          _ptr(b_scale), int(b_scale_group_stride), _ptr(out), int(out_stride),
+                          int(out_dtype))
+    return int(load().moe_int8_matmul(ctypes.byref(args), _stream(stream)))
 
 
 def moe_test_mxfp4_probe(shape, a, a_scale, b, b_scale, d, stream=None) -> int:

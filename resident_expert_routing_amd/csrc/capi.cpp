@@ -16,7 +16,8 @@ extern "C" MOE_EXPORT const char* moe_status_string(int status) {
     case MOE_OK: return "MOE_OK: success";
     case MOE_EINVAL: return "MOE_EINVAL: null pointer, bad size or misaligned pointer";
     case MOE_EUNSUPPORTED:
-      return "MOE_EUNSUPPORTED: H or I not a multiple of 32, k > min(E, 32), E > 1024 or S > 8192";
+      return "MOE_EUNSUPPORTED: H or I not a multiple of 32, k > min(E, 32), E > 1024, S > 8192, "
+             "or another size past the entry point's limits";
     case MOE_EWORKSPACE: return "MOE_EWORKSPACE: workspace smaller than moe_workspace_bytes()";
     case MOE_EHIP: return "MOE_EHIP: a HIP launch or copy failed";
     case MOE_EIO: return "MOE_EIO: a history file could not be opened, read, written or renamed";

@@ -1,0 +1,427 @@
+// 8-bit integer rows and their matrix products: moe_int8_quantize,
+// moe_int8_matmul.
+//
+//   s[m]   = max(max_i |x[m,i]| / 127, 2^-126),  q[m,i] = round(x[m,i] / s[m])
+//   y[p,n] = sa[r] * sb[g,n] * sum_i qa[r,i] * qb[g,n,i]
+//
+// The sums are exact 32-bit integers on the matrix cores, so neither the order
+// of the contraction nor how it is split over waves changes a result; the two
+// scales are applied to the finished sum in float32.
+#include "elements.hpp"
+
+using namespace moe;
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126, the smallest normal float
+constexpr int kMaxGrid = 1 << 22;             // workgroups of a launch; they stride over the rest
+constexpr int kMaxK = 131056;                 // 128 * 128 * K stays below 2^31
+
+__host__ __device__ inline int up16(int v) { return (v + 15) & ~15; }
+
+// ---------------------------------------------------------------------------
+// moe_int8_quantize
+// ---------------------------------------------------------------------------
+constexpr int kQThreads = 256;
+constexpr int kQPieces = 4;  // 16-byte pieces of a row that a thread keeps
+
+// round(x / s) to the nearest integer, ties to even, of the exact quotient.
+// x * (1 / s) is within 2e-5 of it (|quotient| <= 127 and a bit, three
+// roundings of 2^-24 each), which decides everything but quotients that close
+// to a half; those are decided by the remainder x - q*s, exact in float64.
+__device__ __forceinline__ int quantized(float x, float s, float inv) {
+  const float t = x * inv;
+  float q = __builtin_rintf(t);
+  if (__builtin_expect(fabsf(fabsf(t - q) - 0.5f) < 1e-4f, 0)) {
+    const double e = fma(-(double)q, (double)s, (double)x), half = 0.5 * (double)s;
+    const float away = e > 0 ? 1.0f : -1.0f;
+    if (fabs(e) > half || (fabs(e) == half && ((int)q & 1))) q += away;
+  }
+  return (int)q;
+}
+
+// One pass: the row stays in registers between its maximum and its rounding
+// (rows past 256 threads x 4 pieces are read again, from the cache).  Bound by
+// memory.  A row that holds an infinity or a NaN gets scale NaN and zeros, so
+// that everything computed from it is NaN.
+template <typename E>
+__global__ __launch_bounds__(kQThreads) void quantize_rows(const E* __restrict__ x, int M, int K,
+                                                           size_t x_stride, int8_t* __restrict__ q,
+                                                           size_t q_stride,
+                                                           float* __restrict__ scale, int lanes) {
+  constexpr int N = Piece<E>::kN;
+  __shared__ uint32_t part[kQThreads / kWave];
+  const int per = kQThreads / lanes;
+  const int lane = threadIdx.x & (lanes - 1);
+  const int width = up16(K);
+  for (int64_t b = (int64_t)blockIdx.x * per; b < M; b += (int64_t)gridDim.x * per) {
+    const int64_t m = b + threadIdx.x / lanes;
+    const E* row = x + (m < M ? m : M - 1) * x_stride;
+    Piece<E> v[kQPieces];
+    uint32_t top = 0;
+    auto fold = [&](const Piece<E>& u) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        top = max(top, __float_as_uint(to_f32<E>(u.e[e])) & 0x7FFFFFFFu);
+    };
+#pragma unroll
+    for (int c = 0; c < kQPieces; ++c) {
+      const int i = (c * lanes + lane) * N;
+      if (i < K)
+        v[c].load_upto(row + i, K - i);
+      else
+        v[c] = Piece<E>{};
+    }
+#pragma unroll
+    for (int c = 0; c < kQPieces; ++c) fold(v[c]);
+    for (int i = (kQPieces * lanes + lane) * N; i < K; i += lanes * N) {
+      Piece<E> u;
+      u.load_upto(row + i, K - i);
+      fold(u);
+    }
+    top = wave_umax32(top);
+    if (lanes > kWave) {
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x / kWave] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kQThreads / kWave; ++w) top = max(top, part[w]);
+    }
+    const bool finite = top < 0x7F800000u;
+    const float s = fmaxf(__uint_as_float(top) / 127.0f, kMinScale);
+    const float inv = finite ? 1.0f / s : 0.0f;
+    if (m >= M) continue;
+    if (lane == 0) scale[m] = finite ? s : __uint_as_float(0x7FC00000u);
+    int8_t* out = q + m * q_stride;
+    auto put = [&](const Piece<E>& u, int i) {  // whole pieces: the row is padded to 16 bytes
+      Piece<int8_t, N> o;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        o.e[e] = finite ? (int8_t)quantized(to_f32<E>(u.e[e]), s, inv) : (int8_t)0;
+      o.store(out + i);
+    };
+#pragma unroll
+    for (int c = 0; c < kQPieces; ++c) {
+      const int i = (c * lanes + lane) * N;
+      if (i < width) put(v[c], i);
+    }
+    for (int i = (kQPieces * lanes + lane) * N; i < width; i += lanes * N) {
+      Piece<E> u{};
+      if (i < K) u.load_upto(row + i, K - i);
+      put(u, i);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// moe_int8_matmul
+// ---------------------------------------------------------------------------
+struct MatArgs {
+  int M, N, K, G, a_rows, index_div, out_dtype;
+  const int8_t* a;
+  const float* a_scale;
+  const int32_t* index;
+  const int32_t* offsets;
+  const int8_t* b;
+  const float* b_scale;
+  void* out;
+  size_t a_stride, b_stride, b_group_stride, b_scale_group_stride, out_stride;
+};
+
+struct Rows {
+  int g, lo, hi;  // rows [lo, hi) of out, at most as many as asked for, of group g
+};
+
+__device__ __forceinline__ int clamp_row(int v, int M) { return min(max(v, 0), M); }
+
+// The item-th piece of at most R rows, counted through the groups in order;
+// false past the last.  Every wave finds it by itself: each lane counts the
+// pieces of its share of the groups, a scan over the lanes gives the lane that
+// holds the piece, and that lane its group.  Offsets outside [0, M] are cut.
+__device__ __forceinline__ bool find_rows(const MatArgs& p, int item, int R, Rows& r) {
+  if (!p.offsets) {
+    r.g = 0, r.lo = item * R, r.hi = min(p.M, r.lo + R);
+    return r.lo < p.M;
+  }
+  const int lane = threadIdx.x & 63;
+  const int share = (p.G + 63) / 64;
+  const int g0 = min(lane * share, p.G), g1 = min(g0 + share, p.G);
+  auto pieces = [&](int g) {
+    const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+    return hi > lo ? (hi - lo) / R + ((hi - lo) % R != 0) : 0;
+  };
+  // Sums stop at a bound above every item, so that offsets which are no
+  // bucketing cannot overflow them.
+  constexpr int kMost = 1 << 29;
+  int sum = 0;
+  for (int g = g0; g < g1; ++g) sum = min(sum + pieces(g), kMost);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(sum, d, 64);
+    if (lane >= d) sum = min(sum + o, kMost);
+  }
+  const unsigned long long past = __ballot(sum > item);
+  if (past == 0) return false;
+  const int owner = __ffsll((long long)past) - 1;
+  int g = g0, before = __shfl_up(sum, 1, 64);
+  if (lane == 0) before = 0;
+  if (lane == owner)
+    for (; g < g1 - 1; ++g) {
+      const int n = pieces(g);
+      if (before + n > item) break;
+      before += n;
+    }
+  g = __builtin_amdgcn_readfirstlane(__shfl(g, owner, 64));
+  before = __builtin_amdgcn_readfirstlane(__shfl(before, owner, 64));
+  const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+  r.g = g;
+  r.lo = lo + (item - before) * R;
+  r.hi = min(hi, r.lo + R);
+  return r.lo < r.hi;
+}
+
+// Most pieces of R rows that M rows in G groups can make.
+inline int64_t max_items(int M, int G, int R) {
+  return (int64_t)M / R + (G > 0 ? (G < M ? G : M) : 1);
+}
+
+// The row of a that row m of out is computed from; -1 if it names none.
+__device__ __forceinline__ int source_row(const MatArgs& p, int m) {
+  int r = m;
+  if (p.index) {
+    r = p.index[m];
+    r = r < 0 ? -1 : r / p.index_div;
+  }
+  return (unsigned)r < (unsigned)p.a_rows ? r : -1;
+}
+
+__device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
+
+template <typename E>
+__device__ __forceinline__ void store4(const MatArgs& p, int m, int n, const float (&y)[4]) {
+  Piece<E, 4> o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.e[i] = from_f32<E>(y[i]);
+  o.store_upto((E*)p.out + (size_t)m * p.out_stride + n, p.N - n);
+}
+
+__device__ __forceinline__ void store_out(const MatArgs& p, int m, int n, const float (&y)[4]) {
+  if (p.out_dtype == MOE_DT_BF16)
+    store4<Bf16>(p, m, n, y);
+  else if (p.out_dtype == MOE_DT_FP16)
+    store4<Fp16>(p, m, n, y);
+  else
+    store4<float>(p, m, n, y);
+}
+
+// 16 bytes at element k of a row, zero from element K on; 0 <= k < up16(K).
+__device__ __forceinline__ i32x4 load_k(const int8_t* row, int k) {
+  return *(const i32x4*)(row + k);
+}
+__device__ __forceinline__ i32x4 mask_k(i32x4 v, int valid) {  // the first `valid` bytes
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int left = valid - 4 * w;
+    v[w] = left >= 4 ? v[w] : left <= 0 ? 0 : v[w] & (int)((1u << (8 * left)) - 1u);
+  }
+  return v;
+}
+
+// Streaming form, for few rows in each group: a workgroup takes 32 rows of b
+// (with SwiGLU, 16 gate rows and their 16 up rows) and up to 16 * MT rows of
+// one group, its kSWaves waves the chunks of 64 along K in turn; the integer
+// sums are added through LDS.  b goes from memory straight to the registers of
+// the matrix instruction (lane l: row l % 16, bytes 16 (l / 16) of the chunk),
+// since nothing else in the workgroup uses it.
+constexpr int kSWaves = 4;
+constexpr int kSUnroll = 4;  // chunks in flight
+
+template <int MT, bool GLU>
+__device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int n0,
+                                            i32x4 (&part)[kSWaves][MT * 2][kWave]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
+  const int col = lane & 15, quad = lane >> 4;
+
+  const int8_t* b = p.b + (size_t)r.g * p.b_group_stride;
+  const int8_t* brow[2];
+  brow[0] = b + (size_t)min(n0 + col, p.N - 1) * p.b_stride;
+  brow[1] = b + (size_t)(GLU ? p.N + min(n0 + col, p.N - 1) : min(n0 + 16 + col, p.N - 1)) *
+                    p.b_stride;
+  const int8_t* arow[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int src = source_row(p, min(r.lo + 16 * t + col, r.hi - 1));
+    arow[t] = p.a + (size_t)max(src, 0) * p.a_stride;
+  }
+
+  i32x4 acc[MT][2] = {};
+  const int full = p.K / 64;  // chunks that lie inside the rows
+  int c = wave;
+  for (; c + kSWaves * (kSUnroll - 1) < full; c += kSWaves * kSUnroll) {
+    i32x4 wb[kSUnroll][2], wa[kSUnroll][MT];
+#pragma unroll
+    for (int u = 0; u < kSUnroll; ++u) {
+      const int k = 64 * (c + kSWaves * u) + 16 * quad;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) wb[u][s] = load_k(brow[s], k);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) wa[u][t] = load_k(arow[t], k);
+    }
+#pragma unroll
+    for (int u = 0; u < kSUnroll; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          acc[t][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wb[u][s], wa[u][t], acc[t][s], 0, 0, 0);
+  }
+  for (; 64 * c < p.K; c += kSWaves) {
+    const int k = 64 * c + 16 * quad, valid = p.K - k;
+    const int at = valid > 0 ? k : 0;  // a piece past the row is read from its start and zeroed
+    i32x4 wb[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) wb[s] = load_k(brow[s], at);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const i32x4 wa = mask_k(load_k(arow[t], at), valid);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        acc[t][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wb[s], wa, acc[t][s], 0, 0, 0);
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) part[wave][t * 2 + s][lane] = acc[t][s];
+  __syncthreads();
+  for (int t = wave; t < MT; t += kSWaves) {
+    i32x4 sum[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      sum[s] = part[0][t * 2 + s][lane];
+#pragma unroll
+      for (int w = 1; w < kSWaves; ++w) sum[s] += part[w][t * 2 + s][lane];
+    }
+    // lane: row `col` of out, columns 4 * quad .. + 3 of each 16
+    const int m = r.lo + 16 * t + col;
+    if (m >= r.hi) continue;
+    const int src = source_row(p, m);
+    if (src < 0) continue;
+    const float sa = p.a_scale[src];
+    const float* sb = p.b_scale + (size_t)r.g * p.b_scale_group_stride;
+    float y[2][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 4 * quad + i + (GLU ? 0 : 16 * s);
+        const float sn = sb[min(n, p.N - 1) + (GLU && s ? p.N : 0)];
+        y[s][i] = (float)sum[s][i] * sa * sn;
+      }
+    const int n = n0 + 4 * quad;
+    if (GLU) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[0][i] = silu(y[0][i]) * y[1][i];
+      if (n < p.N) store_out(p, m, n, y[0]);
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (n + 16 * s < p.N) store_out(p, m, n + 16 * s, y[s]);
+    }
+  }
+}
+
+template <int MT, bool GLU>
+__global__ __launch_bounds__(kSWaves* kWave) void int8_stream(MatArgs p, int cols, int64_t tiles) {
+  __shared__ i32x4 part[kSWaves][MT * 2][kWave];
+  for (int64_t w = blockIdx.x; w < tiles; w += gridDim.x) {
+    Rows r;
+    if (!find_rows(p, (int)(w / cols), 16 * MT, r)) return;  // nor are there later ones
+    stream_tile<MT, GLU>(p, r, (int)(w % cols) * (GLU ? 16 : 32), part);
+    __syncthreads();  // the sums have been read
+  }
+}
+
+template <int MT>
+void launch_stream(const MatArgs& p, bool glu, hipStream_t stream) {
+  const int per = glu ? 16 : 32, cols = (p.N + per - 1) / per;
+  const int64_t tiles = max_items(p.M, p.G, 16 * MT) * cols;
+  const unsigned grid = (unsigned)(tiles < kMaxGrid ? tiles : kMaxGrid);
+  if (glu)
+    int8_stream<MT, true><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, tiles);
+  else
+    int8_stream<MT, false><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, tiles);
+}
+
+int matmul_status(const moe_int8_matmul_args* a) {
+  if (!a) return MOE_EINVAL;
+  if (a->M < 0 || a->N <= 0 || a->K <= 0 || a->G < 0 || a->a_rows < 0) return MOE_EINVAL;
+  if (dtype_bytes(a->out_dtype) == 0 || (a->swiglu != 0 && a->swiglu != 1)) return MOE_EINVAL;
+  if (a->K > kMaxK || a->G > MOE_MAX_S || a->N > (1 << 24)) return MOE_EUNSUPPORTED;
+  if (a->M == 0) return MOE_OK;
+  if (!a->a || !a->a_scale || !a->b || !a->b_scale || !a->out) return MOE_EINVAL;
+  if ((a->G > 0) != (a->offsets != nullptr)) return MOE_EINVAL;
+  if (a->index ? a->index_div < 1 : a->a_rows < a->M) return MOE_EINVAL;
+  if (a->a_rows == 0) return MOE_EINVAL;
+  const size_t row = (size_t)up16(a->K), wide = (size_t)a->N * (a->swiglu ? 2 : 1);
+  if (!aligned(a->a, 16) || !aligned(a->b, 16) || a->a_stride % 16 || a->b_stride % 16 ||
+      a->b_group_stride % 16)
+    return MOE_EINVAL;
+  if (!aligned(a->a_scale, 4) || !aligned(a->b_scale, 4) || !aligned(a->index, 4) ||
+      !aligned(a->offsets, 4) || !aligned(a->out, dtype_bytes(a->out_dtype)))
+    return MOE_EINVAL;
+  if (a->a_stride < row || a->b_stride < row || a->out_stride < (size_t)a->N) return MOE_EINVAL;
+  if (a->G > 1 && (a->b_group_stride < (wide - 1) * a->b_stride + row ||
+                   a->b_scale_group_stride < wide))
+    return MOE_EINVAL;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" MOE_EXPORT size_t moe_int8_row_bytes(int K) {
+  return K <= 0 || K > kMaxK ? 0 : (size_t)up16(K);
+}
+
+extern "C" MOE_EXPORT int moe_int8_quantize(const void* x, int M, int K, size_t x_stride, int dtype,
+                                            int8_t* q, size_t q_stride, float* scale,
+                                            hipStream_t stream) {
+  const size_t e = dtype_bytes(dtype);
+  if (M < 0 || K <= 0 || e == 0) return MOE_EINVAL;
+  if (K > kMaxK) return MOE_EUNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !q || !scale || !aligned(x, e) || !aligned(q, 16) || !aligned(scale, 4))
+    return MOE_EINVAL;
+  if (x_stride < (size_t)K || q_stride % 16 || q_stride < (size_t)up16(K)) return MOE_EINVAL;
+  const int pieces = (K * (int)e + 15) / 16;
+  const int lanes = pieces <= kWave * kQPieces ? kWave : kQThreads;
+  const int64_t want = ((int64_t)M * lanes + kQThreads - 1) / kQThreads;
+  const unsigned grid = (unsigned)(want < kMaxGrid ? want : kMaxGrid);
+  if (dtype == MOE_DT_BF16)
+    quantize_rows<Bf16><<<grid, kQThreads, 0, stream>>>((const Bf16*)x, M, K, x_stride, q, q_stride,
+                                                        scale, lanes);
+  else if (dtype == MOE_DT_FP16)
+    quantize_rows<Fp16><<<grid, kQThreads, 0, stream>>>((const Fp16*)x, M, K, x_stride, q, q_stride,
+                                                        scale, lanes);
+  else
+    quantize_rows<float><<<grid, kQThreads, 0, stream>>>((const float*)x, M, K, x_stride, q,
+                                                         q_stride, scale, lanes);
+  return hip_status();
+}
+
+extern "C" MOE_EXPORT int moe_int8_matmul(const moe_int8_matmul_args* a, hipStream_t stream) {
+  const int s = matmul_status(a);
+  if (s != MOE_OK || a->M == 0) return s;
+  MatArgs p{};
+  p.M = a->M, p.N = a->N, p.K = a->K, p.G = a->G;
+  p.a_rows = a->a_rows, p.index_div = a->index_div, p.out_dtype = a->out_dtype;
+  p.a = a->a, p.a_scale = a->a_scale, p.index = a->index, p.offsets = a->offsets;
+  p.b = a->b, p.b_scale = a->b_scale, p.out = a->out;
+  p.a_stride = a->a_stride, p.b_stride = a->b_stride, p.b_group_stride = a->b_group_stride;
+  p.b_scale_group_stride = a->b_scale_group_stride, p.out_stride = a->out_stride;
+  launch_stream<4>(p, a->swiglu, stream);
+  return hip_status();
+}

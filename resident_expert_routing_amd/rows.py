@@ -1,0 +1,175 @@
+"""Token rows in the order of the slots and back, as differentiable torch functions.
+
+    order = RowOrder(buf.perm, T, k)            # perm as moe_route wrote it
+    rows = dispatch(x, order)                   # [T*k, H], row p: token perm[p] // k
+    ... any experts, slot s on rows slot_offsets[s] .. slot_offsets[s+1] ...
+    out = combine(rows, order, buf.sel_weight)  # [T, H]
+
+Both take bf16, fp16 or fp32 rows and float32 weights, and pass gradients to the
+rows and to the weights (moe_dispatch_backward, moe_combine_backward).  They run
+on the current stream of the rows' device and synchronise nothing.  A gradient
+captured into a graph is taken with torch.autograd.grad, or with no graph made
+outside the capture alive over the same leaves: torch ties a leaf's accumulation
+to the stream that first used it.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import binding as B
+
+DTYPES = {torch.bfloat16: B.MOE_DT_BF16, torch.float16: B.MOE_DT_FP16,
+          torch.float32: B.MOE_DT_FP32}
+
+
+def on_device(t: torch.Tensor):
+    """A context in which the tensor's device is the current one."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def stream_of(t: torch.Tensor) -> int:
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def dtype_of(t: torch.Tensor, what: str) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be bfloat16, float16 or float32, not {t.dtype}")
+    return code
+
+
+def gpu_tensor(t, what: str, device=None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{what} must be a tensor on a GPU")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the rows on {device}")
+    return t
+
+
+def row_major(t: torch.Tensor) -> tuple[torch.Tensor, int]:
+    """(t, elements from row to row) of a matrix whose rows are contiguous and
+    apart; other layouts (transposed, expanded) are copied first."""
+    n, width = t.shape
+    if (width == 1 or t.stride(1) == 1) and (n <= 1 or t.stride(0) >= width):
+        return t, t.stride(0) if n > 1 else width
+    return t.contiguous(), width
+
+
+class RowOrder:
+    """The order of a batch's T*k assignments by slot: perm (row -> assignment,
+    int32, as moe_route wrote it, -1 behind the last row that is used) and its
+    inverse pos [T, k] (assignment -> row, -1 for none), which moe_positions
+    computes unless the caller already has it."""
+
+    def __init__(self, perm: torch.Tensor, T: int, k: int, pos: torch.Tensor | None = None):
+        self.T, self.k = int(T), int(k)
+        n = self.T * self.k
+        gpu_tensor(perm, "perm")
+        if perm.dtype != torch.int32 or perm.numel() != n:
+            raise ValueError(f"perm must hold T*k = {n} int32 values")
+        self.perm = perm.contiguous()
+        if pos is None:
+            pos = torch.empty((self.T, self.k), dtype=torch.int32, device=perm.device)
+            with on_device(perm):
+                B.check(B.moe_positions(self.perm, self.T, self.k, pos, stream_of(perm)),
+                        "moe_positions")
+        elif gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or pos.numel() != n:
+            raise ValueError(f"pos must hold T*k = {n} int32 values")
+        self.pos = pos.contiguous()
+
+
+def _weights(weight, order: RowOrder, device):
+    if weight is None:
+        return None
+    gpu_tensor(weight, "weight", device)
+    if weight.dtype != torch.float32 or weight.numel() != order.T * order.k:
+        raise ValueError(f"weight must hold [{order.T}, {order.k}] float32 values")
+    return weight.contiguous()
+
+
+def _check(src: torch.Tensor, n: int, order: RowOrder, what: str) -> None:
+    gpu_tensor(src, what, order.perm.device)
+    if src.dim() != 2 or src.shape[0] != n:
+        raise ValueError(f"{what} must have shape [{n}, H], not {list(src.shape)}")
+
+
+def _spread(src, order, weight, rows=None):
+    """Token rows to rows; with `rows` (the forward rows) the weights' gradient too."""
+    dt, (src, stride), H = dtype_of(src, "rows"), row_major(src), src.shape[1]
+    dst = torch.empty((order.T * order.k, H), dtype=src.dtype, device=src.device)
+    with on_device(src):
+        if rows is None:
+            B.check(B.moe_dispatch(order.T, H, order.k, dt, order.pos, src, stride, dst, H, weight,
+                                   order.perm, stream_of(src)), "moe_dispatch")
+            return dst, None
+        rows, rstride = row_major(rows)
+        dw = torch.empty((order.T, order.k), dtype=torch.float32, device=src.device)
+        B.check(B.moe_combine_backward(order.T, H, order.k, dt, order.pos, src, stride, dst, H,
+                                       weight, order.perm, rows, rstride, dw, stream_of(src)),
+                "moe_combine_backward")
+        return dst, dw
+
+
+def _gather(src, order, weight, tokens=None):
+    """Rows to token rows; with `tokens` (the forward token rows) the weights' gradient too."""
+    dt, (src, stride), H = dtype_of(src, "rows"), row_major(src), src.shape[1]
+    dst = torch.empty((order.T, H), dtype=src.dtype, device=src.device)
+    with on_device(src):
+        if tokens is None:
+            B.check(B.moe_combine(order.T, H, order.k, dt, order.pos, src, stride, dst, H, weight,
+                                  stream_of(src)), "moe_combine")
+            return dst, None
+        tokens, tstride = row_major(tokens)
+        dw = torch.empty((order.T, order.k), dtype=torch.float32, device=src.device)
+        B.check(B.moe_dispatch_backward(order.T, H, order.k, dt, order.pos, src, stride, dst, H,
+                                        weight, tokens, tstride, dw, stream_of(src)),
+                "moe_dispatch_backward")
+        return dst, dw
+
+
+class _Move(torch.autograd.Function):
+    """forward: `there`; backward: `back`, the other of _spread and _gather."""
+
+    @staticmethod
+    def forward(ctx, src, weight, order, there, back):
+        w = _weights(weight, order, src.device)
+        ctx.order, ctx.back = order, back
+        keep = src if weight is not None and ctx.needs_input_grad[1] else None
+        ctx.save_for_backward(keep, w)
+        ctx.wshape = None if weight is None else weight.shape
+        return there(src, order, w)[0]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        src, w = ctx.saved_tensors
+        dsrc, dw = ctx.back(grad, ctx.order, w, src)
+        return (dsrc if ctx.needs_input_grad[0] else None,
+                dw.view(ctx.wshape) if dw is not None else None, None, None, None)
+
+
+def _move(src, weight, order, there, back):
+    if torch.is_grad_enabled() and (src.requires_grad
+                                    or (weight is not None and weight.requires_grad)):
+        return _Move.apply(src, weight, order, there, back)
+    return there(src, order, _weights(weight, order, src.device))[0]
+
+
+def dispatch(x: torch.Tensor, order: RowOrder, weight: torch.Tensor | None = None) -> torch.Tensor:
+    """x [T, H] -> rows [T*k, H]: row p is x[perm[p] // k], times its weight if
+    `weight` [T, k] is given; rows that perm does not use are zero."""
+    _check(x, order.T, order, "x")
+    return _move(x, weight, order, _spread, _gather)
+
+
+def combine(rows: torch.Tensor, order: RowOrder,
+            weight: torch.Tensor | None = None) -> torch.Tensor:
+    """rows [T*k, H] -> out [T, H]: each token's rows, weighted and summed in
+    float32 over ascending picks; a token without rows gets zeros."""
+    _check(rows, order.T * order.k, order, "rows")
+    return _move(rows, weight, order, _gather, _spread)
