@@ -356,6 +356,193 @@ void launch_stream(const MatArgs& p, bool glu, hipStream_t stream) {
     int8_stream<MT, false><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, tiles);
 }
 
+// Tiled form, for groups of more rows: a workgroup of kTWaves waves takes 16 * MF
+// rows of one group and 64 rows of b for each wave (with SwiGLU, 32 gate rows
+// and their 32 up rows).  The rows of a, which every wave needs, go through LDS
+// (direct loads, two buffers of 128 bytes of K); those of b, which only one wave
+// needs, go straight to its registers, one step ahead.
+constexpr int kTWaves = 4;
+constexpr int kStep = 128;  // bytes of K a step
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const int8_t* p) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7FFFFFFF, 0x00020000);
+}
+
+template <typename E, int MF, bool GLU>
+__device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, uint8_t* smem) {
+  constexpr int kLoads = MF * 2 / kTWaves;   // direct loads of a wave in a step, 8 rows each
+  constexpr int kBuf = MF * 16 * kStep;      // bytes of an LDS buffer
+  constexpr int kOut = GLU ? 8 : 16;         // consecutive columns of out that a lane ends with
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, quad = lane >> 4;
+  const int nw = n0 + wave * kOut * 4;
+
+  // Weight rows: fragment s gives lane's quad q the columns kOut * q + 4 * s + i,
+  // so that its results are kOut consecutive columns of out.  They are read
+  // through buffers that start at the wave's first row, with 32-bit offsets;
+  // an offset past the buffer's end reads zeros, which serves the pieces
+  // behind a row.
+  const int first = min(nw, p.N - 1), top = p.N - 1 - first;
+  const int8_t* b = p.b + (size_t)r.g * p.b_group_stride + (size_t)first * p.b_stride;
+  const __amdgpu_buffer_rsrc_t bbuf[2] = {
+      row_buffer(b), row_buffer(GLU ? b + (size_t)p.N * p.b_stride : b)};
+  uint32_t boff[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    boff[s] = (uint32_t)min(kOut * (col >> 2) + 4 * (GLU ? s & 1 : s) + (col & 3), top) *
+                  (uint32_t)p.b_stride + 16 * quad;
+  // Rows of a: LDS place (row, c) of 16 bytes holds piece c ^ (row & 7) of the
+  // row's 128 bytes, so that the 16 rows of a fragment spread over the banks.
+  const int piece = 16 * ((lane & 7) ^ (lane >> 3));
+  const int8_t* arow[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int m = r.lo + (wave * kLoads + j) * 8 + (lane >> 3);
+    arow[j] = p.a + (size_t)max(source_row(p, min(m, r.hi - 1)), 0) * p.a_stride;
+  }
+  const int steps = (p.K + kStep - 1) / kStep;
+  const int width = up16(p.K);
+
+  auto load_a = [&](int step, int buf) {
+    int k = step * kStep + piece;
+    k = k < width ? k : 0;  // past the row: any of its bytes, b is zero there
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      dma16((const uint8_t*)arow[j] + k, smem + buf * kBuf + (wave * kLoads + j) * 1024);
+  };
+  auto load_b = [&](int step, i32x4 (&v)[2][4]) {
+    const int k0 = step * kStep;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const bool in = k0 + 64 * c + 16 * quad < p.K;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        v[c][s] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                bbuf[s >> 1], in ? boff[s] + 64 * c : ~0u, k0, 0));
+    }
+  };
+
+  i32x4 acc[MF][4] = {};
+  auto compute = [&](int buf, const i32x4 (&v)[2][4]) {
+    const uint8_t* at = smem + buf * kBuf + col * kStep;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int slot = 16 * ((4 * c + quad) ^ (col & 7));
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        const i32x4 w = *(const i32x4*)(at + f * 16 * kStep + slot);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          acc[f][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[c][s], w, acc[f][s], 0, 0, 0);
+      }
+    }
+  };
+
+  // Each step loads the next one's operands before its own products.  The last
+  // step stands apart: a piece that the end of the row cuts is masked there.
+  auto last = [&](int buf, i32x4 (&v)[2][4]) {
+    if (p.K % 16 != 0) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          v[c][s] = mask_k(v[c][s], p.K - ((steps - 1) * kStep + 64 * c + 16 * quad));
+    }
+    compute(buf, v);
+  };
+  i32x4 b0[2][4], b1[2][4];
+  load_a(0, 0);
+  load_b(0, b0);
+  wait_loads();
+  barrier();
+  int i = 0;
+  for (; i + 2 < steps; i += 2) {
+    load_a(i + 1, 1);
+    load_b(i + 1, b1);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(0, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads();
+    barrier();
+    load_a(i + 2, 0);
+    load_b(i + 2, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(1, b1);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads();
+    barrier();
+  }
+  if (i + 1 < steps) {
+    load_a(i + 1, 1);
+    load_b(i + 1, b1);
+    compute(0, b0);
+    wait_loads();
+    barrier();
+    last(1, b1);
+  } else {
+    last(0, b0);
+  }
+
+  const float* sb = p.b_scale + (size_t)r.g * p.b_scale_group_stride;
+  const int n = nw + kOut * quad;
+  float sn[4][4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sn[s][i] = sb[min(n + 4 * (GLU ? s & 1 : s) + i, p.N - 1) + (GLU && s >= 2 ? p.N : 0)];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const int m = r.lo + 16 * f + col;
+    if (m >= r.hi) continue;
+    const int src = source_row(p, m);
+    if (src < 0 || n >= p.N) continue;
+    const float sa = p.a_scale[src];
+    Piece<E, kOut> o;
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      float y = (float)acc[f][j / 4][j % 4] * sa * sn[j / 4][j % 4];
+      if (GLU) y = silu(y) * ((float)acc[f][2 + j / 4][j % 4] * sa * sn[2 + j / 4][j % 4]);
+      o.e[j] = from_f32<E>(y);
+    }
+    o.store_upto((E*)p.out + (size_t)m * p.out_stride + n, p.N - n);
+  }
+}
+
+template <typename E, bool GLU>
+__global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int cols, int64_t first) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * 128 * kStep];
+  const int64_t w = first + blockIdx.x;
+  Rows r;
+  if (!find_rows(p, (int)(w / cols), 128, r)) return;
+  const int n0 = (int)(w % cols) * (GLU ? 128 : 256);
+  if (r.hi - r.lo <= 64)
+    tile<E, 4, GLU>(p, r, n0, smem);
+  else
+    tile<E, 8, GLU>(p, r, n0, smem);
+}
+
+template <typename E>
+void launch_tiles(const MatArgs& p, bool glu, hipStream_t stream) {
+  const int per = glu ? 128 : 256, cols = (p.N + per - 1) / per;
+  const int64_t tiles = max_items(p.M, p.G, 128) * cols;
+  for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+    const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
+    if (glu)
+      int8_tiles<E, true><<<grid, kTWaves * kWave, 0, stream>>>(p, cols, first);
+    else
+      int8_tiles<E, false><<<grid, kTWaves * kWave, 0, stream>>>(p, cols, first);
+  }
+}
+
 int matmul_status(const moe_int8_matmul_args* a) {
   if (!a) return MOE_EINVAL;
   if (a->M < 0 || a->N <= 0 || a->K <= 0 || a->G < 0 || a->a_rows < 0) return MOE_EINVAL;
@@ -422,6 +609,13 @@ extern "C" MOE_EXPORT int moe_int8_matmul(const moe_int8_matmul_args* a, hipStre
   p.b = a->b, p.b_scale = a->b_scale, p.out = a->out;
   p.a_stride = a->a_stride, p.b_stride = a->b_stride, p.b_group_stride = a->b_group_stride;
   p.b_scale_group_stride = a->b_scale_group_stride, p.out_stride = a->out_stride;
-  launch_stream<4>(p, a->swiglu, stream);
+  if (p.M <= 64 * (p.G > 0 ? p.G : 1))
+    launch_stream<4>(p, a->swiglu, stream);
+  else if (p.out_dtype == MOE_DT_BF16)
+    launch_tiles<Bf16>(p, a->swiglu, stream);
+  else if (p.out_dtype == MOE_DT_FP16)
+    launch_tiles<Fp16>(p, a->swiglu, stream);
+  else
+    launch_tiles<float>(p, a->swiglu, stream);
   return hip_status();
 }
