@@ -7,6 +7,8 @@
 // The sums are exact 32-bit integers on the matrix cores, so neither the order
 // of the contraction nor how it is split over waves changes a result; the two
 // scales are applied to the finished sum in float32.
+#include <type_traits>
+
 #include "elements.hpp"
 
 using namespace moe;
@@ -16,7 +18,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126, the smallest normal float
-constexpr int kMaxGrid = 1 << 22;             // workgroups of a launch; they stride over the rest
+constexpr int kMaxGrid = 1 << 22;             // workgroups of a launch
 constexpr int kMaxK = 131056;                 // 128 * 128 * K stays below 2^31
 
 __host__ __device__ inline int up16(int v) { return (v + 15) & ~15; }
@@ -136,50 +138,58 @@ struct Rows {
 
 __device__ __forceinline__ int clamp_row(int v, int M) { return min(max(v, 0), M); }
 
-// The item-th piece of at most R rows, counted through the groups in order;
-// false past the last.  Every wave finds it by itself: each lane counts the
-// pieces of its share of the groups, a scan over the lanes gives the lane that
-// holds the piece, and that lane its group.  Offsets outside [0, M] are cut.
-__device__ __forceinline__ bool find_rows(const MatArgs& p, int item, int R, Rows& r) {
-  if (!p.offsets) {
-    r.g = 0, r.lo = item * R, r.hi = min(p.M, r.lo + R);
-    return r.lo < p.M;
-  }
-  const int lane = threadIdx.x & 63;
-  const int share = (p.G + 63) / 64;
-  const int g0 = min(lane * share, p.G), g1 = min(g0 + share, p.G);
-  auto pieces = [&](int g) {
-    const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
-    return hi > lo ? (hi - lo) / R + ((hi - lo) % R != 0) : 0;
-  };
-  // Sums stop at a bound above every item, so that offsets which are no
-  // bucketing cannot overflow them.
+// The pieces of at most R rows that the groups make, counted through the groups
+// in order.  Every wave does it by itself: each lane counts the pieces of its
+// share of the groups, and a scan over the lanes gives the sums.  Offsets
+// outside [0, M] are cut, and sums stop at a bound above every count, so that
+// offsets which are no bucketing cannot overflow them.
+struct Pieces {
+  int sum;    // pieces of this lane's groups and the lanes' before it
+  int total;  // of all groups
+};
+
+__device__ __forceinline__ int pieces_of(const MatArgs& p, int g, int R) {
+  const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+  return hi > lo ? (hi - lo) / R + ((hi - lo) % R != 0) : 0;
+}
+
+__device__ __forceinline__ int first_group(const MatArgs& p, int lane) {
+  return min(lane * ((p.G + 63) / 64), p.G);
+}
+
+__device__ __forceinline__ Pieces count_pieces(const MatArgs& p, int R) {
+  if (!p.offsets) return {0, p.M / R + (p.M % R != 0)};
   constexpr int kMost = 1 << 29;
+  const int lane = threadIdx.x & 63;
   int sum = 0;
-  for (int g = g0; g < g1; ++g) sum = min(sum + pieces(g), kMost);
+  for (int g = first_group(p, lane); g < first_group(p, lane + 1); ++g)
+    sum = min(sum + pieces_of(p, g, R), kMost);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int o = __shfl_up(sum, d, 64);
     if (lane >= d) sum = min(sum + o, kMost);
   }
-  const unsigned long long past = __ballot(sum > item);
-  if (past == 0) return false;
-  const int owner = __ffsll((long long)past) - 1;
-  int g = g0, before = __shfl_up(sum, 1, 64);
+  return {sum, __builtin_amdgcn_readlane(sum, 63)};
+}
+
+// The item-th piece, item < c.total: the first lane whose sum passes it holds
+// its group.
+__device__ __forceinline__ Rows find_rows(const MatArgs& p, const Pieces& c, int item, int R) {
+  if (!p.offsets) return {0, item * R, min(p.M, item * R + R)};
+  const int lane = threadIdx.x & 63;
+  const int owner = __ffsll((long long)__ballot(c.sum > item)) - 1;
+  int g = first_group(p, lane), before = __shfl_up(c.sum, 1, 64);
   if (lane == 0) before = 0;
   if (lane == owner)
-    for (; g < g1 - 1; ++g) {
-      const int n = pieces(g);
+    for (; g < first_group(p, lane + 1) - 1; ++g) {
+      const int n = pieces_of(p, g, R);
       if (before + n > item) break;
       before += n;
     }
   g = __builtin_amdgcn_readfirstlane(__shfl(g, owner, 64));
   before = __builtin_amdgcn_readfirstlane(__shfl(before, owner, 64));
-  const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
-  r.g = g;
-  r.lo = lo + (item - before) * R;
-  r.hi = min(hi, r.lo + R);
-  return r.lo < r.hi;
+  const int lo = clamp_row(p.offsets[g], p.M) + (item - before) * R;
+  return {g, lo, min(clamp_row(p.offsets[g + 1], p.M), lo + R)};
 }
 
 // Most pieces of R rows that M rows in G groups can make.
@@ -335,173 +345,164 @@ __device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int
 }
 
 template <int MT, bool GLU>
-__global__ __launch_bounds__(kSWaves* kWave) void int8_stream(MatArgs p, int cols, int64_t tiles) {
+__global__ __launch_bounds__(kSWaves* kWave) void int8_stream(MatArgs p, int cols, int64_t first) {
   __shared__ i32x4 part[kSWaves][MT * 2][kWave];
-  for (int64_t w = blockIdx.x; w < tiles; w += gridDim.x) {
-    Rows r;
-    if (!find_rows(p, (int)(w / cols), 16 * MT, r)) return;  // nor are there later ones
-    stream_tile<MT, GLU>(p, r, (int)(w % cols) * (GLU ? 16 : 32), part);
-    __syncthreads();  // the sums have been read
-  }
+  const Pieces c = count_pieces(p, 16 * MT);
+  const int64_t w = first + blockIdx.x;
+  if (w / cols >= c.total) return;
+  const Rows r = find_rows(p, c, (int)(w / cols), 16 * MT);
+  stream_tile<MT, GLU>(p, r, (int)(w % cols) * (GLU ? 16 : 32), part);
 }
 
 template <int MT>
 void launch_stream(const MatArgs& p, bool glu, hipStream_t stream) {
   const int per = glu ? 16 : 32, cols = (p.N + per - 1) / per;
   const int64_t tiles = max_items(p.M, p.G, 16 * MT) * cols;
-  const unsigned grid = (unsigned)(tiles < kMaxGrid ? tiles : kMaxGrid);
-  if (glu)
-    int8_stream<MT, true><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, tiles);
-  else
-    int8_stream<MT, false><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, tiles);
+  for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+    const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
+    if (glu)
+      int8_stream<MT, true><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, first);
+    else
+      int8_stream<MT, false><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, first);
+  }
 }
 
-// Tiled form, for groups of more rows: a workgroup of kTWaves waves takes 16 * MF
-// rows of one group and 64 rows of b for each wave (with SwiGLU, 32 gate rows
-// and their 32 up rows).  The rows of a, which every wave needs, go through LDS
-// (direct loads, two buffers of 128 bytes of K); those of b, which only one wave
-// needs, go straight to its registers, one step ahead.
-constexpr int kTWaves = 4;
-constexpr int kStep = 128;  // bytes of K a step
+// Tiled form, for groups of more rows: a workgroup of eight waves, two by four,
+// takes 32 * MF rows of one group and 256 rows of b (with SwiGLU, 128 gate rows
+// and their 128 up rows); a wave has 16 * MF rows by 64.  Both operands go
+// through LDS by direct loads, in a ring of S stages of 128 bytes of K: whole
+// cache lines of a row, which the memory path takes fastest.
+constexpr int kTWaves = 8;
+constexpr int kStep = 128;  // bytes of K a stage
+constexpr int kColRows = 256;
 
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __align__(16) const uint8_t kZeros[16] = {};  // source of what lies behind a row
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const int8_t* p) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7FFFFFFF, 0x00020000);
-}
-
-template <typename E, int MF, bool GLU>
+template <typename E, int MF, int S, bool GLU>
 __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, uint8_t* smem) {
-  constexpr int kLoads = MF * 2 / kTWaves;   // direct loads of a wave in a step, 8 rows each
-  constexpr int kBuf = MF * 16 * kStep;      // bytes of an LDS buffer
-  constexpr int kOut = GLU ? 8 : 16;         // consecutive columns of out that a lane ends with
+  constexpr int kRows = 32 * MF;
+  constexpr int kStage = (kRows + kColRows) * kStep;  // bytes of a stage, rows of a first
+  constexpr int kLoadsA = kRows / 8 / kTWaves;        // direct loads of a wave, 8 rows each
+  constexpr int kLoadsB = kColRows / 8 / kTWaves;
+  constexpr int kLoads = kLoadsA + kLoadsB;
+  constexpr int kOut = GLU ? 8 : 16;                  // consecutive columns a lane ends with
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, quad = lane >> 4;
-  const int nw = n0 + wave * kOut * 4;
+  const int wm = wave >> 2, wn = wave & 3;
 
-  // Weight rows: fragment s gives lane's quad q the columns kOut * q + 4 * s + i,
-  // so that its results are kOut consecutive columns of out.  They are read
-  // through buffers that start at the wave's first row, with 32-bit offsets;
-  // an offset past the buffer's end reads zeros, which serves the pieces
-  // behind a row.
-  const int first = min(nw, p.N - 1), top = p.N - 1 - first;
-  const int8_t* b = p.b + (size_t)r.g * p.b_group_stride + (size_t)first * p.b_stride;
-  const __amdgpu_buffer_rsrc_t bbuf[2] = {
-      row_buffer(b), row_buffer(GLU ? b + (size_t)p.N * p.b_stride : b)};
-  uint32_t boff[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-    boff[s] = (uint32_t)min(kOut * (col >> 2) + 4 * (GLU ? s & 1 : s) + (col & 3), top) *
-                  (uint32_t)p.b_stride + 16 * quad;
-  // Rows of a: LDS place (row, c) of 16 bytes holds piece c ^ (row & 7) of the
-  // row's 128 bytes, so that the 16 rows of a fragment spread over the banks.
+  // Direct loads: a lane loads 16 bytes of row lane / 8 of its instruction's
+  // eight.  LDS place (row, c) holds piece c ^ (row & 7) of the row's 128 bytes,
+  // so that the 16 rows of a fragment spread over the banks.
   const int piece = 16 * ((lane & 7) ^ (lane >> 3));
-  const int8_t* arow[kLoads];
+  const int8_t* arow[kLoadsA];
 #pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int m = r.lo + (wave * kLoads + j) * 8 + (lane >> 3);
-    arow[j] = p.a + (size_t)max(source_row(p, min(m, r.hi - 1)), 0) * p.a_stride;
+  for (int j = 0; j < kLoadsA; ++j) {
+    const int m = r.lo + (wave * kLoadsA + j) * 8 + (lane >> 3);
+    arow[j] = p.a + (size_t)max(source_row(p, min(m, r.hi - 1)), 0) * p.a_stride + piece;
+  }
+  // LDS row 64 w + 16 s + x of b is row x of fragment s of the waves wn = w: the
+  // weight row that gives lane quad q of the result the columns kOut * q + 4 * s
+  // + i, so that a lane ends with kOut consecutive columns of out.
+  const int8_t* brow[kLoadsB];
+#pragma unroll
+  for (int j = 0; j < kLoadsB; ++j) {
+    const int l = (wave * kLoadsB + j) * 8 + (lane >> 3);
+    const int s = (l >> 4) & 3, x = l & 15;
+    const int n = n0 + (l >> 6) * 4 * kOut + kOut * (x >> 2) + 4 * (GLU ? s & 1 : s) + (x & 3);
+    brow[j] = p.b + (size_t)r.g * p.b_group_stride +
+              (size_t)(min(n, p.N - 1) + (GLU && s >= 2 ? p.N : 0)) * p.b_stride + piece;
   }
   const int steps = (p.K + kStep - 1) / kStep;
   const int width = up16(p.K);
 
-  auto load_a = [&](int step, int buf) {
-    int k = step * kStep + piece;
-    k = k < width ? k : 0;  // past the row: any of its bytes, b is zero there
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-      dma16((const uint8_t*)arow[j] + k, smem + buf * kBuf + (wave * kLoads + j) * 1024);
+  // Load j of stage i's kLoads.  Behind a row, b's pieces are zero, and a's any
+  // bytes of the row.
+  auto load = [&](int i, int j) {
+    uint8_t* base = smem + (i % S) * kStage;
+    const int k = i * kStep;
+    const bool in = k + piece < width;
+    if (j < kLoadsB)
+      dma16(in ? (const uint8_t*)brow[j] + k : kZeros,
+            base + kRows * kStep + (wave * kLoadsB + j) * 1024);
+    else
+      dma16((const uint8_t*)arow[j - kLoadsB] + (in ? k : -piece),
+            base + (wave * kLoadsA + j - kLoadsB) * 1024);
   };
-  auto load_b = [&](int step, i32x4 (&v)[2][4]) {
-    const int k0 = step * kStep;
+
+  // One stage: 2 * MF groups of four products, a group for each 64 bytes of 16
+  // rows of a.  Fragments are read two groups ahead (b's a half stage ahead), and
+  // the loads of stage i + S - 1 are issued one for each group.
+  i32x4 acc[MF][4] = {};
+  auto stage = [&](int i, auto more, auto cut) {
+    const uint8_t* sa = smem + (i % S) * kStage + (wm * MF * 16 + col) * kStep;
+    const uint8_t* sb = smem + (i % S) * kStage + (kRows + wn * 64 + col) * kStep;
+    const int slot[2] = {16 * (quad ^ (col & 7)), 16 * ((4 + quad) ^ (col & 7))};
+    auto frag = [&](int x) { return *(const i32x4*)(sa + (x % MF) * 16 * kStep + slot[x / MF]); };
+    auto weight = [&](int c, int s) {
+      i32x4 v = *(const i32x4*)(sb + s * 16 * kStep + slot[c]);
+      if (decltype(cut)::value) v = mask_k(v, p.K - (i * kStep + 64 * c + 16 * quad));
+      return v;
+    };
+    i32x4 w[3], v[2][4];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const bool in = k0 + 64 * c + 16 * quad < p.K;
+    for (int s = 0; s < 4; ++s) v[0][s] = weight(0, s);
+    w[0] = frag(0);
+    w[1] = frag(1);
+#pragma unroll
+    for (int x = 0; x < 2 * MF; ++x) {
+      if (x + 2 < 2 * MF) w[(x + 2) % 3] = frag(x + 2);
+      if (x < 4) v[1][x] = weight(1, x);
+      if (decltype(more)::value && x < kLoads) load(i + S - 1, x);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        v[c][s] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                bbuf[s >> 1], in ? boff[s] + 64 * c : ~0u, k0, 0));
+        acc[x % MF][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[x / MF][s], w[x % 3],
+                                                               acc[x % MF][s], 0, 0, 0);
     }
   };
 
-  i32x4 acc[MF][4] = {};
-  auto compute = [&](int buf, const i32x4 (&v)[2][4]) {
-    const uint8_t* at = smem + buf * kBuf + col * kStep;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int slot = 16 * ((4 * c + quad) ^ (col & 7));
-#pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        const i32x4 w = *(const i32x4*)(at + f * 16 * kStep + slot);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          acc[f][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[c][s], w, acc[f][s], 0, 0, 0);
-      }
-    }
-  };
-
-  // Each step loads the next one's operands before its own products.  The last
-  // step stands apart: a piece that the end of the row cuts is masked there.
-  auto last = [&](int buf, i32x4 (&v)[2][4]) {
-    if (p.K % 16 != 0) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          v[c][s] = mask_k(v[c][s], p.K - ((steps - 1) * kStep + 64 * c + 16 * quad));
-    }
-    compute(buf, v);
-  };
-  i32x4 b0[2][4], b1[2][4];
-  load_a(0, 0);
-  load_b(0, b0);
-  wait_loads();
-  barrier();
+  for (int i = 0; i < S - 1; ++i)
+    if (i < steps)
+      for (int j = 0; j < kLoads; ++j) load(i, j);
+  // At the top of stage i its loads, issued S - 1 stages ago, have to have
+  // landed (those of the S - 2 stages after it may still be in flight), and
+  // every wave has to be done with the stage before, whose place is loaded next.
   int i = 0;
-  for (; i + 2 < steps; i += 2) {
-    load_a(i + 1, 1);
-    load_b(i + 1, b1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(0, b0);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_loads();
+  for (; i + S - 1 < steps; ++i) {
+    wait_loads<(S - 2) * kLoads>();
     barrier();
-    load_a(i + 2, 0);
-    load_b(i + 2, b0);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(1, b1);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_loads();
-    barrier();
+    stage(i, std::true_type{}, std::false_type{});
   }
-  if (i + 1 < steps) {
-    load_a(i + 1, 1);
-    load_b(i + 1, b1);
-    compute(0, b0);
-    wait_loads();
-    barrier();
-    last(1, b1);
-  } else {
-    last(0, b0);
-  }
+  wait_loads<0>();
+  barrier();
+  for (; i + 1 < steps; ++i) stage(i, std::false_type{}, std::false_type{});
+  if (p.K % 16 != 0)  // a piece that the row's end cuts is masked
+    stage(i, std::false_type{}, std::true_type{});
+  else
+    stage(i, std::false_type{}, std::false_type{});
 
-  const float* sb = p.b_scale + (size_t)r.g * p.b_scale_group_stride;
-  const int n = nw + kOut * quad;
+  const float* scale = p.b_scale + (size_t)r.g * p.b_scale_group_stride;
+  const int n = n0 + wn * 4 * kOut + kOut * quad;
   float sn[4][4];
 #pragma unroll
   for (int s = 0; s < 4; ++s)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sn[s][i] = sb[min(n + 4 * (GLU ? s & 1 : s) + i, p.N - 1) + (GLU && s >= 2 ? p.N : 0)];
+    for (int e = 0; e < 4; ++e)
+      sn[s][e] = scale[min(n + 4 * (GLU ? s & 1 : s) + e, p.N - 1) + (GLU && s >= 2 ? p.N : 0)];
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    const int m = r.lo + 16 * f + col;
+    const int m = r.lo + (wm * MF + f) * 16 + col;
     if (m >= r.hi) continue;
     const int src = source_row(p, m);
     if (src < 0 || n >= p.N) continue;
@@ -519,21 +520,22 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
 
 template <typename E, bool GLU>
 __global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int cols, int64_t first) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * 128 * kStep];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * (128 + kColRows) * kStep];
+  const Pieces c = count_pieces(p, 256);
   const int64_t w = first + blockIdx.x;
-  Rows r;
-  if (!find_rows(p, (int)(w / cols), 128, r)) return;
-  const int n0 = (int)(w % cols) * (GLU ? 128 : 256);
-  if (r.hi - r.lo <= 64)
-    tile<E, 4, GLU>(p, r, n0, smem);
+  if (w / cols >= c.total) return;
+  const Rows r = find_rows(p, c, (int)(w / cols), 256);
+  const int n0 = (int)(w % cols) * (GLU ? kColRows / 2 : kColRows);
+  if (r.hi - r.lo <= 128)
+    tile<E, 4, 3, GLU>(p, r, n0, smem);
   else
-    tile<E, 8, GLU>(p, r, n0, smem);
+    tile<E, 8, 2, GLU>(p, r, n0, smem);
 }
 
 template <typename E>
 void launch_tiles(const MatArgs& p, bool glu, hipStream_t stream) {
-  const int per = glu ? 128 : 256, cols = (p.N + per - 1) / per;
-  const int64_t tiles = max_items(p.M, p.G, 128) * cols;
+  const int per = glu ? kColRows / 2 : kColRows, cols = (p.N + per - 1) / per;
+  const int64_t tiles = max_items(p.M, p.G, 256) * cols;
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (glu)
