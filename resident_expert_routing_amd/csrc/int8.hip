@@ -382,14 +382,25 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+// The wave's own LDS reads and writes are done when it arrives.
 __device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
+// What the epilogue needs of a tile's rows and columns, loaded beside the first
+// stage.
+struct Side {
+  float row[256], col[256];
+  int live[256];  // rows of out that are written
+};
+
+constexpr int kOutBytes = 16384;  // LDS that a wave's results pass through
+
 template <typename E, int MF, int S, bool GLU>
-__device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, uint8_t* smem) {
+__device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, uint8_t* smem,
+                                     Side& side) {
   constexpr int kRows = 32 * MF;
   constexpr int kStage = (kRows + kColRows) * kStep;  // bytes of a stage, rows of a first
   constexpr int kLoadsA = kRows / 8 / kTWaves;        // direct loads of a wave, 8 rows each
@@ -475,6 +486,18 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   for (int i = 0; i < S - 1; ++i)
     if (i < steps)
       for (int j = 0; j < kLoads; ++j) load(i, j);
+  {
+    const int t = threadIdx.x & 255;
+    if (threadIdx.x < 256) {
+      const int src = r.lo + t < r.hi ? source_row(p, r.lo + t) : -1;
+      side.live[t] = src >= 0;
+      side.row[t] = src >= 0 ? p.a_scale[src] : 0.0f;
+    } else {
+      const int n = n0 + (GLU ? t & 127 : t);
+      side.col[t] = p.b_scale[(size_t)r.g * p.b_scale_group_stride + min(n, p.N - 1) +
+                              (GLU && t >= 128 ? p.N : 0)];
+    }
+  }
   // At the top of stage i its loads, issued S - 1 stages ago, have to have
   // landed (those of the S - 2 stages after it may still be in flight), and
   // every wave has to be done with the stage before, whose place is loaded next.
@@ -492,44 +515,66 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   else
     stage(i, std::false_type{}, std::false_type{});
 
-  const float* scale = p.b_scale + (size_t)r.g * p.b_scale_group_stride;
-  const int n = n0 + wn * 4 * kOut + kOut * quad;
+  // Results leave through LDS, each wave through a part of its own, so that
+  // eight lanes store 128 consecutive bytes of a row of out.  16 bytes c of row
+  // x lie at c ^ (x & 7) of each 128, for the banks.
+  constexpr int kRowBytes = 4 * kOut * (int)sizeof(E);    // a wave's part of a row of out
+  constexpr int kPartRows = kOutBytes / kRowBytes;        // rows that pass at a time
+  constexpr int kPart = MF * 16 < kPartRows ? MF : kPartRows / 16;  // fragments of them
+  constexpr int kPieces = kRowBytes / 16;
   float sn[4][4];
 #pragma unroll
   for (int s = 0; s < 4; ++s)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      sn[s][e] = scale[min(n + 4 * (GLU ? s & 1 : s) + e, p.N - 1) + (GLU && s >= 2 ? p.N : 0)];
+      sn[s][e] = side.col[(GLU && s >= 2 ? 128 : 0) + (wn * 4 + quad) * kOut +
+                          4 * (GLU ? s & 1 : s) + e];
+  barrier();  // every wave has read the last stage
+  uint8_t* mine = smem + wave * kOutBytes;
+  auto place = [&](int x, int c) { return mine + x * kRowBytes + 16 * (c ^ (x & (kPieces - 1) & 7)); };
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    const int m = r.lo + (wm * MF + f) * 16 + col;
-    if (m >= r.hi) continue;
-    const int src = source_row(p, m);
-    if (src < 0 || n >= p.N) continue;
-    const float sa = p.a_scale[src];
-    Piece<E, kOut> o;
+  for (int f0 = 0; f0 < MF; f0 += kPart) {
 #pragma unroll
-    for (int j = 0; j < kOut; ++j) {
-      float y = (float)acc[f][j / 4][j % 4] * sa * sn[j / 4][j % 4];
-      if (GLU) y = silu(y) * ((float)acc[f][2 + j / 4][j % 4] * sa * sn[2 + j / 4][j % 4]);
-      o.e[j] = from_f32<E>(y);
+    for (int f = f0; f < f0 + kPart; ++f) {
+      const float sa = side.row[(wm * MF + f) * 16 + col];
+      Piece<E, kOut> o;
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        float y = (float)acc[f][j / 4][j % 4] * sa * sn[j / 4][j % 4];
+        if (GLU) y = silu(y) * ((float)acc[f][2 + j / 4][j % 4] * sa * sn[2 + j / 4][j % 4]);
+        o.e[j] = from_f32<E>(y);
+      }
+      constexpr int kMine = kOut * (int)sizeof(E) / 16;
+#pragma unroll
+      for (int c = 0; c < kMine; ++c)
+        __builtin_memcpy(place((f - f0) * 16 + col, quad * kMine + c), (const char*)o.e + 16 * c, 16);
     }
-    o.store_upto((E*)p.out + (size_t)m * p.out_stride + n, p.N - n);
+    constexpr int kPer = 64 / kPieces;  // rows of a store instruction
+#pragma unroll
+    for (int x0 = 0; x0 < kPart * 16; x0 += kPer) {
+      const int x = x0 + lane / kPieces, c = lane % kPieces;
+      Piece<E> o;
+      __builtin_memcpy(o.e, place(x, c), 16);
+      const int row = (wm * MF + f0) * 16 + x, n = n0 + wn * 4 * kOut + c * Piece<E>::kN;
+      if (side.live[row] && n < p.N)
+        o.store_upto((E*)p.out + (size_t)(r.lo + row) * p.out_stride + n, p.N - n);
+    }
   }
 }
 
 template <typename E, bool GLU>
 __global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int cols, int64_t first) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * (128 + kColRows) * kStep];
+  __shared__ Side side;
   const Pieces c = count_pieces(p, 256);
   const int64_t w = first + blockIdx.x;
   if (w / cols >= c.total) return;
   const Rows r = find_rows(p, c, (int)(w / cols), 256);
   const int n0 = (int)(w % cols) * (GLU ? kColRows / 2 : kColRows);
   if (r.hi - r.lo <= 128)
-    tile<E, 4, 3, GLU>(p, r, n0, smem);
+    tile<E, 4, 3, GLU>(p, r, n0, smem, side);
   else
-    tile<E, 8, 2, GLU>(p, r, n0, smem);
+    tile<E, 8, 2, GLU>(p, r, n0, smem, side);
 }
 
 template <typename E>
