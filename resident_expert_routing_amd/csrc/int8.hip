@@ -391,12 +391,20 @@ __device__ __forceinline__ void barrier() {
 
 // What the epilogue needs of a tile's rows and columns, loaded beside the first
 // stage.
+constexpr int kMostRows = 256;
+
 struct Side {
-  float row[256], col[256];
-  int live[256];  // rows of out that are written
+  float row[kMostRows], col[kColRows];
+  int live[kMostRows];  // rows of out that are written
 };
 
 constexpr int kOutBytes = 16384;  // LDS that a wave's results pass through
+
+constexpr int part_of(int n, int most) {  // the largest divisor of n that is at most `most`
+  int d = n < most ? n : most;
+  while (n % d) --d;
+  return d;
+}
 
 template <typename E, int MF, int S, bool GLU>
 __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, uint8_t* smem,
@@ -455,16 +463,12 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   // rows of a.  Fragments are read two groups ahead (b's a half stage ahead), and
   // the loads of stage i + S - 1 are issued one for each group.
   i32x4 acc[MF][4] = {};
-  auto stage = [&](int i, auto more, auto cut) {
+  auto stage = [&](int i, auto more) {
     const uint8_t* sa = smem + (i % S) * kStage + (wm * MF * 16 + col) * kStep;
     const uint8_t* sb = smem + (i % S) * kStage + (kRows + wn * 64 + col) * kStep;
     const int slot[2] = {16 * (quad ^ (col & 7)), 16 * ((4 + quad) ^ (col & 7))};
     auto frag = [&](int x) { return *(const i32x4*)(sa + (x % MF) * 16 * kStep + slot[x / MF]); };
-    auto weight = [&](int c, int s) {
-      i32x4 v = *(const i32x4*)(sb + s * 16 * kStep + slot[c]);
-      if (decltype(cut)::value) v = mask_k(v, p.K - (i * kStep + 64 * c + 16 * quad));
-      return v;
-    };
+    auto weight = [&](int c, int s) { return *(const i32x4*)(sb + s * 16 * kStep + slot[c]); };
     i32x4 w[3], v[2][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) v[0][s] = weight(0, s);
@@ -486,17 +490,15 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   for (int i = 0; i < S - 1; ++i)
     if (i < steps)
       for (int j = 0; j < kLoads; ++j) load(i, j);
-  {
-    const int t = threadIdx.x & 255;
-    if (threadIdx.x < 256) {
-      const int src = r.lo + t < r.hi ? source_row(p, r.lo + t) : -1;
-      side.live[t] = src >= 0;
-      side.row[t] = src >= 0 ? p.a_scale[src] : 0.0f;
-    } else {
-      const int n = n0 + (GLU ? t & 127 : t);
-      side.col[t] = p.b_scale[(size_t)r.g * p.b_scale_group_stride + min(n, p.N - 1) +
-                              (GLU && t >= 128 ? p.N : 0)];
-    }
+  for (int t = threadIdx.x; t < kRows; t += kTWaves * kWave) {
+    const int src = r.lo + t < r.hi ? source_row(p, r.lo + t) : -1;
+    side.live[t] = src >= 0;
+    side.row[t] = src >= 0 ? p.a_scale[src] : 0.0f;
+  }
+  for (int t = threadIdx.x; t < kColRows; t += kTWaves * kWave) {
+    const int n = n0 + (GLU ? t & 127 : t);
+    side.col[t] = p.b_scale[(size_t)r.g * p.b_scale_group_stride + min(n, p.N - 1) +
+                            (GLU && t >= 128 ? p.N : 0)];
   }
   // At the top of stage i its loads, issued S - 1 stages ago, have to have
   // landed (those of the S - 2 stages after it may still be in flight), and
@@ -505,22 +507,27 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   for (; i + S - 1 < steps; ++i) {
     wait_loads<(S - 2) * kLoads>();
     barrier();
-    stage(i, std::true_type{}, std::false_type{});
+    stage(i, std::true_type{});
   }
   wait_loads<0>();
   barrier();
-  for (; i + 1 < steps; ++i) stage(i, std::false_type{}, std::false_type{});
-  if (p.K % 16 != 0)  // a piece that the row's end cuts is masked
-    stage(i, std::false_type{}, std::true_type{});
-  else
-    stage(i, std::false_type{}, std::false_type{});
+  if (p.K % 16 != 0) {  // the end of the row cuts a piece of the last stage: zeros from there on
+    const int k = p.K / 16 * 16 - (steps - 1) * kStep;
+    for (int x = threadIdx.x; x < kColRows; x += kTWaves * kWave) {
+      i32x4* at = (i32x4*)(smem + ((steps - 1) % S) * kStage + (kRows + x) * kStep +
+                           (k ^ (16 * (x & 7))));
+      *at = mask_k(*at, p.K % 16);
+    }
+    barrier();
+  }
+  for (; i < steps; ++i) stage(i, std::false_type{});
 
   // Results leave through LDS, each wave through a part of its own, so that
   // eight lanes store 128 consecutive bytes of a row of out.  16 bytes c of row
   // x lie at c ^ (x & 7) of each 128, for the banks.
   constexpr int kRowBytes = 4 * kOut * (int)sizeof(E);    // a wave's part of a row of out
   constexpr int kPartRows = kOutBytes / kRowBytes;        // rows that pass at a time
-  constexpr int kPart = MF * 16 < kPartRows ? MF : kPartRows / 16;  // fragments of them
+  constexpr int kPart = part_of(MF, kPartRows / 16);      // fragments of them
   constexpr int kPieces = kRowBytes / 16;
   float sn[4][4];
 #pragma unroll
@@ -563,16 +570,19 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
 }
 
 template <typename E, bool GLU>
-__global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int cols, int64_t first) {
+__global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int R, int cols,
+                                                               int64_t first) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * (128 + kColRows) * kStep];
   __shared__ Side side;
-  const Pieces c = count_pieces(p, 256);
+  const Pieces c = count_pieces(p, R);
   const int64_t w = first + blockIdx.x;
   if (w / cols >= c.total) return;
-  const Rows r = find_rows(p, c, (int)(w / cols), 256);
-  const int n0 = (int)(w % cols) * (GLU ? kColRows / 2 : kColRows);
-  if (r.hi - r.lo <= 128)
+  const Rows r = find_rows(p, c, (int)(w / cols), R);
+  const int n0 = (int)(w % cols) * (GLU ? kColRows / 2 : kColRows), rows = r.hi - r.lo;
+  if (rows <= 128)
     tile<E, 4, 3, GLU>(p, r, n0, smem, side);
+  else if (rows <= 192)
+    tile<E, 6, 2, GLU>(p, r, n0, smem, side);
   else
     tile<E, 8, 2, GLU>(p, r, n0, smem, side);
 }
@@ -580,13 +590,14 @@ __global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int c
 template <typename E>
 void launch_tiles(const MatArgs& p, bool glu, hipStream_t stream) {
   const int per = glu ? kColRows / 2 : kColRows, cols = (p.N + per - 1) / per;
-  const int64_t tiles = max_items(p.M, p.G, 256) * cols;
+  const int R = kMostRows;
+  const int64_t tiles = max_items(p.M, p.G, R) * cols;
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (glu)
-      int8_tiles<E, true><<<grid, kTWaves * kWave, 0, stream>>>(p, cols, first);
+      int8_tiles<E, true><<<grid, kTWaves * kWave, 0, stream>>>(p, R, cols, first);
     else
-      int8_tiles<E, false><<<grid, kTWaves * kWave, 0, stream>>>(p, cols, first);
+      int8_tiles<E, false><<<grid, kTWaves * kWave, 0, stream>>>(p, R, cols, first);
   }
 }
 
