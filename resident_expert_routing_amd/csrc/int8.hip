@@ -391,7 +391,7 @@ __device__ __forceinline__ void barrier() {
 
 // What the epilogue needs of a tile's rows and columns, loaded beside the first
 // stage.
-constexpr int kMostRows = 256;
+constexpr int kMostRows = 320;
 
 struct Side {
   float row[kMostRows], col[kColRows];
@@ -477,8 +477,12 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
 #pragma unroll
     for (int x = 0; x < 2 * MF; ++x) {
       if (x + 2 < 2 * MF) w[(x + 2) % 3] = frag(x + 2);
-      if (x < 4) v[1][x] = weight(1, x);
-      if (decltype(more)::value && x < kLoads) load(i + S - 1, x);
+#pragma unroll
+      for (int s = x; x < MF && s < 4; s += MF) v[1][s] = weight(1, s);
+      if (decltype(more)::value) {
+#pragma unroll
+        for (int j = x; j < kLoads; j += 2 * MF) load(i + S - 1, j);
+      }
 #pragma unroll
       for (int s = 0; s < 4; ++s)
         acc[x % MF][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[x / MF][s], w[x % 3],
@@ -572,25 +576,38 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
 template <typename E, bool GLU>
 __global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int R, int cols,
                                                                int64_t first) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * (128 + kColRows) * kStep];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (kMostRows + kColRows) * kStep];
   __shared__ Side side;
   const Pieces c = count_pieces(p, R);
   const int64_t w = first + blockIdx.x;
   if (w / cols >= c.total) return;
   const Rows r = find_rows(p, c, (int)(w / cols), R);
   const int n0 = (int)(w % cols) * (GLU ? kColRows / 2 : kColRows), rows = r.hi - r.lo;
-  if (rows <= 128)
+  if (rows <= 64)
+    tile<E, 2, 3, GLU>(p, r, n0, smem, side);
+  else if (rows <= 128)
     tile<E, 4, 3, GLU>(p, r, n0, smem, side);
   else if (rows <= 192)
     tile<E, 6, 2, GLU>(p, r, n0, smem, side);
-  else
+  else if (rows <= 256)
     tile<E, 8, 2, GLU>(p, r, n0, smem, side);
+  else
+    tile<E, 10, 2, GLU>(p, r, n0, smem, side);
+}
+
+// Most rows of a tile.  More rows share a load of b's, but a dense product's
+// last round of workgroups over the 256 CUs may then be emptier: its time goes
+// as rounds * (rows + 256), the bytes that a tile loads in a stage.
+int rows_of_tile(const MatArgs& p, int cols) {
+  if (p.G > 0) return kMostRows;
+  auto cost = [&](int R) { return (((int64_t)p.M + R - 1) / R * cols + 255) / 256 * (R + 256); };
+  return cost(256) < cost(kMostRows) ? 256 : kMostRows;
 }
 
 template <typename E>
 void launch_tiles(const MatArgs& p, bool glu, hipStream_t stream) {
   const int per = glu ? kColRows / 2 : kColRows, cols = (p.N + per - 1) / per;
-  const int R = kMostRows;
+  const int R = rows_of_tile(p, cols);
   const int64_t tiles = max_items(p.M, p.G, R) * cols;
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
