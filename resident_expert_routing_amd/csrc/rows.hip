@@ -22,17 +22,19 @@ constexpr int kMaxGrid = 1 << 22;      // workgroups of a launch; they stride ov
 constexpr int kLdsPositions = 16384;   // assignments that one workgroup orders in LDS
 
 struct RowsArgs {
-  int T, H, k, n;          // n = T*k rows
-  int lanes;               // threads of a token (a power of two, <= kThreads)
+  int T, H, k, n;  // n = T*k rows
   const int32_t* perm;
   const int32_t* pos;
   const float* weight;
-  const void* src;
-  void* dst;
-  const void* other;
+  const char* src;
+  char* dst;
+  const char* other;
   float* dweight;
-  size_t src_stride, dst_stride, other_stride;
+  size_t src_stride, dst_stride, other_stride;  // bytes
 };
+
+// A workgroup has one token at a time, so its rows and weights are scalars and
+// a row's address is a scalar base and a thread's 32-bit offset (H * 4 <= 2^32).
 
 // The rows of picks j0 .. j0 + 7 of token t: -1 past k and for absent ones.
 __device__ __forceinline__ void rows_of(const RowsArgs& p, int t, int j0, int (&row)[8]) {
@@ -40,7 +42,7 @@ __device__ __forceinline__ void rows_of(const RowsArgs& p, int t, int j0, int (&
   for (int u = 0; u < 8; ++u) {
     int r = -1;
     if (j0 + u < p.k) r = p.pos[(size_t)t * p.k + j0 + u];
-    row[u] = (unsigned)r < (unsigned)p.n ? r : -1;
+    row[u] = __builtin_amdgcn_readfirstlane((unsigned)r < (unsigned)p.n ? r : -1);
   }
 }
 
@@ -50,83 +52,101 @@ __device__ __forceinline__ void weights_of(const RowsArgs& p, int t, int j0, flo
     w[u] = p.weight && j0 + u < p.k ? p.weight[(size_t)t * p.k + j0 + u] : 1.0f;
 }
 
-// Row p of the output where perm names no assignment: picks with no slot have
-// no row of their own, so these are the last rows, and they are set to zero
-// (each by the token whose assignments have the same numbers).
-template <typename E>
-__device__ __forceinline__ void zero_unnamed(const RowsArgs& p, int t, int i, int left) {
-  if (!p.perm) return;
-  const Piece<E> zero{};
-  for (int j = 0; j < p.k; ++j) {
-    const size_t r = (size_t)t * p.k + j;
-    if ((unsigned)p.perm[r] >= (unsigned)p.n)
-      zero.store_upto((E*)p.dst + r * p.dst_stride + i, left);
-  }
+// A row is taken in pieces of N elements (16 bytes; single elements where the
+// row has fewer).  The last piece of a row that N does not divide starts early,
+// at H - N: what it shares with the piece before is computed twice, alike.
+template <typename E, int N>
+__device__ __forceinline__ uint32_t start_of(uint32_t i, uint32_t H) {
+  return N == 1 ? i : min(i, H - N);
+}
+template <typename E, int N>
+__device__ __forceinline__ void load_piece(Piece<E, N>& v, const char* row, uint32_t i) {
+  v.load((const E*)(row + i * (uint32_t)sizeof(E)));
+}
+template <typename E, int N>
+__device__ __forceinline__ void store_piece(const Piece<E, N>& v, char* row, uint32_t i) {
+  v.store((E*)(row + i * (uint32_t)sizeof(E)));
 }
 
-template <typename E>
-__device__ __forceinline__ Piece<E> scaled(const Piece<E>& v, float w) {
-  Piece<E> o;
+template <typename E, int N>
+__device__ __forceinline__ Piece<E, N> scaled(const Piece<E, N>& v, float w) {
+  Piece<E, N> o;
 #pragma unroll
-  for (int i = 0; i < Piece<E>::kN; ++i) o.e[i] = from_f32<E>(w * to_f32<E>(v.e[i]));
+  for (int i = 0; i < N; ++i) o.e[i] = from_f32<E>(w * to_f32<E>(v.e[i]));
   return o;
 }
 
-// spread: every thread reads a 16-byte piece of a token row and stores it k
-// times.  Bound by the stores.
-template <typename E>
+// The rows that perm gives no assignment: picks with no slot have no row of
+// their own, so these are the last rows, and they are set to zero (row t*k + j
+// by the workgroups of token t, the pieces from i0 to before i1 by this one).
+template <typename E, int N>
+__device__ __forceinline__ void zero_unnamed(const RowsArgs& p, int t, uint32_t i0, uint32_t i1) {
+  if (!p.perm) return;
+  for (int j = 0; j < p.k; ++j) {
+    const size_t r = (size_t)t * p.k + j;
+    if ((unsigned)p.perm[r] < (unsigned)p.n) continue;
+    for (uint32_t i = i0 + threadIdx.x * N; i < i1; i += blockDim.x * N)
+      store_piece(Piece<E, N>{}, p.dst + r * p.dst_stride, start_of<E, N>(i, p.H));
+  }
+}
+
+// spread: a thread reads pieces of a token row and stores each k times.  Bound
+// by the stores, which are as many bytes as the rows have.  A workgroup holds up
+// to kHold pieces a thread, so that it writes whole stretches of one row after
+// another.
+constexpr int kHold = 4;
+
+template <typename E, int N, bool WEIGHT>
 __global__ __launch_bounds__(kThreads) void spread_rows(RowsArgs p) {
-  constexpr int N = Piece<E>::kN;
-  const int per = kThreads / p.lanes;
-  const int lane = threadIdx.x & (p.lanes - 1);
-  for (int64_t t0 = (int64_t)blockIdx.x * per + threadIdx.x / p.lanes; t0 < p.T;
-       t0 += (int64_t)gridDim.x * per) {
-    const int t = (int)t0;
-    for (int i = (blockIdx.y * p.lanes + lane) * N; i < p.H; i += gridDim.y * p.lanes * N) {
-      const int left = p.H - i;
-      Piece<E> v;
-      v.load_upto((const E*)p.src + t * p.src_stride + i, left);
+  const uint32_t step = blockDim.x * N, span = kHold * step, H = p.H;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    for (uint32_t i0 = blockIdx.y * span; i0 < H; i0 += gridDim.y * span) {
+      const uint32_t first = i0 + threadIdx.x * N;
+      Piece<E, N> v[kHold];
+#pragma unroll
+      for (int c = 0; c < kHold; ++c)
+        if (first + c * step < H)
+          load_piece(v[c], p.src + t * p.src_stride, start_of<E, N>(first + c * step, H));
       for (int j0 = 0; j0 < p.k; j0 += 8) {
         int row[8];
         float w[8];
         rows_of(p, t, j0, row);
-        weights_of(p, t, j0, w);
+        if (WEIGHT) weights_of(p, t, j0, w);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (row[u] >= 0) {
-            const Piece<E> o = p.weight ? scaled<E>(v, w[u]) : v;
-            o.store_upto((E*)p.dst + (size_t)row[u] * p.dst_stride + i, left);
-          }
+        for (int u = 0; u < 8; ++u) {
+          if (row[u] < 0) continue;
+          char* to = p.dst + (size_t)row[u] * p.dst_stride;
+#pragma unroll
+          for (int c = 0; c < kHold; ++c)
+            if (first + c * step < H)
+              store_piece(WEIGHT ? scaled(v[c], w[u]) : v[c], to,
+                          start_of<E, N>(first + c * step, H));
+        }
       }
-      zero_unnamed<E>(p, t, i, left);
+      zero_unnamed<E, N>(p, t, i0, min(i0 + span, H));
     }
   }
 }
 
-// gather: every thread sums a 16-byte piece of a token row over its k rows,
-// eight loads in flight.  An absent pick's load goes to row 0 and is dropped
-// by a select, never multiplied, so what that row holds does not matter.
-template <typename E>
+// gather: a thread sums a piece of a token row over its k rows, eight loads in
+// flight.  An absent pick's load goes to row 0 and its sum is skipped, never
+// multiplied, so what that row holds does not matter.
+template <typename E, int N>
 __global__ __launch_bounds__(kThreads) void gather_rows(RowsArgs p) {
-  constexpr int N = Piece<E>::kN;
-  const int per = kThreads / p.lanes;
-  const int lane = threadIdx.x & (p.lanes - 1);
-  for (int64_t t0 = (int64_t)blockIdx.x * per + threadIdx.x / p.lanes; t0 < p.T;
-       t0 += (int64_t)gridDim.x * per) {
-    const int t = (int)t0;
-    for (int i = (blockIdx.y * p.lanes + lane) * N; i < p.H; i += gridDim.y * p.lanes * N) {
-      const int left = p.H - i;
+  const uint32_t step = blockDim.x * N, H = p.H;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    for (uint32_t i = blockIdx.y * step + threadIdx.x * N; i < H; i += gridDim.y * step) {
+      const uint32_t at = start_of<E, N>(i, H);
       float acc[N] = {};
       for (int j0 = 0; j0 < p.k; j0 += 8) {
         int row[8];
         float w[8];
-        Piece<E> v[8];
+        Piece<E, N> v[8];
         rows_of(p, t, j0, row);
         weights_of(p, t, j0, w);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          if (j0 + u < p.k)
-            v[u].load_upto((const E*)p.src + (size_t)max(row[u], 0) * p.src_stride + i, left);
+          if (j0 + u < p.k) load_piece(v[u], p.src + (size_t)max(row[u], 0) * p.src_stride, at);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (row[u] >= 0) {
@@ -134,19 +154,18 @@ __global__ __launch_bounds__(kThreads) void gather_rows(RowsArgs p) {
             for (int e = 0; e < N; ++e) acc[e] = fmaf(w[u], to_f32<E>(v[u].e[e]), acc[e]);
           }
       }
-      Piece<E> o;
+      Piece<E, N> o;
 #pragma unroll
       for (int e = 0; e < N; ++e) o.e[e] = from_f32<E>(acc[e]);
-      o.store_upto((E*)p.dst + t * p.dst_stride + i, left);
+      store_piece(o, p.dst + t * p.dst_stride, at);
     }
   }
 }
 
-// Sums of KP values over the threads of a token (64, one wave, or all 256): a
-// wave's by shuffles, then the waves' in ascending order through LDS.  Thread
-// `lane` < KP of the token gets value `lane`.
+// Sums of KP values over the workgroup: a wave's by shuffles, then the waves' in
+// ascending order through LDS.  Thread j < KP gets value j.
 template <int KP>
-__device__ __forceinline__ float token_sums(const float (&acc)[KP], int lanes, int lane) {
+__device__ __forceinline__ float token_sums(const float (&acc)[KP]) {
   __shared__ float part[kThreads / kWave][KP];
   const int wave = threadIdx.x / kWave;
   __syncthreads();  // the sums of the token before have been read
@@ -156,78 +175,66 @@ __device__ __forceinline__ float token_sums(const float (&acc)[KP], int lanes, i
     if ((threadIdx.x & 63) == j) part[wave][j] = s;
   }
   __syncthreads();
-  if (lane >= KP) return 0.0f;
-  if (lanes == kWave) return part[wave][lane];
-  float s = part[0][lane];
-#pragma unroll
-  for (int v = 1; v < kThreads / kWave; ++v) s += part[v][lane];
+  if (threadIdx.x >= KP) return 0.0f;
+  float s = part[0][threadIdx.x];
+  for (unsigned v = 1; v < blockDim.x / kWave; ++v) s += part[v][threadIdx.x];
   return s;
 }
 
 // The backward calls with the weight's gradient: spread or gather, and the dot
 // products of the token's k rows with its token row on the way, so neither is
 // read twice.  SPREAD: src holds the token rows, other the rows; otherwise src
-// holds the rows, other the token rows.  Every workgroup makes the same number
-// of rounds for all its tokens, so its barriers are reached by every wave.
-template <typename E, int KP, bool SPREAD>
+// holds the rows, other the token rows.
+template <typename E, int N, int KP, bool SPREAD>
 __global__ __launch_bounds__(kThreads) void rows_dot(RowsArgs p) {
-  constexpr int N = Piece<E>::kN;
-  const int per = kThreads / p.lanes;
-  const int lane = threadIdx.x & (p.lanes - 1);
-  for (int64_t b = (int64_t)blockIdx.x * per; b < p.T; b += (int64_t)gridDim.x * per) {
-    const int64_t t0 = b + threadIdx.x / p.lanes;
-    const int t = (int)(t0 < p.T ? t0 : p.T - 1);
+  const uint32_t step = blockDim.x * N, H = p.H;
+  const char* tokens = SPREAD ? p.src : p.other;
+  const char* rows = SPREAD ? p.other : p.src;
+  const size_t token_stride = SPREAD ? p.src_stride : p.other_stride;
+  const size_t row_stride = SPREAD ? p.other_stride : p.src_stride;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     float dot[KP] = {};
-    if (t0 < p.T) {
-      for (int i = lane * N; i < p.H; i += p.lanes * N) {
-        const int left = p.H - i;
-        Piece<E> tok;
-        if (SPREAD)
-          tok.load_upto((const E*)p.src + t * p.src_stride + i, left);
-        else
-          tok.load_upto((const E*)p.other + t * p.other_stride + i, left);
-        float acc[N] = {};
+    for (uint32_t i = threadIdx.x * N; i < H; i += step) {
+      const uint32_t at = start_of<E, N>(i, H), twice = i - at;  // elements counted before
+      Piece<E, N> tok;
+      load_piece(tok, tokens + t * token_stride, at);
+      float acc[N] = {};
 #pragma unroll
-        for (int j0 = 0; j0 < KP; j0 += 8) {
-          int row[8];
-          float w[8];
-          Piece<E> v[8];
-          rows_of(p, t, j0, row);
-          weights_of(p, t, j0, w);
+      for (int j0 = 0; j0 < KP; j0 += 8) {
+        int row[8];
+        float w[8];
+        Piece<E, N> v[8];
+        rows_of(p, t, j0, row);
+        weights_of(p, t, j0, w);
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (j0 + u < p.k) {
-              const E* base = SPREAD ? (const E*)p.other + (size_t)max(row[u], 0) * p.other_stride
-                                     : (const E*)p.src + (size_t)max(row[u], 0) * p.src_stride;
-              v[u].load_upto(base + i, left);
-            }
+        for (int u = 0; u < 8; ++u)
+          if (j0 + u < p.k) load_piece(v[u], rows + (size_t)max(row[u], 0) * row_stride, at);
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (row[u] >= 0) {
+        for (int u = 0; u < 8; ++u) {
+          if (row[u] < 0) continue;
+          if (SPREAD)
+            store_piece(p.weight ? scaled(tok, w[u]) : tok, p.dst + (size_t)row[u] * p.dst_stride,
+                        at);
 #pragma unroll
-              for (int e = 0; e < N; ++e) {
-                const float x = to_f32<E>(v[u].e[e]);
-                dot[j0 + u] = fmaf(x, to_f32<E>(tok.e[e]), dot[j0 + u]);
-                if (!SPREAD) acc[e] = fmaf(w[u], x, acc[e]);
-              }
-              if (SPREAD) {
-                const Piece<E> o = p.weight ? scaled<E>(tok, w[u]) : tok;
-                o.store_upto((E*)p.dst + (size_t)row[u] * p.dst_stride + i, left);
-              }
-            }
-        }
-        if (SPREAD) {
-          zero_unnamed<E>(p, t, i, left);
-        } else {
-          Piece<E> o;
-#pragma unroll
-          for (int e = 0; e < N; ++e) o.e[e] = from_f32<E>(acc[e]);
-          o.store_upto((E*)p.dst + t * p.dst_stride + i, left);
+          for (int e = 0; e < N; ++e) {
+            const float x = to_f32<E>(v[u].e[e]);
+            const float d = fmaf(x, to_f32<E>(tok.e[e]), dot[j0 + u]);
+            dot[j0 + u] = e + 1 == N || e >= (int)twice ? d : dot[j0 + u];
+            if (!SPREAD) acc[e] = fmaf(w[u], x, acc[e]);
+          }
         }
       }
+      if (!SPREAD) {
+        Piece<E, N> o;
+#pragma unroll
+        for (int e = 0; e < N; ++e) o.e[e] = from_f32<E>(acc[e]);
+        store_piece(o, p.dst + t * p.dst_stride, at);
+      }
     }
-    const float s = token_sums<KP>(dot, p.lanes, lane);
-    if (t0 < p.T && lane < p.k && lane < KP) p.dweight[(size_t)t * p.k + lane] = s;
+    if (SPREAD) zero_unnamed<E, N>(p, t, 0, H);
+    const float s = token_sums<KP>(dot);
+    if (threadIdx.x < KP && (int)threadIdx.x < p.k)
+      p.dweight[(size_t)t * p.k + threadIdx.x] = s;
   }
 }
 
@@ -299,43 +306,49 @@ int rows_status(const moe_rows_args* a, bool src_rows, bool backward) {
   return MOE_OK;
 }
 
-template <typename E, int KP, bool SPREAD>
-void launch_dot(RowsArgs p, hipStream_t stream) {
-  const int pieces = (p.H + Piece<E>::kN - 1) / Piece<E>::kN;
-  p.lanes = pieces <= 2 * kWave ? kWave : kThreads;
-  rows_dot<E, KP, SPREAD><<<blocks_for(p.T, kThreads / p.lanes), kThreads, 0, stream>>>(p);
+template <typename E, int N, bool SPREAD>
+void launch_pieces(const RowsArgs& p, hipStream_t stream) {
+  const int pieces = (p.H + N - 1) / N;
+  const int threads = pieces <= kWave ? kWave : pieces <= 2 * kWave ? 2 * kWave : kThreads;
+  const unsigned grid = blocks_for(p.T, 1);
+  if (p.dweight) {
+    if (p.k <= 8)
+      rows_dot<E, N, 8, SPREAD><<<grid, threads, 0, stream>>>(p);
+    else if (p.k <= 16)
+      rows_dot<E, N, 16, SPREAD><<<grid, threads, 0, stream>>>(p);
+    else
+      rows_dot<E, N, 32, SPREAD><<<grid, threads, 0, stream>>>(p);
+    return;
+  }
+  const int per = SPREAD ? threads * kHold : threads, across = (pieces + per - 1) / per;
+  const dim3 g(grid, across < 1024 ? across : 1024);
+  if (!SPREAD)
+    gather_rows<E, N><<<g, threads, 0, stream>>>(p);
+  else if (p.weight)
+    spread_rows<E, N, true><<<g, threads, 0, stream>>>(p);
+  else
+    spread_rows<E, N, false><<<g, threads, 0, stream>>>(p);
 }
 
 template <typename E, bool SPREAD>
-void launch_rows(RowsArgs p, hipStream_t stream) {
-  if (p.dweight) {
-    if (p.k <= 8)
-      launch_dot<E, 8, SPREAD>(p, stream);
-    else if (p.k <= 16)
-      launch_dot<E, 16, SPREAD>(p, stream);
-    else
-      launch_dot<E, 32, SPREAD>(p, stream);
-    return;
-  }
-  const int pieces = (p.H + Piece<E>::kN - 1) / Piece<E>::kN;
-  p.lanes = 1;
-  while (p.lanes < kThreads && p.lanes < pieces) p.lanes *= 2;
-  const int across = (pieces + p.lanes - 1) / p.lanes;
-  const dim3 grid(blocks_for(p.T, kThreads / p.lanes), across < 1024 ? across : 1024);
-  if (SPREAD)
-    spread_rows<E><<<grid, kThreads, 0, stream>>>(p);
+void launch_rows(const RowsArgs& p, hipStream_t stream) {
+  if (p.H >= Piece<E>::kN)
+    launch_pieces<E, Piece<E>::kN, SPREAD>(p, stream);
   else
-    gather_rows<E><<<grid, kThreads, 0, stream>>>(p);
+    launch_pieces<E, 1, SPREAD>(p, stream);
 }
 
 template <bool SPREAD>
 int rows_launch(const moe_rows_args* a, hipStream_t stream) {
   if (a->T == 0) return MOE_OK;
+  const size_t e = dtype_bytes(a->dtype);
   RowsArgs p{};
   p.T = a->T, p.H = a->H, p.k = a->k, p.n = a->T * a->k;
   p.perm = a->perm, p.pos = a->pos, p.weight = a->weight;
-  p.src = a->src, p.dst = a->dst, p.other = a->other, p.dweight = a->dweight;
-  p.src_stride = a->src_stride, p.dst_stride = a->dst_stride, p.other_stride = a->other_stride;
+  p.src = (const char*)a->src, p.dst = (char*)a->dst, p.other = (const char*)a->other;
+  p.dweight = a->dweight;
+  p.src_stride = a->src_stride * e, p.dst_stride = a->dst_stride * e;
+  p.other_stride = a->other_stride * e;
   if (a->dtype == MOE_DT_BF16)
     launch_rows<Bf16, SPREAD>(p, stream);
   else if (a->dtype == MOE_DT_FP16)
