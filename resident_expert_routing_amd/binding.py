@@ -190,11 +190,9 @@ def load() -> ctypes.CDLL:
 
 
 def _ptr(p) -> int | None:
-    if p is None:
-        return None
-    if isinstance(p, int):
+    if p is None or isinstance(p, int):
         return p
-    return int(p.data_ptr())
+    return p.data_ptr()
 
 
 def _host(a) -> int | None:

@@ -29,19 +29,73 @@ __host__ __device__ inline int up16(int v) { return (v + 15) & ~15; }
 constexpr int kQThreads = 256;
 constexpr int kQPieces = 4;  // 16-byte pieces of a row that a thread keeps
 
-// round(x / s) to the nearest integer, ties to even, of the exact quotient.
-// x * (1 / s) is within 2e-5 of it (|quotient| <= 127 and a bit, three
-// roundings of 2^-24 each), which decides everything but quotients that close
-// to a half; those are decided by the remainder x - q*s, exact in float64.
-__device__ __forceinline__ int quantized(float x, float s, float inv) {
-  const float t = x * inv;
-  float q = __builtin_rintf(t);
-  if (__builtin_expect(fabsf(fabsf(t - q) - 0.5f) < 1e-4f, 0)) {
-    const double e = fma(-(double)q, (double)s, (double)x), half = 0.5 * (double)s;
-    const float away = e > 0 ? 1.0f : -1.0f;
-    if (fabs(e) > half || (fabs(e) == half && ((int)q & 1))) q += away;
+// round(x / s) to the nearest integer, ties to even, of the exact quotient, for
+// a quotient that x * (1 / s) puts next to a half: the candidate q is decided by
+// the remainder x - q*s, exact in float64.
+__device__ __forceinline__ int settled(float x, float s, int q) {
+  const double e = fma(-(double)q, (double)s, (double)x), half = 0.5 * (double)s;
+  if (fabs(e) > half || (fabs(e) == half && (q & 1))) q += e > 0 ? 1 : -1;
+  return q;
+}
+
+// N quotients as bytes.  x * inv is within 2e-5 of the quotient (|quotient| <=
+// 127 and a bit, roundings of 2^-24 each), so its rounding is the quotient's
+// unless it lies within 1e-4 of a half, which is rare.  Adding 1.5 * 2^23 rounds
+// to an integer, ties to even, and leaves it in the sum's low byte.
+template <typename E, int N>
+__device__ __forceinline__ void quantize_piece(const Piece<E, N>& u, float s, float inv,
+                                               int8_t* out) {
+  constexpr float kRound = 12582912.0f;
+  uint32_t bits[N];
+  float off = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float x = to_f32<E>(u.e[e]), t = fmaf(x, inv, kRound);
+    bits[e] = __float_as_uint(t);
+    off = fmaxf(off, fabsf(fmaf(x, inv, -(t - kRound))));
   }
-  return (int)q;
+  if (__builtin_expect(off > 0.4999f, 0)) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      bits[e] = (uint32_t)settled(to_f32<E>(u.e[e]), s, (int)(int8_t)bits[e]);
+  }
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const uint32_t lo = __builtin_amdgcn_perm(bits[4 * i + 1], bits[4 * i], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(bits[4 * i + 3], bits[4 * i + 2], 0x0C0C0400u);
+    w[i] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+  }
+  __builtin_memcpy(out, w, N);
+}
+
+// The largest magnitude of a piece, as the bits of a float.  Types of 16 bits
+// compare two at a time; order and NaN are as for the floats they stand for.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <typename E, int N>
+__device__ __forceinline__ uint32_t top_bits(const Piece<E, N>& u, uint32_t top) {
+  uint32_t w[N * sizeof(E) / 4];
+  __builtin_memcpy(w, u.e, sizeof(w));
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = max(top, w[i] & 0x7FFFFFFFu);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      top = __builtin_bit_cast(
+          uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, top),
+                                              __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu)));
+  }
+  return top;
+}
+template <typename E>
+__device__ __forceinline__ uint32_t as_f32_bits(uint32_t top) {
+  if constexpr (sizeof(E) == 4) {
+    return top;
+  } else {
+    const uint32_t m = max(top & 0xFFFFu, top >> 16);
+    return __float_as_uint(to_f32<E>(E{(uint16_t)m}));
+  }
 }
 
 // One pass: the row stays in registers between its maximum and its rounding
@@ -63,11 +117,6 @@ __global__ __launch_bounds__(kQThreads) void quantize_rows(const E* __restrict__
     const E* row = x + (m < M ? m : M - 1) * x_stride;
     Piece<E> v[kQPieces];
     uint32_t top = 0;
-    auto fold = [&](const Piece<E>& u) {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        top = max(top, __float_as_uint(to_f32<E>(u.e[e])) & 0x7FFFFFFFu);
-    };
 #pragma unroll
     for (int c = 0; c < kQPieces; ++c) {
       const int i = (c * lanes + lane) * N;
@@ -77,13 +126,13 @@ __global__ __launch_bounds__(kQThreads) void quantize_rows(const E* __restrict__
         v[c] = Piece<E>{};
     }
 #pragma unroll
-    for (int c = 0; c < kQPieces; ++c) fold(v[c]);
+    for (int c = 0; c < kQPieces; ++c) top = top_bits(v[c], top);
     for (int i = (kQPieces * lanes + lane) * N; i < K; i += lanes * N) {
       Piece<E> u;
       u.load_upto(row + i, K - i);
-      fold(u);
+      top = top_bits(u, top);
     }
-    top = wave_umax32(top);
+    top = wave_umax32(as_f32_bits<E>(top));
     if (lanes > kWave) {
       __syncthreads();
       if ((threadIdx.x & 63) == 0) part[threadIdx.x / kWave] = top;
@@ -98,11 +147,7 @@ __global__ __launch_bounds__(kQThreads) void quantize_rows(const E* __restrict__
     if (lane == 0) scale[m] = finite ? s : __uint_as_float(0x7FC00000u);
     int8_t* out = q + m * q_stride;
     auto put = [&](const Piece<E>& u, int i) {  // whole pieces: the row is padded to 16 bytes
-      Piece<int8_t, N> o;
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        o.e[e] = finite ? (int8_t)quantized(to_f32<E>(u.e[e]), s, inv) : (int8_t)0;
-      o.store(out + i);
+      quantize_piece(finite ? u : Piece<E>{}, s, inv, out + i);
     };
 #pragma unroll
     for (int c = 0; c < kQPieces; ++c) {

@@ -14,7 +14,8 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .rows import DTYPES, RowOrder, combine, dtype_of, gpu_tensor, on_device, row_major, stream_of
+from .rows import (DTYPES, RowOrder, combine, dtype_of, gpu_tensor, on_its_device, row_major,
+                   stream_of)
 
 
 def _rows16(*shape, device) -> torch.Tensor:
@@ -70,10 +71,13 @@ def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = No
             raise ValueError("q must be int8 [M, K] with rows at multiples of 16 bytes")
         if scale.dtype != torch.float32 or scale.numel() != M or not scale.is_contiguous():
             raise ValueError("scale must hold M contiguous float32 values")
-    with on_device(x):
-        B.check(B.moe_int8_quantize(x, M, K, stride, dt, q, _stride(q, 0), scale, stream_of(x)),
-                "moe_int8_quantize")
+    _quantize(x, M, K, stride, dt, q, _stride(q, 0), scale)
     return q, scale
+
+
+@on_its_device
+def _quantize(x, *args):
+    B.check(B.moe_int8_quantize(x, *args, stream_of(x)), "moe_int8_quantize")
 
 
 def _stride(q: torch.Tensor, axis: int) -> int:
@@ -138,13 +142,17 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     od = dtype_of(out, "out")
     if (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
         raise ValueError("the rows of out must be contiguous and apart")
-    with on_device(a):
-        B.check(B.moe_int8_matmul(
-            M, N, K, G, swiglu, a_rows, a, _stride(a, 0), a_scale, index, index_div, offsets, b,
+    _matmul(a, M, N, K, G, swiglu, a_rows, _stride(a, 0), a_scale, index, index_div, offsets, b,
             _stride(b, -2), _stride(b, 0) if G else 0, b_scale,
             (b_scale.stride(0) if G > 1 else wide) if G else 0, out, out.stride(0) if M > 1 else N,
-            od, stream_of(a)), "moe_int8_matmul")
+            od)
     return out
+
+
+@on_its_device
+def _matmul(a, M, N, K, G, swiglu, a_rows, *args):
+    B.check(B.moe_int8_matmul(M, N, K, G, swiglu, a_rows, a, *args, stream_of(a)),
+            "moe_int8_matmul")
 
 
 class Int8Experts:

@@ -14,7 +14,7 @@ to the stream that first used it.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -25,15 +25,20 @@ DTYPES = {torch.bfloat16: B.MOE_DT_BF16, torch.float16: B.MOE_DT_FP16,
           torch.float32: B.MOE_DT_FP32}
 
 
-def on_device(t: torch.Tensor):
-    """A context in which the tensor's device is the current one."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
-
-
 def stream_of(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    """The handle of the current stream of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def on_its_device(call):
+    """`call`, with the device of its first argument (a tensor) the current one."""
+    @functools.wraps(call)
+    def run(t, *args, **kwargs):
+        if t.device.index == torch.cuda.current_device():
+            return call(t, *args, **kwargs)
+        with torch.cuda.device(t.device):
+            return call(t, *args, **kwargs)
+    return run
 
 
 def dtype_of(t: torch.Tensor, what: str) -> int:
@@ -44,7 +49,7 @@ def dtype_of(t: torch.Tensor, what: str) -> int:
 
 
 def gpu_tensor(t, what: str, device=None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a tensor on a GPU")
     if device is not None and t.device != device:
         raise ValueError(f"{what} is on {t.device}, the rows on {device}")
@@ -55,9 +60,17 @@ def row_major(t: torch.Tensor) -> tuple[torch.Tensor, int]:
     """(t, elements from row to row) of a matrix whose rows are contiguous and
     apart; other layouts (transposed, expanded) are copied first."""
     n, width = t.shape
-    if (width == 1 or t.stride(1) == 1) and (n <= 1 or t.stride(0) >= width):
-        return t, t.stride(0) if n > 1 else width
+    down, across = t.stride()
+    if (across == 1 or width == 1) and (n <= 1 or down >= width):
+        return t, down if n > 1 else width
     return t.contiguous(), width
+
+
+@on_its_device
+def _positions(perm, T, k):
+    pos = torch.empty((T, k), dtype=torch.int32, device=perm.device)
+    B.check(B.moe_positions(perm, T, k, pos, stream_of(perm)), "moe_positions")
+    return pos
 
 
 class RowOrder:
@@ -69,15 +82,11 @@ class RowOrder:
     def __init__(self, perm: torch.Tensor, T: int, k: int, pos: torch.Tensor | None = None):
         self.T, self.k = int(T), int(k)
         n = self.T * self.k
-        gpu_tensor(perm, "perm")
-        if perm.dtype != torch.int32 or perm.numel() != n:
+        if gpu_tensor(perm, "perm").dtype != torch.int32 or perm.numel() != n:
             raise ValueError(f"perm must hold T*k = {n} int32 values")
         self.perm = perm.contiguous()
         if pos is None:
-            pos = torch.empty((self.T, self.k), dtype=torch.int32, device=perm.device)
-            with on_device(perm):
-                B.check(B.moe_positions(self.perm, self.T, self.k, pos, stream_of(perm)),
-                        "moe_positions")
+            pos = _positions(self.perm, self.T, self.k)
         elif gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or pos.numel() != n:
             raise ValueError(f"pos must hold T*k = {n} int32 values")
         self.pos = pos.contiguous()
@@ -98,38 +107,36 @@ def _check(src: torch.Tensor, n: int, order: RowOrder, what: str) -> None:
         raise ValueError(f"{what} must have shape [{n}, H], not {list(src.shape)}")
 
 
+@on_its_device
 def _spread(src, order, weight, rows=None):
     """Token rows to rows; with `rows` (the forward rows) the weights' gradient too."""
-    dt, (src, stride), H = dtype_of(src, "rows"), row_major(src), src.shape[1]
-    dst = torch.empty((order.T * order.k, H), dtype=src.dtype, device=src.device)
-    with on_device(src):
-        if rows is None:
-            B.check(B.moe_dispatch(order.T, H, order.k, dt, order.pos, src, stride, dst, H, weight,
-                                   order.perm, stream_of(src)), "moe_dispatch")
-            return dst, None
-        rows, rstride = row_major(rows)
-        dw = torch.empty((order.T, order.k), dtype=torch.float32, device=src.device)
-        B.check(B.moe_combine_backward(order.T, H, order.k, dt, order.pos, src, stride, dst, H,
-                                       weight, order.perm, rows, rstride, dw, stream_of(src)),
-                "moe_combine_backward")
-        return dst, dw
+    dt, (src, stride), H, T, k = dtype_of(src, "rows"), row_major(src), src.shape[1], order.T, order.k
+    dst = torch.empty((T * k, H), dtype=src.dtype, device=src.device)
+    if rows is None:
+        B.check(B.moe_dispatch(T, H, k, dt, order.pos, src, stride, dst, H, weight, order.perm,
+                               stream_of(src)), "moe_dispatch")
+        return dst, None
+    rows, rstride = row_major(rows)
+    dw = torch.empty((T, k), dtype=torch.float32, device=src.device)
+    B.check(B.moe_combine_backward(T, H, k, dt, order.pos, src, stride, dst, H, weight, order.perm,
+                                   rows, rstride, dw, stream_of(src)), "moe_combine_backward")
+    return dst, dw
 
 
+@on_its_device
 def _gather(src, order, weight, tokens=None):
     """Rows to token rows; with `tokens` (the forward token rows) the weights' gradient too."""
-    dt, (src, stride), H = dtype_of(src, "rows"), row_major(src), src.shape[1]
-    dst = torch.empty((order.T, H), dtype=src.dtype, device=src.device)
-    with on_device(src):
-        if tokens is None:
-            B.check(B.moe_combine(order.T, H, order.k, dt, order.pos, src, stride, dst, H, weight,
-                                  stream_of(src)), "moe_combine")
-            return dst, None
-        tokens, tstride = row_major(tokens)
-        dw = torch.empty((order.T, order.k), dtype=torch.float32, device=src.device)
-        B.check(B.moe_dispatch_backward(order.T, H, order.k, dt, order.pos, src, stride, dst, H,
-                                        weight, tokens, tstride, dw, stream_of(src)),
-                "moe_dispatch_backward")
-        return dst, dw
+    dt, (src, stride), H, T, k = dtype_of(src, "rows"), row_major(src), src.shape[1], order.T, order.k
+    dst = torch.empty((T, H), dtype=src.dtype, device=src.device)
+    if tokens is None:
+        B.check(B.moe_combine(T, H, k, dt, order.pos, src, stride, dst, H, weight,
+                              stream_of(src)), "moe_combine")
+        return dst, None
+    tokens, tstride = row_major(tokens)
+    dw = torch.empty((T, k), dtype=torch.float32, device=src.device)
+    B.check(B.moe_dispatch_backward(T, H, k, dt, order.pos, src, stride, dst, H, weight, tokens,
+                                    tstride, dw, stream_of(src)), "moe_dispatch_backward")
+    return dst, dw
 
 
 class _Move(torch.autograd.Function):
