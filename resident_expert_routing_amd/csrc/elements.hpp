@@ -49,16 +49,35 @@ __device__ __forceinline__ float from_f32<float>(float v) {
   return v;
 }
 
-// N consecutive elements.  The copies go through memcpy, so a piece may start
-// at any element: the compiler emits one 16-byte access, which the hardware
-// takes at any address.
+// 16 bytes at any element's address, which the hardware takes in one access.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+
+// N consecutive elements.  16 bytes pass as one value of four words: element by
+// element the compiler joins them to smaller accesses (quantising 65536 rows of
+// 2048: 92 us against 74; dispatch of 2048 rows of 4096 to 8 places: 42 against
+// 32).
 template <typename E, int N = 16 / (int)sizeof(E)>
 struct Piece {
   static constexpr int kN = N;
   E e[N];
 
-  __device__ __forceinline__ void load(const E* p) { __builtin_memcpy(e, p, sizeof(e)); }
-  __device__ __forceinline__ void store(E* p) const { __builtin_memcpy(p, e, sizeof(e)); }
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (sizeof(e) == 16) {
+      const u32x4 w = *(const u32x4*)p;
+      __builtin_memcpy(e, &w, 16);
+    } else {
+      __builtin_memcpy(e, p, sizeof(e));
+    }
+  }
+  __device__ __forceinline__ void store(E* p) const {
+    if constexpr (sizeof(e) == 16) {
+      u32x4 w;
+      __builtin_memcpy(&w, e, 16);
+      *(u32x4*)p = w;
+    } else {
+      __builtin_memcpy(p, e, sizeof(e));
+    }
+  }
   // the first n elements only (n < N); the others are zero
   __device__ __forceinline__ void load_head(const E* p, int n) {
 #pragma unroll

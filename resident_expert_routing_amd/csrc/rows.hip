@@ -60,11 +60,6 @@ template <typename E, int N>
 __device__ __forceinline__ uint32_t start_of(uint32_t i, uint32_t H) {
   return N == 1 ? i : min(i, H - N);
 }
-// 16 bytes pass as one value of four words: element by element the compiler
-// joins them to smaller accesses (2048 x 4096 token rows, top-8, dispatch: 42 us
-// against 32).
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
-
 template <typename E, int N>
 __device__ __forceinline__ void load_piece(Piece<E, N>& v, const char* row, uint32_t i) {
   v.load((const E*)(row + i * (uint32_t)sizeof(E)));
@@ -88,13 +83,10 @@ __device__ __forceinline__ void load_once(Piece<E, N>& v, const char* row, uint3
 // those rows 181 us against 190).
 template <bool NT, typename E, int N>
 __device__ __forceinline__ void store_piece(const Piece<E, N>& v, char* row, uint32_t i) {
-  if constexpr (N * sizeof(E) == 16) {
+  if constexpr (NT && N * sizeof(E) == 16) {
     u32x4 w;
     __builtin_memcpy(&w, v.e, 16);
-    if constexpr (NT)
-      __builtin_nontemporal_store(w, (u32x4*)(row + i * (uint32_t)sizeof(E)));
-    else
-      *(u32x4*)(row + i * (uint32_t)sizeof(E)) = w;
+    __builtin_nontemporal_store(w, (u32x4*)(row + i * (uint32_t)sizeof(E)));
   } else {
     v.store((E*)(row + i * (uint32_t)sizeof(E)));
   }
