@@ -78,6 +78,17 @@ struct Piece {
       __builtin_memcpy(p, e, sizeof(e));
     }
   }
+  __device__ __forceinline__ void store_past(E* p) const {  // past the caches (16 bytes)
+    u32x4 w;
+    static_assert(sizeof(e) == 16, "a whole piece");
+    __builtin_memcpy(&w, e, 16);
+    __builtin_nontemporal_store(w, (u32x4*)p);
+  }
+  __device__ __forceinline__ void load_past(const E* p) {
+    static_assert(sizeof(e) == 16, "a whole piece");
+    const u32x4 w = __builtin_nontemporal_load((const u32x4*)p);
+    __builtin_memcpy(e, &w, 16);
+  }
   // the first n elements only (n < N); the others are zero
   __device__ __forceinline__ void load_head(const E* p, int n) {
 #pragma unroll

@@ -183,58 +183,95 @@ struct Rows {
 
 __device__ __forceinline__ int clamp_row(int v, int M) { return min(max(v, 0), M); }
 
-// The pieces of at most R rows that the groups make, counted through the groups
-// in order.  Every wave does it by itself: each lane counts the pieces of its
-// share of the groups, and a scan over the lanes gives the sums.  Offsets
-// outside [0, M] are cut, and sums stop at a bound above every count, so that
-// offsets which are no bucketing cannot overflow them.
+// Which rows a workgroup has.  The groups' rows are cut into pieces of at most R,
+// counted through the groups in order, and every wave finds the item-th piece by
+// itself: a lane counts the pieces of its share of consecutive groups, a scan
+// over the lanes gives the sums, the first lane whose sum passes `item` holds its
+// group.  Offsets outside [0, M] are cut, and sums stop at a bound above every
+// count, so that offsets which are no bucketing cannot overflow them.
+constexpr int kShare = 4;  // groups of a lane that stay in registers (G <= 256)
+constexpr int kMostPieces = 1 << 29;
+
 struct Pieces {
-  int sum;    // pieces of this lane's groups and the lanes' before it
-  int total;  // of all groups
+  int sum;          // pieces of this lane's groups and the lanes' before it
+  int before;       // of the lanes before it
+  int total;        // of all groups
+  int edge[kShare + 1];  // its groups' offsets, where G <= 256
 };
 
-__device__ __forceinline__ int pieces_of(const MatArgs& p, int g, int R) {
-  const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+__device__ __forceinline__ int pieces_of(int lo, int hi, int R) {
   return hi > lo ? (hi - lo) / R + ((hi - lo) % R != 0) : 0;
 }
 
-__device__ __forceinline__ int first_group(const MatArgs& p, int lane) {
-  return min(lane * ((p.G + 63) / 64), p.G);
+// Inclusive sums over the lanes: within rows of 16, then lane 15 of a row into
+// the next, then lane 31 into the upper half.
+__device__ __forceinline__ int wave_scan(int v) {
+#define MOE_SCAN_STEP(CTRL, ROWS) \
+  v = min(v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false), kMostPieces);
+  MOE_SCAN_STEP(0x111, 0xF)  // row_shr by 1, 2, 4, 8
+  MOE_SCAN_STEP(0x112, 0xF)
+  MOE_SCAN_STEP(0x114, 0xF)
+  MOE_SCAN_STEP(0x118, 0xF)
+  MOE_SCAN_STEP(kDppBcast15, 0xA)
+  MOE_SCAN_STEP(kDppBcast31, 0xC)
+#undef MOE_SCAN_STEP
+  return v;
 }
 
 __device__ __forceinline__ Pieces count_pieces(const MatArgs& p, int R) {
-  if (!p.offsets) return {0, p.M / R + (p.M % R != 0)};
-  constexpr int kMost = 1 << 29;
-  const int lane = threadIdx.x & 63;
-  int sum = 0;
-  for (int g = first_group(p, lane); g < first_group(p, lane + 1); ++g)
-    sum = min(sum + pieces_of(p, g, R), kMost);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(sum, d, 64);
-    if (lane >= d) sum = min(sum + o, kMost);
+  Pieces c{};
+  if (!p.offsets) {
+    c.total = p.M / R + (p.M % R != 0);
+    return c;
   }
-  return {sum, __builtin_amdgcn_readlane(sum, 63)};
+  const int lane = threadIdx.x & 63;
+  int mine = 0;
+  if (p.G <= 64 * kShare) {
+#pragma unroll
+    for (int i = 0; i <= kShare; ++i)
+      c.edge[i] = clamp_row(p.offsets[min(lane * kShare + i, p.G)], p.M);
+#pragma unroll
+    for (int i = 0; i < kShare; ++i) mine += pieces_of(c.edge[i], c.edge[i + 1], R);
+  } else {
+    const int share = (p.G + 63) / 64;
+    for (int g = lane * share; g < min(lane * share + share, p.G); ++g)
+      mine = min(mine + pieces_of(clamp_row(p.offsets[g], p.M), clamp_row(p.offsets[g + 1], p.M), R),
+                 kMostPieces);
+  }
+  c.sum = wave_scan(min(mine, kMostPieces));
+  c.before = __shfl_up(c.sum, 1, 64);
+  if (lane == 0) c.before = 0;
+  c.total = __builtin_amdgcn_readlane(c.sum, 63);
+  return c;
 }
 
-// The item-th piece, item < c.total: the first lane whose sum passes it holds
-// its group.
 __device__ __forceinline__ Rows find_rows(const MatArgs& p, const Pieces& c, int item, int R) {
   if (!p.offsets) return {0, item * R, min(p.M, item * R + R)};
   const int lane = threadIdx.x & 63;
   const int owner = __ffsll((long long)__ballot(c.sum > item)) - 1;
-  int g = first_group(p, lane), before = __shfl_up(c.sum, 1, 64);
-  if (lane == 0) before = 0;
-  if (lane == owner)
-    for (; g < first_group(p, lane + 1) - 1; ++g) {
-      const int n = pieces_of(p, g, R);
-      if (before + n > item) break;
-      before += n;
+  int g, left = item - c.before, lo, hi;  // left: of the pieces from group g on
+  if (p.G <= 64 * kShare) {
+    int i = 0;
+    lo = c.edge[0], hi = c.edge[1];
+#pragma unroll
+    for (int j = 1; j < kShare; ++j) {
+      const int n = pieces_of(lo, hi, R);
+      if (i == j - 1 && left >= n) i = j, left -= n, lo = c.edge[j], hi = c.edge[j + 1];
     }
-  g = __builtin_amdgcn_readfirstlane(__shfl(g, owner, 64));
-  before = __builtin_amdgcn_readfirstlane(__shfl(before, owner, 64));
-  const int lo = clamp_row(p.offsets[g], p.M) + (item - before) * R;
-  return {g, lo, min(clamp_row(p.offsets[g + 1], p.M), lo + R)};
+    g = lane * kShare + i;
+  } else {
+    const int share = (p.G + 63) / 64, last = min(lane * share + share, p.G) - 1;
+    g = min(lane * share, p.G - 1);
+    lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+    if (lane == owner)
+      for (int n; g < last && left >= (n = pieces_of(lo, hi, R)); left -= n) {
+        ++g;
+        lo = hi, hi = clamp_row(p.offsets[g + 1], p.M);
+      }
+  }
+  g = __builtin_amdgcn_readlane(g, owner);
+  lo = __builtin_amdgcn_readlane(lo, owner) + __builtin_amdgcn_readlane(left, owner) * R;
+  return {g, lo, min(__builtin_amdgcn_readlane(hi, owner), lo + R)};
 }
 
 // Most pieces of R rows that M rows in G groups can make.
@@ -252,7 +289,11 @@ __device__ __forceinline__ int source_row(const MatArgs& p, int m) {
   return (unsigned)r < (unsigned)p.a_rows ? r : -1;
 }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
+// v / (1 + exp(-v)); the reciprocal's error is one unit in the last place, where
+// the division's ten instructions took 2 us of a tile's epilogue.
+__device__ __forceinline__ float silu(float v) {
+  return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
 
 template <typename E>
 __device__ __forceinline__ void store4(const MatArgs& p, int m, int n, const float (&y)[4]) {
@@ -284,18 +325,20 @@ __device__ __forceinline__ i32x4 mask_k(i32x4 v, int valid) {  // the first `val
   return v;
 }
 
-// Streaming form, for few rows in each group: a workgroup takes 32 rows of b
-// (with SwiGLU, 16 gate rows and their 16 up rows) and up to 16 * MT rows of
-// one group, its kSWaves waves the chunks of 64 along K in turn; the integer
-// sums are added through LDS.  b goes from memory straight to the registers of
-// the matrix instruction (lane l: row l % 16, bytes 16 (l / 16) of the chunk),
-// since nothing else in the workgroup uses it.
-constexpr int kSWaves = 4;
-constexpr int kSUnroll = 4;  // chunks in flight
+// Streaming form, for products of few tiles: a workgroup takes 32 rows of b (with
+// SwiGLU, 16 gate rows and their 16 up rows) and up to 16 * MT rows of one
+// group, its W waves the chunks of 64 along K in turn; the integer sums are added
+// through LDS.  b goes from memory straight to the registers of the matrix
+// instruction (lane l: row l % 16, bytes 16 (l / 16) of the chunk), since nothing
+// else in the workgroup uses it.  Bound by the latency of those loads, kSUnroll
+// chunks of a wave in flight: one row, K = 4096, 2N = 4096 (16.8 MB) takes 7.5 us
+// with eight waves, 7.8 with four, and 8.3 with four and half the chunks in
+// flight; one row each of eight such groups 33 us with eight waves, 29.8 with four.
+constexpr int kSUnroll = 8;
 
-template <int MT, bool GLU>
+template <int W, int MT, bool GLU>
 __device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int n0,
-                                            i32x4 (&part)[kSWaves][MT * 2][kWave]) {
+                                            i32x4 (&part)[W][MT * 2][kWave]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
   const int col = lane & 15, quad = lane >> 4;
 
@@ -314,11 +357,11 @@ __device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int
   i32x4 acc[MT][2] = {};
   const int full = p.K / 64;  // chunks that lie inside the rows
   int c = wave;
-  for (; c + kSWaves * (kSUnroll - 1) < full; c += kSWaves * kSUnroll) {
+  for (; c + W * (kSUnroll - 1) < full; c += W * kSUnroll) {
     i32x4 wb[kSUnroll][2], wa[kSUnroll][MT];
 #pragma unroll
     for (int u = 0; u < kSUnroll; ++u) {
-      const int k = 64 * (c + kSWaves * u) + 16 * quad;
+      const int k = 64 * (c + W * u) + 16 * quad;
 #pragma unroll
       for (int s = 0; s < 2; ++s) wb[u][s] = load_k(brow[s], k);
 #pragma unroll
@@ -332,7 +375,7 @@ __device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int
         for (int s = 0; s < 2; ++s)
           acc[t][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wb[u][s], wa[u][t], acc[t][s], 0, 0, 0);
   }
-  for (; 64 * c < p.K; c += kSWaves) {
+  for (; 64 * c < p.K; c += W) {
     const int k = 64 * c + 16 * quad, valid = p.K - k;
     const int at = valid > 0 ? k : 0;  // a piece past the row is read from its start and zeroed
     i32x4 wb[2];
@@ -352,13 +395,13 @@ __device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int
 #pragma unroll
     for (int s = 0; s < 2; ++s) part[wave][t * 2 + s][lane] = acc[t][s];
   __syncthreads();
-  for (int t = wave; t < MT; t += kSWaves) {
+  for (int t = wave; t < MT; t += W) {
     i32x4 sum[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       sum[s] = part[0][t * 2 + s][lane];
 #pragma unroll
-      for (int w = 1; w < kSWaves; ++w) sum[s] += part[w][t * 2 + s][lane];
+      for (int w = 1; w < W; ++w) sum[s] += part[w][t * 2 + s][lane];
     }
     // lane: row `col` of out, columns 4 * quad .. + 3 of each 16
     const int m = r.lo + 16 * t + col;
@@ -389,27 +432,35 @@ __device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int
   }
 }
 
-template <int MT, bool GLU>
-__global__ __launch_bounds__(kSWaves* kWave) void int8_stream(MatArgs p, int cols, int64_t first) {
-  __shared__ i32x4 part[kSWaves][MT * 2][kWave];
+template <int W, int MT, bool GLU>
+__global__ __launch_bounds__(W* kWave) void int8_stream(MatArgs p, int cols, int64_t first) {
+  __shared__ i32x4 part[W][MT * 2][kWave];
   const Pieces c = count_pieces(p, 16 * MT);
   const int64_t w = first + blockIdx.x;
   if (w / cols >= c.total) return;
   const Rows r = find_rows(p, c, (int)(w / cols), 16 * MT);
-  stream_tile<MT, GLU>(p, r, (int)(w % cols) * (GLU ? 16 : 32), part);
+  stream_tile<W, MT, GLU>(p, r, (int)(w % cols) * (GLU ? 16 : 32), part);
+}
+
+template <int W, int MT>
+void launch_stream_of(const MatArgs& p, bool glu, int cols, int64_t tiles, hipStream_t stream) {
+  for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+    const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
+    if (glu)
+      int8_stream<W, MT, true><<<grid, W * kWave, 0, stream>>>(p, cols, first);
+    else
+      int8_stream<W, MT, false><<<grid, W * kWave, 0, stream>>>(p, cols, first);
+  }
 }
 
 template <int MT>
 void launch_stream(const MatArgs& p, bool glu, hipStream_t stream) {
   const int per = glu ? 16 : 32, cols = (p.N + per - 1) / per;
   const int64_t tiles = max_items(p.M, p.G, 16 * MT) * cols;
-  for (int64_t first = 0; first < tiles; first += kMaxGrid) {
-    const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
-    if (glu)
-      int8_stream<MT, true><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, first);
-    else
-      int8_stream<MT, false><<<grid, kSWaves * kWave, 0, stream>>>(p, cols, first);
-  }
+  if (tiles <= 512)  // two for each CU: more waves, so that enough is in flight
+    launch_stream_of<8, MT>(p, glu, cols, tiles, stream);
+  else
+    launch_stream_of<4, MT>(p, glu, cols, tiles, stream);
 }
 
 // Tiled form, for groups of more rows: a workgroup of eight waves, two by four,
@@ -469,12 +520,6 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   // eight.  LDS place (row, c) holds piece c ^ (row & 7) of the row's 128 bytes,
   // so that the 16 rows of a fragment spread over the banks.
   const int piece = 16 * ((lane & 7) ^ (lane >> 3));
-  const int8_t* arow[kLoadsA];
-#pragma unroll
-  for (int j = 0; j < kLoadsA; ++j) {
-    const int m = r.lo + (wave * kLoadsA + j) * 8 + (lane >> 3);
-    arow[j] = p.a + (size_t)max(source_row(p, min(m, r.hi - 1)), 0) * p.a_stride + piece;
-  }
   // LDS row 64 w + 16 s + x of b is row x of fragment s of the waves wn = w: the
   // weight row that gives lane quad q of the result the columns kOut * q + 4 * s
   // + i, so that a lane ends with kOut consecutive columns of out.
@@ -490,23 +535,38 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   const int steps = (p.K + kStep - 1) / kStep;
   const int width = up16(p.K);
 
-  // Load j of stage i's kLoads.  Behind a row, b's pieces are zero, and a's any
-  // bytes of the row.
-  auto load = [&](int i, int j) {
-    uint8_t* base = smem + (i % S) * kStage;
+  // Loads of stage i.  Behind a row, b's pieces are zero, and a's any bytes of
+  // the row.
+  auto load_b = [&](int i, int j) {
     const int k = i * kStep;
-    const bool in = k + piece < width;
+    dma16(k + piece < width ? (const uint8_t*)brow[j] + k : kZeros,
+          smem + (i % S) * kStage + kRows * kStep + (wave * kLoadsB + j) * 1024);
+  };
+#pragma unroll
+  for (int j = 0; j < kLoadsB; ++j) load_b(0, j);
+  const int8_t* arow[kLoadsA];
+#pragma unroll
+  for (int j = 0; j < kLoadsA; ++j) {
+    const int m = r.lo + (wave * kLoadsA + j) * 8 + (lane >> 3);
+    arow[j] = p.a + (size_t)max(source_row(p, min(m, r.hi - 1)), 0) * p.a_stride + piece;
+  }
+  auto load_a = [&](int i, int j) {
+    const int k = i * kStep;
+    dma16((const uint8_t*)arow[j] + (k + piece < width ? k : -piece),
+          smem + (i % S) * kStage + (wave * kLoadsA + j) * 1024);
+  };
+  auto load = [&](int i, int j) {
     if (j < kLoadsB)
-      dma16(in ? (const uint8_t*)brow[j] + k : kZeros,
-            base + kRows * kStep + (wave * kLoadsB + j) * 1024);
+      load_b(i, j);
     else
-      dma16((const uint8_t*)arow[j - kLoadsB] + (in ? k : -piece),
-            base + (wave * kLoadsA + j - kLoadsB) * 1024);
+      load_a(i, j - kLoadsB);
   };
 
   // One stage: 2 * MF groups of four products, a group for each 64 bytes of 16
   // rows of a.  Fragments are read two groups ahead (b's a half stage ahead), and
-  // the loads of stage i + S - 1 are issued one for each group.
+  // the loads of stage i + S - 1 are issued one for each group.  A wave at its
+  // products goes before the SIMD's other one at its loads (dense 8192^3 449 us
+  // against 427).
   i32x4 acc[MF][4] = {};
   auto stage = [&](int i, auto more) {
     const uint8_t* sa = smem + (i % S) * kStage + (wm * MF * 16 + col) * kStep;
@@ -528,17 +588,19 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
 #pragma unroll
         for (int j = x; j < kLoads; j += 2 * MF) load(i + S - 1, j);
       }
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
         acc[x % MF][s] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[x / MF][s], w[x % 3],
                                                                acc[x % MF][s], 0, 0, 0);
+      __builtin_amdgcn_s_setprio(0);
     }
   };
 
 #pragma unroll
   for (int i = 0; i < S - 1; ++i)
     if (i < steps)
-      for (int j = 0; j < kLoads; ++j) load(i, j);
+      for (int j = i ? 0 : kLoadsB; j < kLoads; ++j) load(i, j);
   for (int t = threadIdx.x; t < kRows; t += kTWaves * kWave) {
     const int src = r.lo + t < r.hi ? source_row(p, r.lo + t) : -1;
     side.live[t] = src >= 0;
@@ -573,7 +635,8 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
 
   // Results leave through LDS, each wave through a part of its own, so that
   // eight lanes store 128 consecutive bytes of a row of out.  16 bytes c of row
-  // x lie at c ^ (x & 7) of each 128, for the banks.
+  // x lie at c ^ (x & 7) of each 128, for the banks.  The stores pass the caches
+  // by, which leaves these to a and b (8192 x 8192 x 2048 137 us against 121).
   constexpr int kRowBytes = 4 * kOut * (int)sizeof(E);    // a wave's part of a row of out
   constexpr int kPartRows = kOutBytes / kRowBytes;        // rows that pass at a time
   constexpr int kPart = part_of(MF, kPartRows / 16);      // fragments of them
@@ -612,8 +675,12 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
       Piece<E> o;
       __builtin_memcpy(o.e, place(x, c), 16);
       const int row = (wm * MF + f0) * 16 + x, n = n0 + wn * 4 * kOut + c * Piece<E>::kN;
-      if (side.live[row] && n < p.N)
-        o.store_upto((E*)p.out + (size_t)(r.lo + row) * p.out_stride + n, p.N - n);
+      if (!side.live[row] || n >= p.N) continue;
+      E* to = (E*)p.out + (size_t)(r.lo + row) * p.out_stride + n;
+      if (p.N - n >= Piece<E>::kN)
+        o.store_past(to);
+      else
+        o.store_head(to, p.N - n);
     }
   }
 }

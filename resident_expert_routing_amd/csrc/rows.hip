@@ -70,12 +70,10 @@ __device__ __forceinline__ void load_piece(Piece<E, N>& v, const char* row, uint
 // against 167, with its gradient 772 against 547.
 template <typename E, int N>
 __device__ __forceinline__ void load_once(Piece<E, N>& v, const char* row, uint32_t i) {
-  if constexpr (N * sizeof(E) == 16) {
-    const u32x4 w = __builtin_nontemporal_load((const u32x4*)(row + i * (uint32_t)sizeof(E)));
-    __builtin_memcpy(v.e, &w, 16);
-  } else {
+  if constexpr (N * sizeof(E) == 16)
+    v.load_past((const E*)(row + i * (uint32_t)sizeof(E)));
+  else
     load_piece(v, row, i);
-  }
 }
 
 // NT: past the caches.  Beside such loads that is faster (the same combine 167
@@ -83,13 +81,10 @@ __device__ __forceinline__ void load_once(Piece<E, N>& v, const char* row, uint3
 // those rows 181 us against 190).
 template <bool NT, typename E, int N>
 __device__ __forceinline__ void store_piece(const Piece<E, N>& v, char* row, uint32_t i) {
-  if constexpr (NT && N * sizeof(E) == 16) {
-    u32x4 w;
-    __builtin_memcpy(&w, v.e, 16);
-    __builtin_nontemporal_store(w, (u32x4*)(row + i * (uint32_t)sizeof(E)));
-  } else {
+  if constexpr (NT && N * sizeof(E) == 16)
+    v.store_past((E*)(row + i * (uint32_t)sizeof(E)));
+  else
     v.store((E*)(row + i * (uint32_t)sizeof(E)));
-  }
 }
 
 template <typename E, int N>
