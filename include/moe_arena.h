@@ -716,8 +716,8 @@ int moe_int8_quantize(const void* x, int M, int K, size_t x_stride, int dtype, i
  * Errors : MOE_EINVAL for null or misaligned pointers (16 bytes for a and b), a
  *          bad size, stride, dtype or flag, offsets without G or G without
  *          offsets, index without index_div >= 1, or fewer rows of a than M
- *          without index; MOE_EUNSUPPORTED for K > 131056, N > 2^24 or G >
- *          MOE_MAX_S.  M = 0 is valid and does nothing.  No workspace.
+ *          without index; MOE_EUNSUPPORTED for K > 131056, N > 2^24, M > 2^30
+ *          or G > MOE_MAX_S.  M = 0 is valid and does nothing.  No workspace.
  */
 typedef struct moe_int8_matmul_args {
   int M, N, K, G;

@@ -750,7 +750,8 @@ int matmul_status(const moe_int8_matmul_args* a) {
   if (!a) return MOE_EINVAL;
   if (a->M < 0 || a->N <= 0 || a->K <= 0 || a->G < 0 || a->a_rows < 0) return MOE_EINVAL;
   if (dtype_bytes(a->out_dtype) == 0 || (a->swiglu != 0 && a->swiglu != 1)) return MOE_EINVAL;
-  if (a->K > kMaxK || a->G > MOE_MAX_S || a->N > (1 << 24)) return MOE_EUNSUPPORTED;
+  if (a->K > kMaxK || a->G > MOE_MAX_S || a->N > (1 << 24) || a->M > (1 << 30))
+    return MOE_EUNSUPPORTED;
   if (a->M == 0) return MOE_OK;
   if (!a->a || !a->a_scale || !a->b || !a->b_scale || !a->out) return MOE_EINVAL;
   if ((a->G > 0) != (a->offsets != nullptr)) return MOE_EINVAL;

@@ -77,10 +77,13 @@ class RowOrder:
     """The order of a batch's T*k assignments by slot: perm (row -> assignment,
     int32, as moe_route wrote it, -1 behind the last row that is used) and its
     inverse pos [T, k] (assignment -> row, -1 for none), which moe_positions
-    computes unless the caller already has it."""
+    computes unless the caller already has it.  The tensors are used where they
+    are; a recorded dispatch or combine keeps copies for its backward pass, so a
+    later moe_route may write over them."""
 
     def __init__(self, perm: torch.Tensor, T: int, k: int, pos: torch.Tensor | None = None):
         self.T, self.k = int(T), int(k)
+        self._kept, self._own_pos = None, pos is None
         n = self.T * self.k
         if gpu_tensor(perm, "perm").dtype != torch.int32 or perm.numel() != n:
             raise ValueError(f"perm must hold T*k = {n} int32 values")
@@ -90,6 +93,17 @@ class RowOrder:
         elif gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or pos.numel() != n:
             raise ValueError(f"pos must hold T*k = {n} int32 values")
         self.pos = pos.contiguous()
+
+    def kept(self) -> "RowOrder":
+        """This order in tensors of its own, copied at the first call."""
+        if self._kept is None:
+            kept = object.__new__(RowOrder)
+            kept.T, kept.k, kept._own_pos = self.T, self.k, True
+            kept.perm = self.perm.clone()
+            kept.pos = self.pos if self._own_pos else self.pos.clone()
+            kept._kept = kept
+            self._kept = kept
+        return self._kept
 
 
 def _weights(weight, order: RowOrder, device):
@@ -145,7 +159,7 @@ class _Move(torch.autograd.Function):
     @staticmethod
     def forward(ctx, src, weight, order, there, back):
         w = _weights(weight, order, src.device)
-        ctx.order, ctx.back = order, back
+        ctx.order, ctx.back = order.kept(), back
         keep = src if weight is not None and ctx.needs_input_grad[1] else None
         ctx.save_for_backward(keep, w)
         ctx.wshape = None if weight is None else weight.shape

@@ -308,6 +308,16 @@ def layer_step(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, aren
     experts(buf, arena_ptr, slot_stride, stream)
 
 
+def layer_step_int8(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, int8_experts):
+    """One pass of the layer with its experts in 8-bit integers (int8.Int8Experts,
+    one group for each of buf's S slots): route with demand, the experts on the
+    rows of the bucketing, combine.  x [T, H] bf16; returns [T, H] bf16.  On the
+    current stream of x's device."""
+    route(buf, x, w_router, bias, expert_slot, torch.cuda.current_stream(x.device),
+          hist_row=hist_row)
+    return int8_experts.forward(x, buf.slot_offsets, buf.perm, buf.sel_weight)
+
+
 class SharedArena:
     """One arena shared by L layers: the [L][E] slot table and the [L][E]
     float64 demand history on the device, plus the re-plan flow.

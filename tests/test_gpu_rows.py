@@ -364,6 +364,31 @@ def test_another_stream_and_a_replayed_graph():
             assert torch.equal(a, b) and torch.equal(b, c)
 
 
+def test_backward_after_the_routing_buffers_are_reused():
+    """The next batch's routing writes over perm (and over a pos of the caller's)
+    before the backward pass of this one has run."""
+    from resident_expert_routing_amd import rows
+    T, H, k = 30, 100, 4
+    perm, w = batch(T, k, 6, seed=12, absent=0.4)
+    other, _ = batch(T, k, 6, seed=13)
+    for own_pos in (False, True):
+        buf = torch.from_numpy(perm).cuda()
+        pos = torch.from_numpy(reference(perm, T, k).astype(np.int32)).cuda()
+        order = rows.RowOrder(buf, T, k, pos=pos if own_pos else None)
+        wt = torch.from_numpy(w).cuda().requires_grad_()
+        x = rand((T, H), torch.float32, 1).requires_grad_()
+        g = rand((T, H), torch.float32, 2)
+        y = rows.dispatch(x, order, wt)
+        out = rows.combine(y, order, wt)
+        buf.copy_(torch.from_numpy(other))
+        pos.copy_(torch.from_numpy(reference(other, T, k).astype(np.int32)))
+        gy, gx = torch.autograd.grad(out, [y, x], g)
+        want = spread_ref(f64(g), perm, k, w.astype(np.float64))
+        close(gy, want, np.abs(want), 1, torch.float32, "drows")
+        total, mag = gather_ref(want, reference(perm, T, k), w.astype(np.float64))
+        close(gx, total, mag, k + 3, torch.float32, "dx")
+
+
 def test_two_calls_give_the_same_bits():
     from resident_expert_routing_amd import rows
     T, H, k = 257, 1024, 8

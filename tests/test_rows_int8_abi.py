@@ -155,6 +155,7 @@ def test_quantize_refusals(kw, code):
      B.MOE_EUNSUPPORTED),
     (dict(K=131057, a_stride=1 << 18, b_stride=1 << 18), B.MOE_EUNSUPPORTED),
     (dict(N=(1 << 24) + 1, out_stride=1 << 25), B.MOE_EUNSUPPORTED),
+    (dict(M=(1 << 30) + 1, a_rows=(1 << 30) + 1), B.MOE_EUNSUPPORTED),
     (dict(M=0, a=None, b=None, a_scale=None, b_scale=None, out=None, a_rows=0), B.MOE_OK),
 ])
 def test_matmul_refusals(kw, code):
