@@ -707,16 +707,38 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
   }
 }
 
+// Which tile, item by column, workgroup `id` has.  Consecutive workgroups go to
+// the 8 XCDs in turn.  With `blocks` an XCD gets blocks of kBlockItems x
+// kBlockCols tiles, as many as it has CUs, so that its L2 serves each row of a and
+// b several times; otherwise the columns of an item follow one another.  False
+// for a workgroup without a tile.
+constexpr int kBlockItems = 8, kBlockCols = 4;
+
+__device__ __forceinline__ bool tile_of(int64_t id, bool blocks, int items, int cols, int& item,
+                                        int& col) {
+  if (blocks) {
+    constexpr int kBlock = kBlockItems * kBlockCols;
+    const int64_t j = id >> 3, block = (j / kBlock) * 8 + (id & 7);
+    const int at = (int)(j % kBlock), across = (cols + kBlockCols - 1) / kBlockCols;
+    const int64_t i = block / across * kBlockItems + at / kBlockCols;
+    col = (int)(block % across) * kBlockCols + at % kBlockCols;
+    item = (int)i;
+    return i < items && col < cols;
+  }
+  item = (int)(id / cols), col = (int)(id % cols);
+  return id / cols < items;
+}
+
 template <typename E, bool GLU>
 __global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int R, int cols,
-                                                               int64_t first) {
+                                                               bool blocks, int64_t first) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (kMostRows + kColRows) * kStep];
   __shared__ Side side;
   const Pieces c = count_pieces(p, R);
-  const int64_t w = first + blockIdx.x;
-  if (w / cols >= c.total) return;
-  const Rows r = find_rows(p, c, (int)(w / cols), R);
-  const int n0 = (int)(w % cols) * (GLU ? kColRows / 2 : kColRows), rows = r.hi - r.lo;
+  int item, col;
+  if (!tile_of(first + blockIdx.x, blocks, c.total, cols, item, col)) return;
+  const Rows r = find_rows(p, c, item, R);
+  const int n0 = col * (GLU ? kColRows / 2 : kColRows), rows = r.hi - r.lo;
   if (rows <= 64 && r.all)
     tile<E, 2, 3, GLU, true>(p, r, n0, smem, side);
   else if (rows <= 64)
@@ -762,13 +784,22 @@ template <typename E>
 void launch_tiles(const MatArgs& p, bool glu, hipStream_t stream) {
   const int per = glu ? kColRows / 2 : kColRows, cols = (p.N + per - 1) / per;
   const int R = rows_of_tile(p, cols);
-  const int64_t tiles = max_items(p.M, p.G, R) * cols;
+  const int64_t items = max_items(p.M, p.G, R);
+  // Blocks pay where b is read by several tiles (65536 rows over 130 groups, gate/up
+  // 1642 us against 1605, down 910 against 891) and each XCD has many of them;
+  // weights that are read once gain nothing (16384 rows over 166 groups: 303).
+  const bool blocks = p.M > 128 * (int64_t)(p.G > 0 ? p.G : 1) && items * cols >= 2048;
+  const int64_t tiles =
+      blocks ? (int64_t)up_to((items + kBlockItems - 1) / kBlockItems *
+                                  ((cols + kBlockCols - 1) / kBlockCols), 8) *
+                   kBlockItems * kBlockCols
+             : items * cols;
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (glu)
-      int8_tiles<E, true><<<grid, kTWaves * kWave, 0, stream>>>(p, R, cols, first);
+      int8_tiles<E, true><<<grid, kTWaves * kWave, 0, stream>>>(p, R, cols, blocks, first);
     else
-      int8_tiles<E, false><<<grid, kTWaves * kWave, 0, stream>>>(p, R, cols, first);
+      int8_tiles<E, false><<<grid, kTWaves * kWave, 0, stream>>>(p, R, cols, blocks, first);
   }
 }
 
