@@ -755,16 +755,19 @@ __global__ __launch_bounds__(kTWaves* kWave, 2) void int8_tiles(MatArgs p, int R
     tile<E, 10, 2, GLU, false>(p, r, n0, smem, side);
 }
 
-// Most rows of a tile.  More rows share a load of b's, but a dense product may
-// then leave more of the 256 CUs without a tile in its last, or only, round: its
-// time goes as rounds * (rows + 256), the bytes that a tile loads in a stage
-// (512 x 4096 x 4096: 48 us with 320 rows, 21 with 64).
+// Most rows of a tile.  More rows share a load of b's, but a product of few tiles
+// may then leave more of the 256 CUs without one: its time goes as rounds *
+// (rows + 256), the bytes that a tile loads in a stage (512 x 4096 x 4096: 48 us
+// with 320 rows, 21 with 64).  Groups that fill the CUs get the most rows, so
+// that more of them read their weights once.
 int rows_of_tile(const MatArgs& p, int cols) {
-  if (p.G > 0) return kMostRows;
+  const int64_t groups = p.G > 0 ? (p.G < p.M ? p.G : p.M) : 0;
+  if (groups > 0 && (p.M / kMostRows + groups) * cols >= 256) return kMostRows;
   int best = kMostRows;
   int64_t least = INT64_MAX;
   for (int R : {320, 256, 192, 128, 64}) {
-    const int64_t cost = (((int64_t)p.M + R - 1) / R * cols + 255) / 256 * (R + 256);
+    const int64_t items = groups > 0 ? p.M / R + groups : ((int64_t)p.M + R - 1) / R;
+    const int64_t cost = (items * cols + 255) / 256 * (R + 256);
     if (cost < least) best = R, least = cost;
   }
   return best;
@@ -772,12 +775,19 @@ int rows_of_tile(const MatArgs& p, int cols) {
 
 // The streaming form is for products whose tiles, of 64 rows even, would leave
 // most CUs idle: at N = K = 4096, dense, 128 rows take 17 us against 20 in tiles
-// and 160 rows 24 against 20; with 4096 gate and up rows over groups of one row,
-// 8 groups take 31 us against 34 and 16 groups 54 against 51.
+// and 160 rows 24 against 20.  Groups of few rows are bound by their weights,
+// which more workgroups read faster: with 4096 gate and up rows, 8 groups of one
+// row take 30 us against 34 and 16 groups 54 against 51.
 bool few_tiles(const MatArgs& p, bool glu) {
   const int64_t cols = ((int64_t)p.N + (glu ? 127 : 255)) / (glu ? 128 : 256);
-  const int64_t items = p.G > 0 ? (p.G < p.M ? p.G : p.M) : (p.M + 63) / 64;
-  return items * cols < (p.G > 0 ? 192 : 48);
+  int64_t items = ((int64_t)p.M + 63) / 64;
+  bool thin = false;
+  if (p.G > 0) {
+    const int64_t groups = p.G < p.M ? p.G : p.M;
+    if (items < groups) items = groups;
+    thin = p.M < 4 * groups;
+  }
+  return items * cols < (thin ? 192 : 48);
 }
 
 template <typename E>
@@ -871,7 +881,7 @@ extern "C" MOE_EXPORT int moe_int8_matmul(const moe_int8_matmul_args* a, hipStre
   p.a_stride = a->a_stride, p.b_stride = a->b_stride, p.b_group_stride = a->b_group_stride;
   p.b_scale_group_stride = a->b_scale_group_stride, p.out_stride = a->out_stride;
   if (few_tiles(p, a->swiglu)) {
-    const int rows = p.M / (p.G > 0 ? p.G : 1);  // of a group, on average
+    const int rows = p.M / (p.G > 0 ? (p.G < p.M ? p.G : p.M) : 1);  // of a group, on average
     if (rows <= 32)
       launch_stream<1>(p, a->swiglu, stream);
     else if (rows <= 64)

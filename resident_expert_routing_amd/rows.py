@@ -90,8 +90,9 @@ class RowOrder:
         self.perm = perm.contiguous()
         if pos is None:
             pos = _positions(self.perm, self.T, self.k)
-        elif gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or pos.numel() != n:
-            raise ValueError(f"pos must hold T*k = {n} int32 values")
+        elif gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or \
+                pos.shape not in ((self.T, self.k), (n,)):
+            raise ValueError(f"pos must be int32 [{self.T}, {self.k}]")
         self.pos = pos.contiguous()
 
     def kept(self) -> "RowOrder":
@@ -110,8 +111,9 @@ def _weights(weight, order: RowOrder, device):
     if weight is None:
         return None
     gpu_tensor(weight, "weight", device)
-    if weight.dtype != torch.float32 or weight.numel() != order.T * order.k:
-        raise ValueError(f"weight must hold [{order.T}, {order.k}] float32 values")
+    if weight.dtype != torch.float32 or \
+            weight.shape not in ((order.T, order.k), (order.T * order.k,)):
+        raise ValueError(f"weight must be float32 [{order.T}, {order.k}]")
     return weight.contiguous()
 
 

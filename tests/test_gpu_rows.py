@@ -301,12 +301,15 @@ def test_refusals():
         rows.RowOrder(perm, 4, 3)
     with pytest.raises(ValueError):
         rows.RowOrder(perm.long(), 4, 2)
+    with pytest.raises(ValueError):
+        rows.RowOrder(perm, 4, 2, pos=perm.view(2, 4))
     order = rows.RowOrder(torch.arange(8, dtype=torch.int32, device="cuda"), 4, 2)
     for x, w in ((torch.zeros(5, 16, device="cuda"), None),
                  (torch.zeros(4, 16), None),
                  (torch.zeros(4, 16, device="cuda", dtype=torch.float64), None),
                  (torch.zeros(4, 16, device="cuda"), torch.zeros(4, 2)),
                  (torch.zeros(4, 16, device="cuda"), torch.zeros(3, 2, device="cuda")),
+                 (torch.zeros(4, 16, device="cuda"), torch.zeros(2, 4, device="cuda")),
                  (torch.zeros(4, 16, device="cuda"),
                   torch.zeros(4, 2, device="cuda", dtype=torch.bfloat16)),
                  (torch.zeros(16, device="cuda"), None)):
