@@ -7,10 +7,15 @@
 //   gather   token[t]    = sum_j w[t,j] * row[pos[t,j]]   (combine; dispatch's backward)
 // and the weight's gradient is the dot product of the row with the token row
 // on the other side.  So two kernel forms serve all four calls.  All of them
-// are token-major: a token row is read or written once while its k rows pass,
-// where a row-major walk would read each token row k times, from rows far
-// apart.  Sums run over ascending j in float32 in one thread, dot products in
-// a fixed tree: no atomics, the same result on every call.
+// are token-major: a token row is read or written once while its k rows pass (a
+// row-major dispatch, each row fetching its token's, was correct and slower: 8192
+// tokens of 6144, top-8, 231 us against 183).  Sums run over ascending j in
+// float32 in one thread, dot products in a fixed tree: no atomics, the same
+// result on every call.
+//
+// All are bound by memory.  For 8192 tokens of 6144 bf16, top-8 (65536 rows, 805
+// MB): spread 183 us (906 MB, 4.9 TB/s), gather 156 us (5.8 TB/s), spread with
+// dot products 345 us (1.7 GB, 5.0 TB/s).  A copy of 1 GiB runs at 5.1 TB/s.
 #include "elements.hpp"
 
 using namespace moe;

@@ -100,8 +100,12 @@ class RowOrder:
         if self._kept is None:
             kept = object.__new__(RowOrder)
             kept.T, kept.k, kept._own_pos = self.T, self.k, True
-            kept.perm = self.perm.clone()
-            kept.pos = self.pos if self._own_pos else self.pos.clone()
+            if self._own_pos:
+                kept.perm, kept.pos = self.perm.clone(), self.pos
+            else:
+                n = self.T * self.k
+                both = torch.cat((self.perm.view(-1), self.pos.view(-1)))
+                kept.perm, kept.pos = both[:n], both[n:].view(self.T, self.k)
             kept._kept = kept
             self._kept = kept
         return self._kept
