@@ -595,12 +595,16 @@ int moe_history_scale(double* hist, size_t n, double factor, hipStream_t stream)
  * moe_positions -- the inverse of perm: pos[perm[p]] = p, and pos[a] = -1 for
  * the assignments that perm does not name (padded picks).  An assignment named
  * twice gets the larger p.
- * Input  : perm [T*k] int32.   Output : pos [T][k] int32 (must not alias perm).
+ * Input  : perm [T*k] int32.
+ * Outputs: pos [T][k] int32; perm_copy [T*k] int32 (nullable): perm as it was, for
+ *          a backward pass that runs after perm has been written over.  Neither
+ *          may alias perm.
  * Errors : MOE_EINVAL for null or misaligned (4-byte) pointers, T < 0 or
  *          k <= 0; MOE_EUNSUPPORTED for k > MOE_MAX_K or T*k > 2^31 - 1.
  *          T = 0 is valid and does nothing.
  */
-int moe_positions(const int32_t* perm, int T, int k, int32_t* pos, hipStream_t stream);
+int moe_positions(const int32_t* perm, int T, int k, int32_t* pos, int32_t* perm_copy,
+                  hipStream_t stream);
 
 /*
  * moe_dispatch -- src [T][H] token rows, dst [T*k][H] rows:

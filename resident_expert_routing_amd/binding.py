@@ -168,7 +168,7 @@ def load() -> ctypes.CDLL:
     lib.moe_boot_plan.restype = i
     lib.moe_history_scale.argtypes = [vp, sz, ctypes.c_double, vp]
     lib.moe_history_scale.restype = i
-    lib.moe_positions.argtypes = [vp, i, i, vp, vp]
+    lib.moe_positions.argtypes = [vp, i, i, vp, vp, vp]
     lib.moe_positions.restype = i
     for name in ("moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward"):
         getattr(lib, name).argtypes = [ctypes.POINTER(RowsArgs), vp]
@@ -377,8 +377,9 @@ def moe_history_scale(hist, n, factor, stream=None) -> int:
     return int(load().moe_history_scale(_ptr(hist), int(n), float(factor), _stream(stream)))
 
 
-def moe_positions(perm, T, k, pos, stream=None) -> int:
-    return int(load().moe_positions(_ptr(perm), int(T), int(k), _ptr(pos), _stream(stream)))
+def moe_positions(perm, T, k, pos, perm_copy=None, stream=None) -> int:
+    return int(load().moe_positions(_ptr(perm), int(T), int(k), _ptr(pos), _ptr(perm_copy),
+                                    _stream(stream)))
 
 
 def _rows_args(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight, perm=None,

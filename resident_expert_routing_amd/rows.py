@@ -17,7 +17,6 @@ from __future__ import annotations
 import functools
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -68,47 +67,43 @@ def row_major(t: torch.Tensor) -> tuple[torch.Tensor, int]:
 
 @on_its_device
 def _positions(perm, T, k):
-    pos = torch.empty((T, k), dtype=torch.int32, device=perm.device)
-    B.check(B.moe_positions(perm, T, k, pos, stream_of(perm)), "moe_positions")
-    return pos
+    both = torch.empty((2, T, k), dtype=torch.int32, device=perm.device)
+    pos, copy = both.unbind()
+    B.check(B.moe_positions(perm, T, k, pos, copy, stream_of(perm)), "moe_positions")
+    return pos, copy
 
 
 class RowOrder:
     """The order of a batch's T*k assignments by slot: perm (row -> assignment,
     int32, as moe_route wrote it, -1 behind the last row that is used) and its
-    inverse pos [T, k] (assignment -> row, -1 for none), which moe_positions
-    computes unless the caller already has it.  The tensors are used where they
-    are; a recorded dispatch or combine keeps copies for its backward pass, so a
-    later moe_route may write over them."""
+    inverse pos [T, k] (assignment -> row, -1 for none).  moe_positions computes
+    pos and copies perm, so a later moe_route may write over the caller's; a pos
+    that the caller already has is taken as it is, with perm, and both are
+    copied when a dispatch or combine is recorded for its backward pass."""
 
     def __init__(self, perm: torch.Tensor, T: int, k: int, pos: torch.Tensor | None = None):
         self.T, self.k = int(T), int(k)
-        self._kept, self._own_pos = None, pos is None
         n = self.T * self.k
         if gpu_tensor(perm, "perm").dtype != torch.int32 or perm.numel() != n:
             raise ValueError(f"perm must hold T*k = {n} int32 values")
-        self.perm = perm.contiguous()
-        if pos is None:
-            pos = _positions(self.perm, self.T, self.k)
-        elif gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or \
+        self.own = pos is None
+        if self.own:
+            self.pos, self.perm = _positions(perm.contiguous(), self.T, self.k)
+            return
+        if gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or \
                 pos.shape not in ((self.T, self.k), (n,)):
             raise ValueError(f"pos must be int32 [{self.T}, {self.k}]")
-        self.pos = pos.contiguous()
+        self.pos, self.perm = pos.contiguous(), perm.contiguous()
 
     def kept(self) -> "RowOrder":
-        """This order in tensors of its own, copied at the first call."""
-        if self._kept is None:
-            kept = object.__new__(RowOrder)
-            kept.T, kept.k, kept._own_pos = self.T, self.k, True
-            if self._own_pos:
-                kept.perm, kept.pos = self.perm.clone(), self.pos
-            else:
-                n = self.T * self.k
-                both = torch.cat((self.perm.view(-1), self.pos.view(-1)))
-                kept.perm, kept.pos = both[:n], both[n:].view(self.T, self.k)
-            kept._kept = kept
-            self._kept = kept
-        return self._kept
+        """The order in tensors of its own."""
+        if self.own:
+            return self
+        order = object.__new__(RowOrder)
+        order.T, order.k, order.own = self.T, self.k, True
+        both = torch.cat((self.pos.view(-1), self.perm.view(-1)))
+        order.pos, order.perm = both.view(2, self.T, self.k).unbind()
+        return order
 
 
 def _weights(weight, order: RowOrder, device):
@@ -166,18 +161,21 @@ class _Move(torch.autograd.Function):
     def forward(ctx, src, weight, order, there, back):
         w = _weights(weight, order, src.device)
         ctx.order, ctx.back = order.kept(), back
-        keep = src if weight is not None and ctx.needs_input_grad[1] else None
-        ctx.save_for_backward(keep, w)
-        ctx.wshape = None if weight is None else weight.shape
+        wants = weight is not None and ctx.needs_input_grad[1]
+        ctx.save_for_backward(src if wants else None, w)
+        ctx.wshape = weight.shape if wants else None
         return there(src, order, w)[0]
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad):
+        if torch.is_grad_enabled():
+            raise RuntimeError("dispatch and combine have no second derivative: take their "
+                               "gradient without create_graph")
         src, w = ctx.saved_tensors
         dsrc, dw = ctx.back(grad, ctx.order, w, src)
-        return (dsrc if ctx.needs_input_grad[0] else None,
-                dw.view(ctx.wshape) if dw is not None else None, None, None, None)
+        if dw is not None:
+            dw = dw.view(ctx.wshape)
+        return dsrc, dw, None, None, None
 
 
 def _move(src, weight, order, there, back):

@@ -118,6 +118,7 @@ def test_positions(T, k, S, absent):
     perm, _ = batch(T, k, S, seed=T + k, absent=absent)
     order = rows.RowOrder(torch.from_numpy(perm).cuda(), T, k)
     assert np.array_equal(order.pos.cpu().numpy(), reference(perm, T, k))
+    assert np.array_equal(order.perm.cpu().numpy().reshape(-1), perm)
 
 
 def test_positions_of_foreign_values():
@@ -292,6 +293,16 @@ def test_empty_batch_and_absent_everything():
     z.sum().backward()
     for t in (y, z, x.grad, w.grad):
         assert float(t.detach().abs().max()) == 0
+
+
+def test_no_second_derivative():
+    from resident_expert_routing_amd import rows
+    order = rows.RowOrder(torch.arange(8, dtype=torch.int32, device="cuda"), 4, 2)
+    x = rand((4, 16), torch.float32, 1).requires_grad_()
+    w = torch.ones(4, 2, device="cuda", requires_grad=True)
+    out = rows.combine(rows.dispatch(x, order), order, w)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(out.sum(), [x, w], create_graph=True)
 
 
 def test_refusals():

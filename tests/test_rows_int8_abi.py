@@ -18,6 +18,7 @@ BIG = 1 << 30
     (dict(pos=None), B.MOE_EINVAL),
     (dict(perm=FAKE + 2), B.MOE_EINVAL),
     (dict(pos=FAKE + 1), B.MOE_EINVAL),
+    (dict(perm_copy=FAKE + 2), B.MOE_EINVAL),
     (dict(T=-1), B.MOE_EINVAL),
     (dict(k=0), B.MOE_EINVAL),
     (dict(k=33), B.MOE_EUNSUPPORTED),
