@@ -66,7 +66,7 @@ def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = No
         scale = torch.empty(M, dtype=torch.float32, device=x.device)
     else:
         q, scale = out
-        gpu_tensor(q, "q", x.device), gpu_tensor(scale, "scale", x.device)
+        gpu_tensor(q, "q", x.get_device()), gpu_tensor(scale, "scale", x.get_device())
         if q.dtype != torch.int8 or q.shape != x.shape or not _laid_out(q):
             raise ValueError("q must be int8 [M, K] with rows at multiples of 16 bytes")
         if scale.dtype != torch.float32 or scale.numel() != M or not scale.is_contiguous():
@@ -104,7 +104,7 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     rows at multiples of 16 bytes (quantize and pad_rows do); a is copied if it
     is not.
     """
-    dev = gpu_tensor(a, "a").device
+    dev = gpu_tensor(a, "a").get_device()
     for t, what, dt in ((a_scale, "a_scale", torch.float32), (b, "b", torch.int8),
                         (b_scale, "b_scale", torch.float32), (offsets, "offsets", torch.int32),
                         (index, "index", torch.int32)):
@@ -136,7 +136,7 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     if out is None:
         if out_dtype not in DTYPES:
             raise ValueError(f"out_dtype must be bfloat16, float16 or float32, not {out_dtype}")
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
     elif gpu_tensor(out, "out", dev).shape != (M, N):
         raise ValueError(f"out must have shape [{M}, {N}]")
     od = dtype_of(out, "out")

@@ -20,23 +20,25 @@ import torch
 
 from . import binding as B
 
+_lib = B.load()
+
 DTYPES = {torch.bfloat16: B.MOE_DT_BF16, torch.float16: B.MOE_DT_FP16,
           torch.float32: B.MOE_DT_FP32}
 
 
 def stream_of(t: torch.Tensor) -> int:
     """The handle of the current stream of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def on_its_device(call):
     """`call`, with the device of its first argument (a tensor) the current one."""
     @functools.wraps(call)
-    def run(t, *args, **kwargs):
-        if t.device.index == torch.cuda.current_device():
-            return call(t, *args, **kwargs)
+    def run(t, *args):
+        if t.get_device() == torch.cuda.current_device():
+            return call(t, *args)
         with torch.cuda.device(t.device):
-            return call(t, *args, **kwargs)
+            return call(t, *args)
     return run
 
 
@@ -47,11 +49,12 @@ def dtype_of(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def gpu_tensor(t, what: str, device=None) -> torch.Tensor:
+def gpu_tensor(t, what: str, device: int | None = None) -> torch.Tensor:
+    """t, a tensor on a GPU (on GPU `device`, where that is given)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a tensor on a GPU")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the rows on {device}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}, other tensors on GPU {device}")
     return t
 
 
@@ -86,11 +89,12 @@ class RowOrder:
         n = self.T * self.k
         if gpu_tensor(perm, "perm").dtype != torch.int32 or perm.numel() != n:
             raise ValueError(f"perm must hold T*k = {n} int32 values")
+        self.device = perm.get_device()
         self.own = pos is None
         if self.own:
             self.pos, self.perm = _positions(perm.contiguous(), self.T, self.k)
             return
-        if gpu_tensor(pos, "pos", perm.device).dtype != torch.int32 or \
+        if gpu_tensor(pos, "pos", self.device).dtype != torch.int32 or \
                 pos.shape not in ((self.T, self.k), (n,)):
             raise ValueError(f"pos must be int32 [{self.T}, {self.k}]")
         self.pos, self.perm = pos.contiguous(), perm.contiguous()
@@ -100,58 +104,63 @@ class RowOrder:
         if self.own:
             return self
         order = object.__new__(RowOrder)
-        order.T, order.k, order.own = self.T, self.k, True
+        order.T, order.k, order.device, order.own = self.T, self.k, self.device, True
         both = torch.cat((self.pos.view(-1), self.perm.view(-1)))
         order.pos, order.perm = both.view(2, self.T, self.k).unbind()
         return order
 
 
-def _weights(weight, order: RowOrder, device):
+def _weights(weight, order: RowOrder):
     if weight is None:
         return None
-    gpu_tensor(weight, "weight", device)
+    gpu_tensor(weight, "weight", order.device)
     if weight.dtype != torch.float32 or \
             weight.shape not in ((order.T, order.k), (order.T * order.k,)):
         raise ValueError(f"weight must be float32 [{order.T}, {order.k}]")
     return weight.contiguous()
 
 
-def _check(src: torch.Tensor, n: int, order: RowOrder, what: str) -> None:
-    gpu_tensor(src, what, order.perm.device)
-    if src.dim() != 2 or src.shape[0] != n:
-        raise ValueError(f"{what} must have shape [{n}, H], not {list(src.shape)}")
+# The two moves.  Small batches are bound by what happens here on the host, so
+# the C entries are called with plain numbers.
+def _move_rows(entry, what, n, src, order, weight, perm, other=None):
+    """entry(src) -> rows or token rows [n, H]; with `other` (the forward input)
+    the weights' gradient too."""
+    if order.device != torch.cuda.current_device():
+        with torch.cuda.device(order.device):
+            return _move_rows(entry, what, n, src, order, weight, perm, other)
+    dt = dtype_of(src, "rows")
+    src, stride = row_major(src)
+    H, T, k = src.shape[1], order.T, order.k
+    dst = torch.empty((n, H), dtype=src.dtype, device=src.device)
+    dw, dwp, op, ostride = None, None, None, 0
+    if other is not None:
+        other, ostride = row_major(other)
+        dw = torch.empty((T, k), dtype=torch.float32, device=src.device)
+        dwp, op = dw.data_ptr(), other.data_ptr()
+    st = entry(B.RowsArgs(T, H, k, dt, None if perm is None else perm.data_ptr(),
+                          order.pos.data_ptr(), None if weight is None else weight.data_ptr(),
+                          src.data_ptr(), stride, dst.data_ptr(), H, op, ostride, dwp),
+               torch._C._cuda_getCurrentRawStream(order.device))
+    if st != B.MOE_OK:
+        raise B.MoeError(st, what)
+    return dst, dw
 
 
-@on_its_device
 def _spread(src, order, weight, rows=None):
     """Token rows to rows; with `rows` (the forward rows) the weights' gradient too."""
-    dt, (src, stride), H, T, k = dtype_of(src, "rows"), row_major(src), src.shape[1], order.T, order.k
-    dst = torch.empty((T * k, H), dtype=src.dtype, device=src.device)
     if rows is None:
-        B.check(B.moe_dispatch(T, H, k, dt, order.pos, src, stride, dst, H, weight, order.perm,
-                               stream_of(src)), "moe_dispatch")
-        return dst, None
-    rows, rstride = row_major(rows)
-    dw = torch.empty((T, k), dtype=torch.float32, device=src.device)
-    B.check(B.moe_combine_backward(T, H, k, dt, order.pos, src, stride, dst, H, weight, order.perm,
-                                   rows, rstride, dw, stream_of(src)), "moe_combine_backward")
-    return dst, dw
+        return _move_rows(_lib.moe_dispatch, "moe_dispatch", order.T * order.k, src, order, weight,
+                          order.perm)
+    return _move_rows(_lib.moe_combine_backward, "moe_combine_backward", order.T * order.k, src,
+                      order, weight, order.perm, rows)
 
 
-@on_its_device
 def _gather(src, order, weight, tokens=None):
     """Rows to token rows; with `tokens` (the forward token rows) the weights' gradient too."""
-    dt, (src, stride), H, T, k = dtype_of(src, "rows"), row_major(src), src.shape[1], order.T, order.k
-    dst = torch.empty((T, H), dtype=src.dtype, device=src.device)
     if tokens is None:
-        B.check(B.moe_combine(T, H, k, dt, order.pos, src, stride, dst, H, weight,
-                              stream_of(src)), "moe_combine")
-        return dst, None
-    tokens, tstride = row_major(tokens)
-    dw = torch.empty((T, k), dtype=torch.float32, device=src.device)
-    B.check(B.moe_dispatch_backward(T, H, k, dt, order.pos, src, stride, dst, H, weight, tokens,
-                                    tstride, dw, stream_of(src)), "moe_dispatch_backward")
-    return dst, dw
+        return _move_rows(_lib.moe_combine, "moe_combine", order.T, src, order, weight, None)
+    return _move_rows(_lib.moe_dispatch_backward, "moe_dispatch_backward", order.T, src, order,
+                      weight, None, tokens)
 
 
 class _Move(torch.autograd.Function):
@@ -159,7 +168,7 @@ class _Move(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, src, weight, order, there, back):
-        w = _weights(weight, order, src.device)
+        w = _weights(weight, order)
         ctx.order, ctx.back = order.kept(), back
         wants = weight is not None and ctx.needs_input_grad[1]
         ctx.save_for_backward(src if wants else None, w)
@@ -182,7 +191,13 @@ def _move(src, weight, order, there, back):
     if torch.is_grad_enabled() and (src.requires_grad
                                     or (weight is not None and weight.requires_grad)):
         return _Move.apply(src, weight, order, there, back)
-    return there(src, order, _weights(weight, order, src.device))[0]
+    return there(src, order, _weights(weight, order))[0]
+
+
+def _check(src: torch.Tensor, n: int, order: RowOrder, what: str) -> None:
+    gpu_tensor(src, what, order.device)
+    if src.dim() != 2 or src.shape[0] != n:
+        raise ValueError(f"{what} must have shape [{n}, H], not {list(src.shape)}")
 
 
 def dispatch(x: torch.Tensor, order: RowOrder, weight: torch.Tensor | None = None) -> torch.Tensor:
