@@ -583,7 +583,8 @@ int moe_history_scale(double* hist, size_t n, double factor, hipStream_t stream)
  * Assignment a = t*k + j is pick j of token t; row p of a "rows" array
  * [T*k][H] belongs to assignment perm[p].  perm and weight are moe_route's perm
  * and sel_weight (or arrays of that form: perm names every assignment at most
- * once; entries outside [0, T*k) name none).
+ * once; entries outside [0, T*k) name none), pos is what moe_positions makes of
+ * perm.
  */
 
 /* Element types (moe_rows_args.dtype, moe_int8_quantize, moe_int8_matmul). */

@@ -17,13 +17,16 @@ from . import binding as B
 from .rows import (DTYPES, RowOrder, combine, dtype_of, gpu_tensor, on_its_device, row_major,
                    stream_of)
 
+_lib = B.load()
+
 
 def _rows16(*shape, device) -> torch.Tensor:
     """An int8 tensor whose rows (last axis) start at multiples of 16 bytes."""
     width = B.moe_int8_row_bytes(shape[-1])
     if width == 0:
         raise ValueError(f"rows of {shape[-1]} elements")
-    return torch.empty(*shape[:-1], width, dtype=torch.int8, device=device)[..., :shape[-1]]
+    q = torch.empty(*shape[:-1], width, dtype=torch.int8, device=device)
+    return q if width == shape[-1] else q[..., :shape[-1]]
 
 
 def pad_rows(q: torch.Tensor) -> torch.Tensor:
@@ -54,10 +57,13 @@ def _laid_out(q: torch.Tensor) -> bool:
 def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
     """x [M, K] (bf16, fp16 or fp32) -> (q int8 [M, K], scale float32 [M]) with
     x ~= q * scale[:, None]; the scale is the row's largest magnitude over 127.
-    `out`: a pair that an earlier call of the same shape returned, to be filled."""
+    `out`: a pair that an earlier call of the same shape returned, to be filled.
+    There is no gradient: an x that wants one is refused."""
     gpu_tensor(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must have shape [M, K], not {list(x.shape)}")
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("quantize has no gradient: detach x, or call it under torch.no_grad()")
     dt = dtype_of(x, "x")
     M, K = x.shape
     x, stride = row_major(x)
@@ -71,13 +77,24 @@ def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = No
             raise ValueError("q must be int8 [M, K] with rows at multiples of 16 bytes")
         if scale.dtype != torch.float32 or scale.numel() != M or not scale.is_contiguous():
             raise ValueError("scale must hold M contiguous float32 values")
-    _quantize(x, M, K, stride, dt, q, _stride(q, 0), scale)
+    _quantize(x, M, K, stride, dt, q.data_ptr(), _stride(q, 0), scale.data_ptr())
     return q, scale
 
 
 @on_its_device
 def _quantize(x, *args):
-    B.check(B.moe_int8_quantize(x, *args, stream_of(x)), "moe_int8_quantize")
+    st = _lib.moe_int8_quantize(x.data_ptr(), *args, stream_of(x))
+    if st != B.MOE_OK:
+        raise B.MoeError(st, "moe_int8_quantize")
+
+
+def _pointer(t, what: str, dtype: torch.dtype, device: int):
+    """The address of a tensor of that type on that GPU; None for None."""
+    if t is None:
+        return None
+    if gpu_tensor(t, what, device).dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    return t.data_ptr()
 
 
 def _stride(q: torch.Tensor, axis: int) -> int:
@@ -105,13 +122,10 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     is not.
     """
     dev = gpu_tensor(a, "a").get_device()
-    for t, what, dt in ((a_scale, "a_scale", torch.float32), (b, "b", torch.int8),
-                        (b_scale, "b_scale", torch.float32), (offsets, "offsets", torch.int32),
-                        (index, "index", torch.int32)):
-        if t is not None and gpu_tensor(t, what, dev).dtype != dt:
-            raise ValueError(f"{what} must be {dt}")
     if a.dtype != torch.int8 or a.dim() != 2:
         raise ValueError("a must be int8 [rows, K]")
+    b_at = _pointer(b, "b", torch.int8, dev)
+    bs_at = _pointer(b_scale, "b_scale", torch.float32, dev)
     a_rows, K = a.shape
     G = 0 if offsets is None else offsets.numel() - 1
     if b.dim() != (3 if offsets is not None else 2) or b.shape[-1] != K or \
@@ -128,9 +142,9 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     if not _laid_out(b):
         raise ValueError("b's rows must start at multiples of 16 bytes: lay it out with pad_rows")
     a, a_scale = pad_rows(a), a_scale.contiguous()
-    M = a_rows if index is None else index.numel()
+    M = a_rows
     if index is not None:
-        index = index.contiguous()
+        index, M = index.contiguous(), index.numel()
     if offsets is not None:
         offsets = offsets.contiguous()
     if out is None:
@@ -142,17 +156,21 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     od = dtype_of(out, "out")
     if (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
         raise ValueError("the rows of out must be contiguous and apart")
-    _matmul(a, M, N, K, G, swiglu, a_rows, _stride(a, 0), a_scale, index, index_div, offsets, b,
-            _stride(b, -2), _stride(b, 0) if G else 0, b_scale,
-            (b_scale.stride(0) if G > 1 else wide) if G else 0, out, out.stride(0) if M > 1 else N,
-            od)
+    _matmul(a, B.Int8MatmulArgs(
+        M, N, K, G, 1 if swiglu else 0, a_rows, a.data_ptr(), _stride(a, 0),
+        _pointer(a_scale, "a_scale", torch.float32, dev),
+        _pointer(index, "index", torch.int32, dev), int(index_div),
+        _pointer(offsets, "offsets", torch.int32, dev), b_at, _stride(b, -2),
+        _stride(b, 0) if G else 0, bs_at, (b_scale.stride(0) if G > 1 else wide) if G else 0,
+        out.data_ptr(), out.stride(0) if M > 1 else N, od))
     return out
 
 
 @on_its_device
-def _matmul(a, M, N, K, G, swiglu, a_rows, *args):
-    B.check(B.moe_int8_matmul(M, N, K, G, swiglu, a_rows, a, *args, stream_of(a)),
-            "moe_int8_matmul")
+def _matmul(a, args):
+    st = _lib.moe_int8_matmul(args, stream_of(a))
+    if st != B.MOE_OK:
+        raise B.MoeError(st, "moe_int8_matmul")
 
 
 class Int8Experts:

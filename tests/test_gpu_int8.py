@@ -12,9 +12,9 @@ A product's integer sum is exact; it is rounded to float32 and scaled twice:
 type.  With SwiGLU the gate value g carries that error d = 3 * 2^-24 |g|, which
 silu, of slope at most 1.1, turns into 1.1 d |u|; exp(-g) is taken as 2^(-g
 log2 e) with one rounding of the argument, |g| * 1.45 * 2^-24 of the result's
-size, and 2 ulp of the instruction; a sum, a quotient and two products (u's own
-error is 3 * 2^-24) follow: together at most (1.5 |g| + 12) * 2^-24 * |silu(g) u|
-more."""
+size, and 2 units in the last place of the instruction (4 * 2^-24); a sum (1), a
+reciprocal to one unit (2) and two products (2) follow, and u's own error (3):
+together at most (1.5 |g| + 12) * 2^-24 * |silu(g) u| more."""
 import numpy as np
 import pytest
 import torch
@@ -120,6 +120,8 @@ def test_quantize_strides_and_given_outputs():
         int8.quantize(x, (room[:, 8:108], out[1]))
     with pytest.raises(ValueError):
         int8.quantize(x.double())
+    with pytest.raises(ValueError, match="gradient"):
+        int8.quantize(x.clone().requires_grad_())
 
 
 def ints(shape, seed, low=-127):
@@ -362,6 +364,14 @@ def test_layouts():
         int8.matmul(a, sa, int8.pad_rows(b[0]), sb[0], out_dtype=torch.float64)
     with pytest.raises(ValueError):
         int8.matmul(a, sa, int8.pad_rows(b[0][:71]), sb[0][:71], swiglu=True)
+    with pytest.raises(ValueError):
+        int8.matmul(a, sa.double(), int8.pad_rows(b[0]), sb[0])
+    with pytest.raises(ValueError):
+        int8.matmul(a, sa, int8.pad_rows(b), sb, offsets=offsets.long())
+    with pytest.raises(ValueError):
+        int8.matmul(a, sa, int8.pad_rows(b), sb, offsets=offsets, index=offsets.cpu())
+    with pytest.raises(ValueError):
+        int8.matmul(a, sa, int8.pad_rows(b), sb, offsets=offsets, out=a.float())
 
 
 def test_scales_that_are_nan_reach_only_their_row():
