@@ -250,6 +250,19 @@ def test_tiled_rows_by_index(swiglu, dtype):
               swiglu=swiglu, dtype=dtype, seed=G)
 
 
+@pytest.mark.parametrize("G,M", [(257, 40), (300, 41), (8192, 40), (8192, 9000), (256, 700)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_groups(G, M, swiglu):
+    """More groups than a wave keeps in registers (256), to the most there can be;
+    most of them empty, the first and the last in use."""
+    rng = np.random.default_rng(G + M)
+    sizes = np.zeros(G, int)
+    sizes[0], sizes[-1] = 3, 2
+    for g in rng.integers(0, G, M - 5):
+        sizes[g] += 1
+    check(M, 64, 80, G=G, offsets=np.concatenate([[0], np.cumsum(sizes)]), swiglu=swiglu, seed=G)
+
+
 @pytest.mark.parametrize("M,N,K", [(160, 4200, 200), (257, 3333, 129), (513, 2570, 64),
                                    (1030, 900, 333), (3200, 300, 96), (2081, 1030, 1000)])
 @pytest.mark.parametrize("swiglu", [False, True])
