@@ -6,11 +6,13 @@
     out = combine(rows, order, buf.sel_weight)  # [T, H]
 
 Both take bf16, fp16 or fp32 rows and float32 weights, and pass gradients to the
-rows and to the weights (moe_dispatch_backward, moe_combine_backward).  They run
-on the current stream of the rows' device and synchronise nothing.  A gradient
-captured into a graph is taken with torch.autograd.grad, or with no graph made
-outside the capture alive over the same leaves: torch ties a leaf's accumulation
-to the stream that first used it.
+rows and to the weights (moe_dispatch_backward, moe_combine_backward).  A call
+that is recorded keeps copies of the order and of the weights, since the next
+moe_route may write over both before the backward pass; rows that the weights'
+gradient needs are kept as they are.  Calls run on the current stream of the
+rows' device and synchronise nothing.  A gradient captured into a graph is taken
+with torch.autograd.grad, or with no graph made outside the capture alive over
+the same leaves: torch ties a leaf's accumulation to the stream that first used it.
 """
 from __future__ import annotations
 
@@ -171,7 +173,8 @@ class _Move(torch.autograd.Function):
         w = _weights(weight, order)
         ctx.order, ctx.back = order.kept(), back
         wants = weight is not None and ctx.needs_input_grad[1]
-        ctx.save_for_backward(src if wants else None, w)
+        kept = w.clone() if w is not None and w.data_ptr() == weight.data_ptr() else w
+        ctx.save_for_backward(src if wants else None, kept)
         ctx.wshape = weight.shape if wants else None
         return there(src, order, w)[0]
 

@@ -403,6 +403,28 @@ def test_backward_after_the_routing_buffers_are_reused():
         close(gx, total, mag, k + 3, torch.float32, "dx")
 
 
+@pytest.mark.parametrize("learned", [False, True])
+def test_backward_after_the_weights_are_overwritten(learned):
+    """The next batch's routing writes over sel_weight, unseen by torch, before the
+    backward pass of this one has run."""
+    from resident_expert_routing_amd import rows
+    T, H, k = 30, 100, 4
+    perm, w = batch(T, k, 6, seed=14, absent=0.4)
+    order = rows.RowOrder(torch.from_numpy(perm).cuda(), T, k)
+    wt = torch.from_numpy(w).cuda().requires_grad_(learned)
+    x = rand((T, H), torch.float32, 1).requires_grad_()
+    y = rand((T * k, H), torch.float32, 3).requires_grad_()
+    g, gr = rand((T, H), torch.float32, 2), rand((T * k, H), torch.float32, 4)
+    r, out = rows.dispatch(x, order, wt), rows.combine(y, order, wt)
+    wt.data.fill_(7.0)
+    gx = torch.autograd.grad(r, x, gr)[0]
+    gy = torch.autograd.grad(out, y, g)[0]
+    want = spread_ref(f64(g), perm, k, w.astype(np.float64))
+    close(gy, want, np.abs(want), 1, torch.float32, "drows")
+    total, mag = gather_ref(f64(gr), reference(perm, T, k), w.astype(np.float64))
+    close(gx, total, mag, k + 3, torch.float32, "dx")
+
+
 def test_two_calls_give_the_same_bits():
     from resident_expert_routing_amd import rows
     T, H, k = 257, 1024, 8
