@@ -54,20 +54,33 @@ def _laid_out(q: torch.Tensor) -> bool:
     return q.storage_offset() + need <= q.untyped_storage().nbytes()
 
 
+def _no_gradient(call: str, *tensors) -> None:
+    for t in tensors:
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{call} has no gradient: detach its tensors, or call it under "
+                             "torch.no_grad()")
+
+
+def _written(*tensors) -> None:
+    """Counts a kernel's write to tensors of the caller's as a change, so that a
+    backward pass that kept what they held before is refused."""
+    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+
+
 def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
     """x [M, K] (bf16, fp16 or fp32) -> (q int8 [M, K], scale float32 [M]) with
     x ~= q * scale[:, None]; the scale is the row's largest magnitude over 127.
     `out`: a pair that an earlier call of the same shape returned, to be filled.
-    There is no gradient: an x that wants one is refused."""
+    There is no gradient: tensors that want one are refused."""
     gpu_tensor(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must have shape [M, K], not {list(x.shape)}")
-    if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError("quantize has no gradient: detach x, or call it under torch.no_grad()")
+    _no_gradient("quantize", x, *(out or ()))
     dt = dtype_of(x, "x")
     M, K = x.shape
     x, stride = row_major(x)
-    if out is None:
+    given = out is not None
+    if not given:
         q = _rows16(M, K, device=x.device)
         scale = torch.empty(M, dtype=torch.float32, device=x.device)
     else:
@@ -78,6 +91,8 @@ def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = No
         if scale.dtype != torch.float32 or scale.numel() != M or not scale.is_contiguous():
             raise ValueError("scale must hold M contiguous float32 values")
     _quantize(x, M, K, stride, dt, q.data_ptr(), _stride(q, 0), scale.data_ptr())
+    if given:
+        _written(q, scale)
     return q, scale
 
 
@@ -119,7 +134,7 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     Rows of `out` in no group, or whose index is negative, are left as they
     were (a new `out` starts undefined there).  b has to be laid out with its
     rows at multiples of 16 bytes (quantize and pad_rows do); a is copied if it
-    is not.
+    is not.  There is no gradient: scales and an `out` that want one are refused.
     """
     dev = gpu_tensor(a, "a").get_device()
     if a.dtype != torch.int8 or a.dim() != 2:
@@ -141,13 +156,15 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
         raise ValueError("the scales of a group must be contiguous")
     if not _laid_out(b):
         raise ValueError("b's rows must start at multiples of 16 bytes: lay it out with pad_rows")
+    _no_gradient("matmul", a_scale, b_scale, *(() if out is None else [out]))
     a, a_scale = pad_rows(a), a_scale.contiguous()
     M = a_rows
     if index is not None:
         index, M = index.contiguous(), index.numel()
     if offsets is not None:
         offsets = offsets.contiguous()
-    if out is None:
+    given = out is not None
+    if not given:
         if out_dtype not in DTYPES:
             raise ValueError(f"out_dtype must be bfloat16, float16 or float32, not {out_dtype}")
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
@@ -163,6 +180,8 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
         _pointer(offsets, "offsets", torch.int32, dev), b_at, _stride(b, -2),
         _stride(b, 0) if G else 0, bs_at, (b_scale.stride(0) if G > 1 else wide) if G else 0,
         out.data_ptr(), out.stride(0) if M > 1 else N, od))
+    if given:
+        _written(out)
     return out
 
 

@@ -557,3 +557,36 @@ def test_training_through_the_routing():
     assert float((out.detach().cpu().double() - ref).abs().max()) <= 1e-4 * float(ref.abs().max())
     for u, v in zip(got, want):
         assert float((u.cpu().double() - v).norm()) <= 1e-4 * float(v.norm())
+
+
+def test_outputs_given_and_gradients():
+    """A given output counts as changed, so that a backward pass that needs what it
+    held before is refused; outputs and scales that want a gradient are refused."""
+    from resident_expert_routing_amd import int8, rows
+    q, s = int8.quantize(torch.randn(8, 64, device="cuda"))
+    wq, ws = int8.quantize(torch.randn(32, 64, device="cuda"))
+    out = torch.empty(8, 32, device="cuda")
+    order = rows.RowOrder(torch.arange(8, dtype=torch.int32, device="cuda"), 4, 2)
+    w = torch.ones(4, 2, device="cuda", requires_grad=True)
+    y = rows.combine(int8.matmul(q, s, wq, ws, out=out), order, w)
+    int8.matmul(q, s, wq, ws, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    before = q._version, s._version
+    int8.quantize(torch.randn(8, 64, device="cuda"), (q, s))
+    assert q._version > before[0] and s._version > before[1]
+    with torch.inference_mode():
+        held = torch.empty(8, 32, device="cuda")
+        int8.matmul(q, s, wq, ws, out=held)
+
+    def wanting(t):
+        return t.detach().clone().requires_grad_()
+
+    for args, kw in (((q, wanting(s), wq, ws), {}), ((q, s, wq, wanting(ws)), {}),
+                     ((q, s, wq, ws), dict(out=wanting(out)))):
+        with pytest.raises(ValueError, match="gradient"):
+            int8.matmul(*args, **kw)
+        with torch.no_grad():
+            int8.matmul(*args, **kw)
+    with pytest.raises(ValueError, match="gradient"):
+        int8.quantize(torch.randn(8, 64, device="cuda"), (q, wanting(s)))
