@@ -211,12 +211,15 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 // Direct loads to LDS at lds_base + size * lane (lds_base is wave-uniform and
 // goes to M0).  Inline assembly, so that the compiler does not add a wait for
 // every outstanding load before each LDS read: the pipeline waits for them
-// explicitly, with the count of loads that may still be in flight.
+// explicitly, with the count of loads that may still be in flight.  Between a
+// scalar write of M0 and a load to LDS that takes its address from it gfx9 wants
+// one wait state, and inside an assembly string the compiler adds none: the
+// s_nop, without which a load could land where the one before it did.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is written here on purpose
 __device__ __forceinline__ void dma16(const uint8_t* g, uint8_t* lds_base) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8*)lds_base);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(m0), "v"(g)
                : "memory", "m0");

@@ -527,12 +527,13 @@ constexpr int part_of(int n, int most) {  // the largest divisor of n that is at
   return d;
 }
 
-// dma16 past the caches, for bytes that no other workgroup reads.
+// dma16 past the caches (with its wait state), for bytes that no other workgroup
+// reads.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is written here on purpose
 __device__ __forceinline__ void dma16_past(const uint8_t* g, uint8_t* lds_base) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8*)lds_base);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off nt"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
                :
                : "s"(m0), "v"(g)
                : "memory", "m0");
