@@ -41,9 +41,11 @@ struct RowsArgs {
 
 // A workgroup has one token at a time, so its rows and weights are scalars and
 // a row's address is a scalar base and a thread's 32-bit offset (H * 4 <= 2^32).
+// Tokens are counted without a sign: the step of the grid leads past 2^31 - 1
+// behind the last one of a batch of nearly as many.
 
 // The rows of picks j0 .. j0 + 7 of token t: -1 past k and for absent ones.
-__device__ __forceinline__ void rows_of(const RowsArgs& p, int t, int j0, int (&row)[8]) {
+__device__ __forceinline__ void rows_of(const RowsArgs& p, uint32_t t, int j0, int (&row)[8]) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     int r = -1;
@@ -52,7 +54,7 @@ __device__ __forceinline__ void rows_of(const RowsArgs& p, int t, int j0, int (&
   }
 }
 
-__device__ __forceinline__ void weights_of(const RowsArgs& p, int t, int j0, float (&w)[8]) {
+__device__ __forceinline__ void weights_of(const RowsArgs& p, uint32_t t, int j0, float (&w)[8]) {
 #pragma unroll
   for (int u = 0; u < 8; ++u)
     w[u] = p.weight && j0 + u < p.k ? p.weight[(size_t)t * p.k + j0 + u] : 1.0f;
@@ -104,7 +106,7 @@ __device__ __forceinline__ Piece<E, N> scaled(const Piece<E, N>& v, float w) {
 // their own, so these are the last rows, and they are set to zero (row t*k + j
 // by the workgroups of token t, the pieces from i0 to before i1 by this one).
 template <typename E, int N>
-__device__ __forceinline__ void zero_unnamed(const RowsArgs& p, int t, uint32_t i0, uint32_t i1) {
+__device__ __forceinline__ void zero_unnamed(const RowsArgs& p, uint32_t t, uint32_t i0, uint32_t i1) {
   if (!p.perm) return;
   for (int j = 0; j < p.k; ++j) {
     const size_t r = (size_t)t * p.k + j;
@@ -121,7 +123,7 @@ __device__ __forceinline__ void zero_unnamed(const RowsArgs& p, int t, uint32_t 
 constexpr int kHold = 4;
 
 template <typename E, int N, bool WEIGHT, bool NT>
-__device__ __forceinline__ void spread_span(const RowsArgs& p, int t, uint32_t i0) {
+__device__ __forceinline__ void spread_span(const RowsArgs& p, uint32_t t, uint32_t i0) {
   const uint32_t step = blockDim.x * N, H = p.H, first = i0 + threadIdx.x * N;
   Piece<E, N> v[kHold];
 #pragma unroll
@@ -155,7 +157,7 @@ __device__ __forceinline__ void spread_span(const RowsArgs& p, int t, uint32_t i
 template <typename E, int N, bool WEIGHT>
 __global__ __launch_bounds__(kThreads) void spread_rows(RowsArgs p) {
   const uint32_t span = kHold * blockDim.x * N;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x)
+  for (uint32_t t = blockIdx.x; t < (uint32_t)p.T; t += gridDim.x)
     for (uint32_t i0 = blockIdx.y * span; i0 < (uint32_t)p.H; i0 += gridDim.y * span)
       spread_span<E, N, WEIGHT, false>(p, t, i0);
 }
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(kThreads) void spread_rows(RowsArgs p) {
 template <typename E, int N>
 __global__ __launch_bounds__(kThreads) void gather_rows(RowsArgs p) {
   const uint32_t step = blockDim.x * N, H = p.H;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+  for (uint32_t t = blockIdx.x; t < (uint32_t)p.T; t += gridDim.x) {
     for (uint32_t i = blockIdx.y * step + threadIdx.x * N; i < H; i += gridDim.y * step) {
       const uint32_t at = start_of<E, N>(i, H);
       float acc[N] = {};
@@ -224,7 +226,7 @@ __global__ __launch_bounds__(kDotThreads) void rows_dot(RowsArgs p) {
   const char* rows = SPREAD ? p.other : p.src;
   const size_t token_stride = SPREAD ? p.src_stride : p.other_stride;
   const size_t row_stride = SPREAD ? p.other_stride : p.src_stride;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+  for (uint32_t t = blockIdx.x; t < (uint32_t)p.T; t += gridDim.x) {
     float dot[KP] = {};
     for (uint32_t i = threadIdx.x * N; i < H; i += step) {
       const uint32_t at = start_of<E, N>(i, H), twice = i - at;  // elements counted before
