@@ -610,8 +610,9 @@ int moe_positions(const int32_t* perm, int T, int k, int32_t* pos, int32_t* perm
 /*
  * moe_dispatch -- src [T][H] token rows, dst [T*k][H] rows:
  *   dst[pos[t,j]] = w[t,j] * src[t]         (w = 1 and a plain copy if weight is NULL)
- *   dst[p] = 0 where perm[p] names no assignment, if perm is given; with perm
- *   NULL, the rows that pos does not name are left as they were.
+ *   dst[p] = 0 where perm[p] names no assignment, or one whose row is another
+ *   (pos[perm[p]] != p: the earlier row of an assignment named twice), if perm is
+ *   given; with perm NULL, the rows that pos does not name are left as they were.
  * moe_dispatch_backward -- its gradient; src [T*k][H] the gradient of the
  * rows, dst [T][H] that of the token rows, other [T][H] the forward call's src:
  *   dst[t] = sum_j w[t,j] * src[pos[t,j]]

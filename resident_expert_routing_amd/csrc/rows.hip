@@ -102,17 +102,29 @@ __device__ __forceinline__ Piece<E, N> scaled(const Piece<E, N>& v, float w) {
   return o;
 }
 
-// The rows that perm gives no assignment: picks with no slot have no row of
-// their own, so these are the last rows, and they are set to zero (row t*k + j
-// by the workgroups of token t, the pieces from i0 to before i1 by this one).
+// The rows that belong to no assignment: those to which perm gives none (picks
+// with no slot have no row of their own, so these are the last rows), and the
+// earlier ones of an assignment that perm names twice, whose row is pos[a].  They
+// are set to zero (row t*k + j by the workgroups of token t, the pieces from i0 to
+// before i1 by this one).  Eight rows at a time, so that their loads overlap.
 template <typename E, int N>
-__device__ __forceinline__ void zero_unnamed(const RowsArgs& p, uint32_t t, uint32_t i0, uint32_t i1) {
+__device__ __forceinline__ void zero_unnamed(const RowsArgs& p, uint32_t t, uint32_t i0,
+                                             uint32_t i1) {
   if (!p.perm) return;
-  for (int j = 0; j < p.k; ++j) {
-    const size_t r = (size_t)t * p.k + j;
-    if ((unsigned)p.perm[r] < (unsigned)p.n) continue;
-    for (uint32_t i = i0 + threadIdx.x * N; i < i1; i += blockDim.x * N)
-      store_piece<false>(Piece<E, N>{}, p.dst + r * p.dst_stride, start_of<E, N>(i, p.H));
+  const size_t first = (size_t)t * p.k;
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    int a[8], at[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a[u] = p.perm[first + min(j0 + u, p.k - 1)];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) at[u] = p.pos[(unsigned)a[u] < (unsigned)p.n ? a[u] : 0];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t r = first + j0 + u;
+      if (j0 + u >= p.k || ((unsigned)a[u] < (unsigned)p.n && at[u] == (int)r)) continue;
+      for (uint32_t i = i0 + threadIdx.x * N; i < i1; i += blockDim.x * N)
+        store_piece<false>(Piece<E, N>{}, p.dst + r * p.dst_stride, start_of<E, N>(i, p.H));
+    }
   }
 }
 

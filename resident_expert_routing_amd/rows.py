@@ -205,7 +205,8 @@ def _check(src: torch.Tensor, n: int, order: RowOrder, what: str) -> None:
 
 def dispatch(x: torch.Tensor, order: RowOrder, weight: torch.Tensor | None = None) -> torch.Tensor:
     """x [T, H] -> rows [T*k, H]: row p is x[perm[p] // k], times its weight if
-    `weight` [T, k] is given; rows that perm does not use are zero."""
+    `weight` [T, k] is given; rows that perm does not use are zero, and so is the
+    earlier row of an assignment that perm names twice."""
     _check(x, order.T, order, "x")
     return _move(x, weight, order, _spread, _gather)
 

@@ -44,3 +44,47 @@ def test_the_most_assignments_there_can_be():
     B.check(B.moe_combine_backward(n, 1, 1, dt, pos, two, 1, z, 1, other=y, other_stride=1,
                                    dweight=dw, stream=stream))
     assert torch.equal(z, two) and torch.equal(dw.to(torch.bfloat16), 2 * x)
+
+
+@pytest.mark.parametrize("T,H,k", [(4, 3, 2), (9, 96, 8), (33, 1001, 9), (2000, 40, 4)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_an_assignment_named_twice(T, H, k, grad):
+    """Its row is the later one; the earlier one belongs to nobody and is zero,
+    in dispatch and in combine's backward pass, whatever the output held before."""
+    from resident_expert_routing_amd import binding as B
+    n = T * k
+    g = torch.Generator().manual_seed(T)
+    perm = torch.randperm(n, generator=g).to(torch.int32)
+    perm[n // 2] = perm[n - 1]                # one twice, so another one not at all
+    perm[1] = perm[n - 2]
+    perm[0] = -1
+    pos = torch.full((n,), -1, dtype=torch.int32)
+    for p in range(n):
+        if perm[p] >= 0:
+            pos[perm[p]] = p
+    owned = torch.zeros(n, dtype=torch.bool)
+    owned[pos[pos >= 0].long()] = True
+    x, w = torch.randn(T, H, generator=g), torch.rand(T, k, generator=g)
+    other = torch.randn(n, H, generator=g)
+    out = torch.full((n, H), 7.25, device="cuda")
+    dw = torch.full((T, k), -1.0, device="cuda")
+    dperm, dpos = perm.cuda(), torch.empty(T, k, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.current_stream()
+    B.check(B.moe_positions(dperm, T, k, dpos, stream=stream))
+    assert torch.equal(dpos.cpu().view(-1), pos)
+    args = (T, H, k, B.MOE_DT_FP32, dpos, x.cuda(), H, out, H, w.cuda())
+    if grad:
+        B.check(B.moe_combine_backward(*args, perm=dperm, other=other.cuda(), other_stride=H,
+                                       dweight=dw, stream=stream))
+        dots = torch.where(pos < 0, 0.0, (other[pos.clamp(min=0).long()].double()
+                                          * x.double().repeat_interleave(k, 0)).sum(1))
+        mag = (other[pos.clamp(min=0).long()].double()
+               * x.double().repeat_interleave(k, 0)).abs().sum(1)
+        off = (dw.cpu().view(-1).double() - dots).abs()
+        assert bool((off <= (H + 12) * 2.0 ** -24 * mag).all())
+    else:
+        B.check(B.moe_dispatch(*args, perm=dperm, stream=stream))
+    a = perm.clamp(min=0).long()
+    # one float32 product: the same number on both sides
+    want = torch.where(owned[:, None], x[a // k] * w.view(-1)[a][:, None], 0.0)
+    assert torch.equal(out.cpu(), want)
