@@ -14,8 +14,8 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .rows import (DTYPES, RowOrder, combine, dtype_of, gpu_tensor, on_its_device, row_major,
-                   stream_of)
+from .rows import (DTYPES, RowOrder, combine, dtype_of, gpu_tensor, no_tangent, on_its_device,
+                   row_major, stream_of)
 
 _lib = B.load()
 
@@ -55,6 +55,7 @@ def _laid_out(q: torch.Tensor) -> bool:
 
 
 def _no_gradient(call: str, *tensors) -> None:
+    no_tangent(call, *tensors)
     for t in tensors:
         if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{call} has no gradient: detach its tensors, or call it under "
@@ -71,7 +72,7 @@ def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = No
     """x [M, K] (bf16, fp16 or fp32) -> (q int8 [M, K], scale float32 [M]) with
     x ~= q * scale[:, None]; the scale is the row's largest magnitude over 127.
     `out`: a pair that an earlier call of the same shape returned, to be filled.
-    There is no gradient: tensors that want one are refused."""
+    There is no gradient: tensors that want one, or carry a tangent, are refused."""
     gpu_tensor(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must have shape [M, K], not {list(x.shape)}")
@@ -134,7 +135,8 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     Rows of `out` in no group, or whose index is negative, are left as they
     were (a new `out` starts undefined there).  b has to be laid out with its
     rows at multiples of 16 bytes (quantize and pad_rows do); a is copied if it
-    is not.  There is no gradient: scales and an `out` that want one are refused.
+    is not.  There is no gradient: scales and an `out` that want one, or carry
+    a tangent, are refused.
     """
     dev = gpu_tensor(a, "a").get_device()
     if a.dtype != torch.int8 or a.dim() != 2:

@@ -9,7 +9,8 @@ Both take bf16, fp16 or fp32 rows and float32 weights, and pass gradients to the
 rows and to the weights (moe_dispatch_backward, moe_combine_backward).  A call
 that is recorded keeps copies of the order and of the weights, since the next
 moe_route may write over both before the backward pass; rows that the weights'
-gradient needs are kept as they are.  Calls run on the current stream of the
+gradient needs are kept as they are.  There is no forward-mode derivative: tensors
+that carry a tangent are refused.  Calls run on the current stream of the
 rows' device and synchronise nothing.  A gradient captured into a graph is taken
 with torch.autograd.grad, or with no graph made outside the capture alive over
 the same leaves: torch ties a leaf's accumulation to the stream that first used it.
@@ -19,6 +20,7 @@ from __future__ import annotations
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 
@@ -58,6 +60,17 @@ def gpu_tensor(t, what: str, device: int | None = None) -> torch.Tensor:
     if device is not None and t.get_device() != device:
         raise ValueError(f"{what} is on {t.device}, other tensors on GPU {device}")
     return t
+
+
+def no_tangent(call: str, *tensors) -> None:
+    """Refuses tensors that carry a forward-mode tangent (None among them is none):
+    the kernels see a tensor's values only, and a result without a tangent would
+    pass for one of derivative zero."""
+    if forward_ad._current_level < 0:  # outside every dual_level: no tensor has one
+        return
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{call} has no forward-mode derivative: a tensor carries a tangent")
 
 
 def row_major(t: torch.Tensor) -> tuple[torch.Tensor, int]:
@@ -183,6 +196,7 @@ class _Move(torch.autograd.Function):
         if torch.is_grad_enabled():
             raise RuntimeError("dispatch and combine have no second derivative: take their "
                                "gradient without create_graph")
+        no_tangent("the gradient of dispatch and combine", grad)
         src, w = ctx.saved_tensors
         dsrc, dw = ctx.back(grad, ctx.order, w, src)
         if dw is not None:
@@ -191,6 +205,7 @@ class _Move(torch.autograd.Function):
 
 
 def _move(src, weight, order, there, back):
+    no_tangent("a call of dispatch or combine", src, weight)
     if torch.is_grad_enabled() and (src.requires_grad
                                     or (weight is not None and weight.requires_grad)):
         return _Move.apply(src, weight, order, there, back)

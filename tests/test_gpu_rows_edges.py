@@ -88,3 +88,48 @@ def test_an_assignment_named_twice(T, H, k, grad):
     # one float32 product: the same number on both sides
     want = torch.where(owned[:, None], x[a // k] * w.view(-1)[a][:, None], 0.0)
     assert torch.equal(out.cpu(), want)
+
+
+def test_tangents_are_refused():
+    """No call drops a forward-mode derivative: of the rows, of the weights, with
+    and without gradients recorded, nor of the gradient in a backward pass."""
+    from torch.autograd import forward_ad
+    from resident_expert_routing_amd import int8, rows
+    T, H, k = 6, 32, 2
+    order = rows.RowOrder(torch.randperm(T * k, device="cuda").int(), T, k)
+    ins = {"x": torch.randn(T, H, device="cuda"), "r": torch.randn(T * k, H, device="cuda"),
+           "w": torch.rand(T, k, device="cuda")}
+    q, s = int8.quantize(ins["x"])
+    wq, ws = int8.quantize(torch.randn(8, H, device="cuda"))
+    out = torch.empty(T, 8, device="cuda")
+    calls = [
+        (lambda x: rows.dispatch(x, order), ins["x"]),
+        (lambda x: rows.dispatch(x, order, ins["w"]), ins["x"]),
+        (lambda w: rows.dispatch(ins["x"], order, w), ins["w"]),
+        (lambda r: rows.combine(r, order, ins["w"]), ins["r"]),
+        (lambda w: rows.combine(ins["r"], order, w), ins["w"]),
+        (int8.quantize, ins["x"]),
+        (lambda t: int8.quantize(ins["x"], (q, t)), s),
+        (lambda t: int8.matmul(q, t, wq, ws), s),
+        (lambda t: int8.matmul(q, s, wq, t), ws),
+        (lambda t: int8.matmul(q, s, wq, ws, out=t), out),
+    ]
+    for call, t in calls:
+        for wants in (False, True):
+            with forward_ad.dual_level():
+                u = t.detach().clone().requires_grad_(wants)
+                d = forward_ad.make_dual(u, torch.ones_like(u))
+                with pytest.raises(ValueError, match="tangent|gradient"):
+                    call(d)
+                with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+                    call(d)
+            with torch.no_grad():
+                call(t.detach().clone())
+    x = ins["x"].detach().clone().requires_grad_()
+    w = ins["w"].detach().clone().requires_grad_()
+    y = rows.dispatch(x, order, w)
+    g = torch.ones_like(y)
+    with forward_ad.dual_level():
+        with pytest.raises(ValueError, match="tangent"):
+            torch.autograd.grad(y, [x, w], forward_ad.make_dual(g, g), retain_graph=True)
+        torch.autograd.grad(y, [x, w], g)
