@@ -36,6 +36,7 @@ MOE_ACT_MXFP6 = 1
 MOE_DT_BF16 = 0
 MOE_DT_FP16 = 1
 MOE_DT_FP32 = 2
+MOE_INT_MAX = 2 ** 31 - 1
 MOE_MAX_E = 1024
 MOE_MAX_K = 32
 MOE_MAX_S = 8192
@@ -193,6 +194,11 @@ def _ptr(p) -> int | None:
     if p is None or isinstance(p, int):
         return p
     return p.data_ptr()
+
+
+def fits(*sizes) -> bool:
+    """Whether every size is one that a C int holds (ctypes would cut it to 32 bits)."""
+    return max(sizes) <= MOE_INT_MAX and min(sizes) >= -MOE_INT_MAX
 
 
 def _host(a) -> int | None:
@@ -377,7 +383,10 @@ def moe_history_scale(hist, n, factor, stream=None) -> int:
     return int(load().moe_history_scale(_ptr(hist), int(n), float(factor), _stream(stream)))
 
 
+# Sizes that a C int does not hold are past every limit of these calls.
 def moe_positions(perm, T, k, pos, perm_copy=None, stream=None) -> int:
+    if not fits(T, k):
+        return MOE_EUNSUPPORTED
     return int(load().moe_positions(_ptr(perm), int(T), int(k), _ptr(pos), _ptr(perm_copy),
                                     _stream(stream)))
 
@@ -392,12 +401,16 @@ def _rows_args(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight, pe
 
 def moe_dispatch(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None, perm=None,
                  stream=None) -> int:
+    if not fits(T, H, k, dtype):
+        return MOE_EUNSUPPORTED
     return int(load().moe_dispatch(_rows_args(T, H, k, dtype, pos, src, src_stride, dst,
                                               dst_stride, weight, perm), _stream(stream)))
 
 
 def moe_dispatch_backward(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None,
                           other=None, other_stride=0, dweight=None, stream=None) -> int:
+    if not fits(T, H, k, dtype):
+        return MOE_EUNSUPPORTED
     return int(load().moe_dispatch_backward(
         _rows_args(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight, None, other,
                    other_stride, dweight), _stream(stream)))
@@ -405,6 +418,8 @@ def moe_dispatch_backward(T, H, k, dtype, pos, src, src_stride, dst, dst_stride,
 
 def moe_combine(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None,
                 stream=None) -> int:
+    if not fits(T, H, k, dtype):
+        return MOE_EUNSUPPORTED
     return int(load().moe_combine(_rows_args(T, H, k, dtype, pos, src, src_stride, dst,
                                              dst_stride, weight), _stream(stream)))
 
@@ -412,16 +427,22 @@ def moe_combine(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=No
 def moe_combine_backward(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight=None,
                          perm=None, other=None, other_stride=0, dweight=None,
                          stream=None) -> int:
+    if not fits(T, H, k, dtype):
+        return MOE_EUNSUPPORTED
     return int(load().moe_combine_backward(
         _rows_args(T, H, k, dtype, pos, src, src_stride, dst, dst_stride, weight, perm, other,
                    other_stride, dweight), _stream(stream)))
 
 
 def moe_int8_row_bytes(K: int) -> int:
+    if not fits(K):
+        return 0
     return int(load().moe_int8_row_bytes(int(K)))
 
 
 def moe_int8_quantize(x, M, K, x_stride, dtype, q, q_stride, scale, stream=None) -> int:
+    if not fits(M, K, dtype):
+        return MOE_EUNSUPPORTED
     return int(load().moe_int8_quantize(_ptr(x), int(M), int(K), int(x_stride), int(dtype),
                                         _ptr(q), int(q_stride), _ptr(scale), _stream(stream)))
 
@@ -429,6 +450,8 @@ def moe_int8_quantize(x, M, K, x_stride, dtype, q, q_stride, scale, stream=None)
 def moe_int8_matmul(M, N, K, G, swiglu, a_rows, a, a_stride, a_scale, index, index_div, offsets,
                     b, b_stride, b_group_stride, b_scale, b_scale_group_stride, out, out_stride,
                     out_dtype, stream=None) -> int:
+    if not fits(M, N, K, G, a_rows, index_div, out_dtype):
+        return MOE_EUNSUPPORTED
     args = Int8MatmulArgs(int(M), int(N), int(K), int(G), 1 if swiglu else 0, int(a_rows),
                           _ptr(a), int(a_stride), _ptr(a_scale), _ptr(index), int(index_div),
                           _ptr(offsets), _ptr(b), int(b_stride), int(b_group_stride),

@@ -102,6 +102,9 @@ class RowOrder:
     def __init__(self, perm: torch.Tensor, T: int, k: int, pos: torch.Tensor | None = None):
         self.T, self.k = int(T), int(k)
         n = self.T * self.k
+        if self.T < 0 or self.k < 1 or n > B.MOE_INT_MAX:
+            raise ValueError(f"{T} tokens of {k} picks: at most 2^31 - 1 assignments, k of 1 "
+                             f"to {B.MOE_MAX_K}")
         if gpu_tensor(perm, "perm").dtype != torch.int32 or perm.numel() != n:
             raise ValueError(f"perm must hold T*k = {n} int32 values")
         self.device = perm.get_device()
@@ -144,8 +147,10 @@ def _move_rows(entry, what, n, src, order, weight, perm, other=None):
         with torch.cuda.device(order.device):
             return _move_rows(entry, what, n, src, order, weight, perm, other)
     dt = dtype_of(src, "rows")
-    src, stride = row_major(src)
     H, T, k = src.shape[1], order.T, order.k
+    if H > B.MOE_INT_MAX:
+        raise B.MoeError(B.MOE_EUNSUPPORTED, what)
+    src, stride = row_major(src)
     dst = torch.empty((n, H), dtype=src.dtype, device=src.device)
     dw, dwp, op, ostride = None, None, None, 0
     if other is not None:

@@ -133,3 +133,31 @@ def test_tangents_are_refused():
         with pytest.raises(ValueError, match="tangent"):
             torch.autograd.grad(y, [x, w], forward_ad.make_dual(g, g), retain_graph=True)
         torch.autograd.grad(y, [x, w], g)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that a C int would cut: refused before anything is copied or written."""
+    from resident_expert_routing_amd import int8, rows
+    from resident_expert_routing_amd.binding import MoeError
+    wide = 2 ** 32 + 8
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="assignments"):
+        rows.RowOrder(one.expand(wide), wide // 8, 8)
+    with pytest.raises(ValueError, match="assignments"):
+        rows.RowOrder(one.expand(8), -2, -4, pos=one.expand(8))
+    order = rows.RowOrder(one, 1, 1)
+    x = torch.zeros(1, 1, dtype=torch.bfloat16, device="cuda")
+    for call in (rows.dispatch, rows.combine):
+        with pytest.raises(MoeError):
+            call(x.expand(1, wide), order)
+    for shape in ((wide, 1), (1, wide)):
+        with pytest.raises(MoeError):
+            int8.quantize(x.expand(*shape))
+    a, s = torch.zeros(8, 16, dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda")
+    index = torch.zeros(8, dtype=torch.int32, device="cuda")
+    with pytest.raises(MoeError):
+        int8.matmul(a, s, a, s, index=index, index_div=2 ** 32 + 2)
+    with pytest.raises(MoeError):
+        int8.matmul(a, s, a, s, index=one.expand(wide))
+    with pytest.raises(MoeError):
+        int8.matmul(a[:1].expand(wide, 16), s[:1].expand(wide), a, s)
