@@ -702,8 +702,9 @@ int moe_int8_quantize(const void* x, int M, int K, size_t x_stride, int dtype, i
  *   y[p][n] = a_scale[r] * b_scale[g][n] * sum_i a[r][i] * b[g][n][i]
  *   out[p][n] = y[p][n], or with swiglu (b has 2N rows, N gate rows and then
  *               N up rows): silu(y[p][n]) * y[p][N+n], silu(v) = v / (1 + exp(-v))
- * with exact 32-bit integer sums, float32 scaling and one rounding to the
- * element type out_dtype.
+ * with exact 32-bit integer sums, float32 scaling (the sum times a_scale, then
+ * times b_scale) and one rounding to the element type out_dtype.  silu is within
+ * (1.25 |v| + 8) * 2^-24 of its value down to v = -174, below which it is 0.
  *   G > 0 : offsets [G+1] int32 (moe_route's slot_offsets); rows
  *           [offsets[g], offsets[g+1]) belong to group g.  Rows in no group are
  *           left as they were.  Offsets are cut to [0, M].

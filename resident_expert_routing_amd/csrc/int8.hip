@@ -304,10 +304,30 @@ __device__ __forceinline__ int source_row(const MatArgs& p, int m) {
   return (unsigned)r < (unsigned)p.a_rows ? r : -1;
 }
 
-// v / (1 + exp(-v)); the reciprocal's error is one unit in the last place, where
-// the division's ten instructions took 2 us of a tile's epilogue.
-__device__ __forceinline__ float silu(float v) {
-  return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+// silu(g) * u, silu(g) = g / (1 + exp(-g)), of N values.  The reciprocal's error is
+// one unit in the last place, where the division's ten instructions took 2 us of
+// a tile's epilogue; exp(-g) = 2^(-g log2 e), whose rounded argument is off by
+// |g| * 1.25 * 2^-24 of the result, is within two units more.  From -88 down exp
+// overflows, and the product would be zero where the value is still a normal
+// number: below kLow, where 1 + exp(-g) is exp(-g) in float32, the value is
+// (g h) (h u) with h = exp(g / 2), so that only the result can be subnormal (h is
+// down to g = -174).  Few gates get there: one minimum a value, one branch for N.
+template <int N>
+__device__ __forceinline__ void swiglu(const float (&g)[N], const float (&u)[N], float (&y)[N]) {
+  constexpr float kLow = -64.0f;
+  float least = g[0];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    least = fminf(least, g[i]);
+    y[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[i])) * u[i];
+  }
+  if (__builtin_expect(least < kLow, 0)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float h = __expf(0.5f * g[i]);
+      if (g[i] < kLow) y[i] = (g[i] * h) * (h * u[i]);
+    }
+  }
 }
 
 template <typename E>
@@ -436,9 +456,9 @@ __device__ __forceinline__ void stream_tile(const MatArgs& p, const Rows& r, int
       }
     const int n = n0 + 4 * quad;
     if (GLU) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[0][i] = silu(y[0][i]) * y[1][i];
-      if (n < p.N) store_out(p, m, n, y[0]);
+      float h[4];
+      swiglu(y[0], y[1], h);
+      if (n < p.N) store_out(p, m, n, h);
     } else {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -702,11 +722,20 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
     for (int f = f0; f < f0 + kPart; ++f) {
       const float sa = side.row[(wm * MF + f) * 16 + col];
       Piece<E, kOut> o;
+      float y[kOut];
 #pragma unroll
-      for (int j = 0; j < kOut; ++j) {
-        float y = (float)acc[f][j / 4][j % 4] * sa * sn[j / 4][j % 4];
-        if (GLU) y = silu(y) * ((float)acc[f][2 + j / 4][j % 4] * sa * sn[2 + j / 4][j % 4]);
-        o.e[j] = from_f32<E>(y);
+      for (int j = 0; j < kOut; ++j) y[j] = (float)acc[f][j / 4][j % 4] * sa * sn[j / 4][j % 4];
+      if constexpr (GLU) {
+        float up[kOut], h[kOut];
+#pragma unroll
+        for (int j = 0; j < kOut; ++j)
+          up[j] = (float)acc[f][2 + j / 4][j % 4] * sa * sn[2 + j / 4][j % 4];
+        swiglu(y, up, h);
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) o.e[j] = from_f32<E>(h[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) o.e[j] = from_f32<E>(y[j]);
       }
       constexpr int kMine = kOut * (int)sizeof(E) / 16;
 #pragma unroll

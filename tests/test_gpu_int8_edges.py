@@ -1,0 +1,99 @@
+"""8-bit products and experts at the edges: saturating gates, tiles mapped to the
+XCDs in blocks, batches that do not fit."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+UNDER = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -150}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu_ready():
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    import resident_expert_routing_amd  # noqa: F401
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+
+
+def tiles_of(M, N, swiglu, G=0):
+    """(tiled form?, items x columns of 64-row tiles) by the rule of few_tiles."""
+    cols = -(-N // (128 if swiglu else 256))
+    items, thin = -(-M // 64), False
+    if G:
+        groups = min(G, M)
+        items, thin = max(items, groups), M < 4 * groups
+    return items * cols >= (192 if thin else 48), items * cols
+
+
+@pytest.mark.parametrize("N", [40, 1801])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_saturating_gates(N, dtype):
+    """SwiGLU with gates over +-127 and beyond, in the streaming and the tiled form.
+
+    Gate and up values are exact: one product each of small integers and scales
+    that are powers of two.  So the only errors are the epilogue's: for |g| <= 64
+    the argument of exp, its instruction (2 units of 2^-24 after the argument's
+    1.25 |g|), a sum (1), a reciprocal (2) and two products (2); below -64 two
+    halves of the argument's 1.25 |g|, two exponentials (4) and three products (3);
+    above, less.  (1.25 |g| + 8) * 2^-24 of the value holds all, then the rounding
+    to the type.  Largest magnitudes of the exact values, 127 * 127 * 2^20 * 16, are
+    finite in float32 and overflow in fp16, as they should."""
+    from resident_expert_routing_amd import int8
+    tiled, n = tiles_of(255, N, True)
+    say(f"gates N={N} {dtype} tiled={tiled} ({n} tiles)")
+    assert tiled == (N > 100)
+    M, K = 255, 16
+    a = torch.zeros(M, K, dtype=torch.int8)
+    a[:, 0] = torch.arange(-127, 128)             # the gate's factor
+    a[:, 1] = torch.arange(M) % 13 - 6            # the up's
+    b = torch.zeros(2 * N, K, dtype=torch.int8)
+    b[:N, 0] = torch.arange(N) % 16 + 1           # gates: r * (1 .. 16) / 16 and / 8
+    b[N:, 1] = torch.arange(N) % 127 + 1
+    sb = torch.ones(2 * N)
+    sb[:N] = torch.where(torch.arange(N) % 3 == 0, 0.125, 0.0625)
+    sb[N:] = 2.0 ** (20 - torch.arange(N) % 21).double()
+    got = int8.matmul(a.cuda(), torch.ones(M, device="cuda"), b.cuda(), sb.cuda(), swiglu=True,
+                      out_dtype=dtype).cpu().double()
+    z = (a.double() @ b.double().t()) * sb.double()
+    g, u = z[:, :N], z[:, N:]
+    assert float(g.min()) < -200 and float(g.max()) > 200
+    want = g / (1 + torch.exp(-g)) * u
+    most = torch.finfo(dtype).max
+    eps = torch.finfo(dtype).eps / 2
+    bound = (1.25 * g.abs() + 8) * 2.0 ** -24 * want.abs() * (1 + eps) + eps * want.abs() \
+        + UNDER[dtype]
+    bound = torch.where(g < -174, bound + want.abs(), bound)   # h is below every normal number
+    fits = want.abs() < most * (1 - 4 * eps)
+    off = (got - want).abs()
+    assert bool((off[fits] <= bound[fits]).all()), float((off / bound)[fits].max())
+    over = want.abs() > most * (1 + 4 * eps)
+    assert bool(torch.isinf(got[over]).all())
+    assert not bool(torch.isnan(got).any())
+    # values that are normal numbers of the type are not lost
+    normal = (g > -174) & (want.abs() > 2 * torch.finfo(dtype).tiny)
+    assert bool((got[normal] != 0).all())
+
+
+def test_gates_that_are_no_numbers():
+    """Infinite and NaN scales reach only the rows they belong to; silu(-inf) is
+    NaN, as g / (1 + exp(-g)) is."""
+    from resident_expert_routing_amd import int8
+    for N in (40, 1801):
+        M, K = 255, 16
+        a, b = torch.ones(M, K, dtype=torch.int8), torch.ones(2 * N, K, dtype=torch.int8)
+        sa = torch.full((M,), 0.125)
+        sa[3], sa[7] = float("nan"), float("inf")
+        b[1] = -1
+        y = int8.matmul(a.cuda(), sa.cuda(), b.cuda(), torch.ones(2 * N, device="cuda"),
+                        swiglu=True, out_dtype=torch.float32).cpu()
+        assert torch.isnan(y[3]).all()
+        assert torch.isnan(y[7, 1]) and bool((y[7, 2:] == float("inf")).all())
+        rest = torch.ones(M, dtype=torch.bool)
+        rest[[3, 7]] = False
+        assert bool(torch.isfinite(y[rest]).all())
