@@ -79,7 +79,7 @@ def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = No
     _no_gradient("quantize", x, *(out or ()))
     dt = dtype_of(x, "x")
     M, K = x.shape
-    if not B.fits(M, K):
+    if max(M, K) > B.MOE_INT_MAX:
         raise B.MoeError(B.MOE_EUNSUPPORTED, "moe_int8_quantize")
     x, stride = row_major(x)
     given = out is not None
@@ -154,7 +154,8 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     N = wide // 2 if swiglu else wide
     if swiglu and wide % 2:
         raise ValueError("swiglu needs an even number of rows of b")
-    if not B.fits(a_rows, K, wide, G, index_div, 0 if index is None else index.numel()):
+    if max(a_rows, K, wide, G) > B.MOE_INT_MAX or \
+            (index is not None and not B.fits(index_div, index.numel())):
         raise B.MoeError(B.MOE_EUNSUPPORTED, "moe_int8_matmul")
     if a_scale.numel() != a_rows or b_scale.shape != b.shape[:-1]:
         raise ValueError("a_scale and b_scale must have one value for each row of a and b")
