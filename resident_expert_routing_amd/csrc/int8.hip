@@ -530,6 +530,15 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Lanes of a wave hand values to each other through LDS across this: LDS is in order
+// within a wave, so the hardware waits for nothing, and the compiler is kept from
+// moving accesses over it.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // What the epilogue needs of a tile's rows and columns, loaded beside the first
 // stage.
 constexpr int kMostRows = 320;
@@ -742,6 +751,7 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
       for (int c = 0; c < kMine; ++c)
         __builtin_memcpy(place((f - f0) * 16 + col, quad * kMine + c), (const char*)o.e + 16 * c, 16);
     }
+    wave_exchange();
     constexpr int kPer = 64 / kPieces;  // rows of a store instruction
 #pragma unroll
     for (int x0 = 0; x0 < kPart * 16; x0 += kPer) {
@@ -756,6 +766,7 @@ __device__ __forceinline__ void tile(const MatArgs& p, const Rows& r, int n0, ui
       else
         o.store_head(to, p.N - n);
     }
+    wave_exchange();  // the part is written over next
   }
 }
 
