@@ -71,7 +71,9 @@ def _written(*tensors) -> None:
 def quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
     """x [M, K] (bf16, fp16 or fp32) -> (q int8 [M, K], scale float32 [M]) with
     x ~= q * scale[:, None]; the scale is the row's largest magnitude over 127.
-    `out`: a pair that an earlier call of the same shape returned, to be filled.
+    `out`: a pair that an earlier call of the same shape returned, to be filled, or
+    views of that layout; from K up to the next multiple of 16 a row of q is set
+    to zero.
     There is no gradient: tensors that want one, or carry a tangent, are refused."""
     gpu_tensor(x, "x")
     if x.dim() != 2:
@@ -235,10 +237,24 @@ class Int8Experts:
         quantize(up, (gu[I:], gs[I:]))
         quantize(down, (self.down[slot], self.down_scale[slot]))
 
+    def check(self, x, T: int) -> None:
+        """Refuses token rows that are not [T, H] of a type that quantize takes, on
+        the experts' device, or that want a gradient."""
+        gpu_tensor(x, "x", self.gate_up.get_device())
+        dtype_of(x, "x")
+        if tuple(x.shape) != (T, self.H):
+            raise ValueError(f"x must have shape [{T}, {self.H}], not {list(x.shape)}")
+        _no_gradient("Int8Experts", x)
+
     def rows(self, x, slot_offsets, perm, k: int, out_dtype=torch.float32) -> torch.Tensor:
         """The experts on the rows of a bucketing: token rows x [T, H] ->
-        [T*k, H], row p from token perm[p] // k.  The second products' inputs
-        are rounded to bf16 before they are quantised."""
+        [T*k, H] (as many rows as perm has), row p from token perm[p] // k; rows
+        that are in no slot are undefined.  The second products' inputs are
+        rounded to bf16 before they are quantised."""
+        self.check(x, x.shape[0])
+        if perm.numel() > x.shape[0] * k:
+            raise ValueError(f"perm holds {perm.numel()} values, more than the T*k = "
+                             f"{x.shape[0] * k} assignments of x")
         q, s = quantize(x)
         h = matmul(q, s, self.gate_up, self.gate_up_scale, offsets=slot_offsets, index=perm,
                    index_div=k, swiglu=True)
@@ -250,5 +266,6 @@ class Int8Experts:
         """x [T, H] -> [T, H] in x's type: the layer's experts and their weighted
         sum, from what moe_route wrote for the batch."""
         T, k = sel_weight.shape
+        self.check(x, T)
         order = RowOrder(perm, T, k, pos)
         return combine(self.rows(x, slot_offsets, perm, k, x.dtype), order, sel_weight)

@@ -311,11 +311,18 @@ def layer_step(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, aren
 def layer_step_int8(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, int8_experts):
     """One pass of the layer with its experts in 8-bit integers (int8.Int8Experts,
     one group for each of buf's S slots): route with demand, the experts on the
-    rows of the bucketing, combine.  x [T, H] bf16; returns [T, H] bf16.  On the
-    current stream of x's device."""
-    route(buf, x, w_router, bias, expert_slot, torch.cuda.current_stream(x.device),
-          hist_row=hist_row)
-    return int8_experts.forward(x, buf.slot_offsets, buf.perm, buf.sel_weight)
+    rows of the bucketing, combine.  x [T, H] bf16, contiguous; returns [T, H] bf16.
+    On the current stream of x's device.  What does not fit is refused before the
+    demand is counted."""
+    int8_experts.check(x, buf.T)
+    if x.dtype != torch.bfloat16 or not x.is_contiguous():
+        raise ValueError("x must be contiguous bfloat16 rows")
+    if (int8_experts.S, int8_experts.H) != (buf.S, buf.H):
+        raise ValueError(f"experts of {int8_experts.S} slots and H = {int8_experts.H} do not fit "
+                         f"buffers of {buf.S} and {buf.H}")
+    with torch.cuda.device(x.device):
+        route(buf, x, w_router, bias, expert_slot, torch.cuda.current_stream(), hist_row=hist_row)
+        return int8_experts.forward(x, buf.slot_offsets, buf.perm, buf.sel_weight)
 
 
 class SharedArena:

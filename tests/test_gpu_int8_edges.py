@@ -97,3 +97,55 @@ def test_gates_that_are_no_numbers():
         rest = torch.ones(M, dtype=torch.bool)
         rest[[3, 7]] = False
         assert bool(torch.isfinite(y[rest]).all())
+
+
+def test_batches_that_do_not_fit_are_refused():
+    """Token rows, perm or buffers that do not belong together, rows that the
+    router would read as something else: refused, and the demand is not counted."""
+    from resident_expert_routing_amd import int8
+    from resident_expert_routing_amd import runtime as R
+    T, H, E, k, I, S = 12, 256, 16, 4, 128, 10
+    dev = torch.device("cuda", 0)
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    w_router = (torch.randn(E, H, generator=g) / 16).cuda()
+    slot = torch.full((E,), -1, dtype=torch.int32)
+    slot[:S] = torch.arange(S, dtype=torch.int32)
+    slot = slot.cuda()
+    buf = R.LayerBuffers(T, H, E, k, I, S, dev)
+    hist = torch.zeros(E, dtype=torch.float64, device="cuda")
+    w = [(torch.randn(S, *s, generator=g) / 16).cuda() for s in ((I, H), (I, H), (H, I))]
+    ex = int8.Int8Experts.from_weights(*w)
+
+    def step(x, ex=ex):
+        return R.layer_step_int8(buf, x, w_router, None, slot, hist, ex)
+
+    want = step(x)
+    counted = hist.clone()
+    assert float(counted.sum()) > 0
+    wide = torch.zeros(T, 2 * H, dtype=torch.bfloat16, device="cuda")
+    wide[:, ::2] = x
+    for bad in (x.view(torch.int16), x.half(), x.float(), x[:-1], x[:, :-8].contiguous(),
+                wide[:, ::2], wide[:, :H], x.cpu(), x.clone().requires_grad_()):
+        with pytest.raises(ValueError):
+            step(bad)
+    for s in (S - 1, S + 1):
+        with pytest.raises(ValueError, match="slots"):
+            step(x, int8.Int8Experts.empty(s, H, I, dev))
+    with pytest.raises(ValueError):
+        step(x, int8.Int8Experts.empty(S, 2 * H, I, dev))
+    torch.cuda.synchronize()
+    assert torch.equal(hist, counted)
+    args = (buf.slot_offsets, buf.perm)
+    for bad in (x[:-1], torch.cat((x, x)), x.view(torch.int16), x.double(), x[0]):
+        with pytest.raises(ValueError):
+            ex.forward(bad, *args, buf.sel_weight)
+    with pytest.raises(ValueError, match="perm"):
+        ex.rows(x[:-1], *args, k)
+    with pytest.raises(ValueError, match="perm"):
+        ex.rows(x, *args, k - 1)
+    assert torch.equal(ex.forward(x, *args, buf.sel_weight), want)
+    m = int(buf.slot_offsets[-1])                 # the rows that are in a slot, and no others
+    assert torch.equal(ex.rows(x, args[0], args[1][:m], k), ex.rows(x, *args, k)[:m])
+    # a matrix of other strides is taken where the router is not asked
+    assert torch.equal(ex.forward(wide[:, ::2], *args, buf.sel_weight), want)
