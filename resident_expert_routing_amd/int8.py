@@ -237,35 +237,47 @@ class Int8Experts:
         quantize(up, (gu[I:], gs[I:]))
         quantize(down, (self.down[slot], self.down_scale[slot]))
 
-    def check(self, x, T: int) -> None:
+    def check(self, x, T: int, *dtypes) -> None:
         """Refuses token rows that are not [T, H] of a type that quantize takes, on
-        the experts' device, or that want a gradient."""
+        the experts' device, or that want a gradient; and other result types."""
         gpu_tensor(x, "x", self.gate_up.get_device())
         dtype_of(x, "x")
         if tuple(x.shape) != (T, self.H):
             raise ValueError(f"x must have shape [{T}, {self.H}], not {list(x.shape)}")
+        for d in dtypes:
+            if d not in DTYPES:
+                raise ValueError(f"rows are bfloat16, float16 or float32, not {d}")
         _no_gradient("Int8Experts", x)
 
-    def rows(self, x, slot_offsets, perm, k: int, out_dtype=torch.float32) -> torch.Tensor:
+    def rows(self, x, slot_offsets, perm, k: int, out_dtype=torch.float32,
+             inner_dtype=torch.bfloat16) -> torch.Tensor:
         """The experts on the rows of a bucketing: token rows x [T, H] ->
         [T*k, H] (as many rows as perm has), row p from token perm[p] // k; rows
         that are in no slot are undefined.  The second products' inputs are
-        rounded to bf16 before they are quantised."""
-        self.check(x, x.shape[0])
+        rounded to inner_dtype before they are quantised: bf16, half the bytes of
+        float32 and off by at most 2^-9 of a value where the 8-bit step is 2^-7 of
+        the row's largest, whatever x's type; float32 leaves the one rounding to 8
+        bits (fp16 overflows at 65504)."""
+        self.check(x, x.shape[0], out_dtype, inner_dtype)
         if perm.numel() > x.shape[0] * k:
             raise ValueError(f"perm holds {perm.numel()} values, more than the T*k = "
                              f"{x.shape[0] * k} assignments of x")
         q, s = quantize(x)
         h = matmul(q, s, self.gate_up, self.gate_up_scale, offsets=slot_offsets, index=perm,
-                   index_div=k, swiglu=True)
+                   index_div=k, swiglu=True, out_dtype=inner_dtype)
         hq, hs = quantize(h)
         return matmul(hq, hs, self.down, self.down_scale, offsets=slot_offsets,
                       out_dtype=out_dtype)
 
-    def forward(self, x, slot_offsets, perm, sel_weight, pos=None) -> torch.Tensor:
+    def forward(self, x, slot_offsets, perm, sel_weight, pos=None, *, row_dtype=None,
+                inner_dtype=torch.bfloat16) -> torch.Tensor:
         """x [T, H] -> [T, H] in x's type: the layer's experts and their weighted
-        sum, from what moe_route wrote for the batch."""
+        sum, from what moe_route wrote for the batch.  The experts' rows are
+        rounded to row_dtype (x's type if None: the sum of bf16 rows reads half
+        the bytes) before they are weighted and summed; of float32 rows only the
+        sum is rounded.  inner_dtype as in rows."""
         T, k = sel_weight.shape
         self.check(x, T)
         order = RowOrder(perm, T, k, pos)
-        return combine(self.rows(x, slot_offsets, perm, k, x.dtype), order, sel_weight)
+        rows = self.rows(x, slot_offsets, perm, k, row_dtype or x.dtype, inner_dtype)
+        return combine(rows, order, sel_weight).to(x.dtype)

@@ -308,13 +308,15 @@ def layer_step(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, aren
     experts(buf, arena_ptr, slot_stride, stream)
 
 
-def layer_step_int8(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, int8_experts):
+def layer_step_int8(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, int8_experts,
+                    row_dtype=None, inner_dtype=torch.bfloat16):
     """One pass of the layer with its experts in 8-bit integers (int8.Int8Experts,
     one group for each of buf's S slots): route with demand, the experts on the
     rows of the bucketing, combine.  x [T, H] bf16, contiguous; returns [T, H] bf16.
-    On the current stream of x's device.  What does not fit is refused before the
-    demand is counted."""
-    int8_experts.check(x, buf.T)
+    row_dtype, inner_dtype: the types between the products and the sum, as in
+    Int8Experts.forward.  On the current stream of x's device.  What does not fit
+    is refused before the demand is counted."""
+    int8_experts.check(x, buf.T, row_dtype or x.dtype, inner_dtype)
     if x.dtype != torch.bfloat16 or not x.is_contiguous():
         raise ValueError("x must be contiguous bfloat16 rows")
     if (int8_experts.S, int8_experts.H) != (buf.S, buf.H):
@@ -322,7 +324,8 @@ def layer_step_int8(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row,
                          f"buffers of {buf.S} and {buf.H}")
     with torch.cuda.device(x.device):
         route(buf, x, w_router, bias, expert_slot, torch.cuda.current_stream(), hist_row=hist_row)
-        return int8_experts.forward(x, buf.slot_offsets, buf.perm, buf.sel_weight)
+        return int8_experts.forward(x, buf.slot_offsets, buf.perm, buf.sel_weight,
+                                    row_dtype=row_dtype, inner_dtype=inner_dtype)
 
 
 class SharedArena:

@@ -129,6 +129,9 @@ def test_batches_that_do_not_fit_are_refused():
                 wide[:, ::2], wide[:, :H], x.cpu(), x.clone().requires_grad_()):
         with pytest.raises(ValueError):
             step(bad)
+    for kw in (dict(row_dtype=torch.float64), dict(inner_dtype=torch.int8)):
+        with pytest.raises(ValueError, match="rows are"):
+            R.layer_step_int8(buf, x, w_router, None, slot, hist, ex, **kw)
     for s in (S - 1, S + 1):
         with pytest.raises(ValueError, match="slots"):
             step(x, int8.Int8Experts.empty(s, H, I, dev))
@@ -137,6 +140,9 @@ def test_batches_that_do_not_fit_are_refused():
     torch.cuda.synchronize()
     assert torch.equal(hist, counted)
     args = (buf.slot_offsets, buf.perm)
+    fine = dict(row_dtype=torch.float32, inner_dtype=torch.float32)
+    assert torch.equal(R.layer_step_int8(buf, x, w_router, None, slot, hist, ex, **fine),
+                       ex.forward(x, *args, buf.sel_weight, **fine))
     for bad in (x[:-1], torch.cat((x, x)), x.view(torch.int16), x.double(), x[0]):
         with pytest.raises(ValueError):
             ex.forward(bad, *args, buf.sel_weight)
@@ -149,3 +155,48 @@ def test_batches_that_do_not_fit_are_refused():
     assert torch.equal(ex.rows(x, args[0], args[1][:m], k), ex.rows(x, *args, k)[:m])
     # a matrix of other strides is taken where the router is not asked
     assert torch.equal(ex.forward(wide[:, ::2], *args, buf.sel_weight), want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("T", [3, 70])
+def test_types_between_the_products_are_the_callers(T, dtype):
+    """inner_dtype and row_dtype: the same chain call by call, and the weighted sum
+    of float32 rows within its own roundings, (k + 1) * 2^-24 of the magnitudes and
+    one to the type.  The defaults (bf16, x's type) are what they were."""
+    from resident_expert_routing_amd import int8, rows
+    H, k, I, S = 200, 3, 72, 6
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g).to(dtype).cuda()
+    sel = torch.stack([torch.randperm(S, generator=g)[:k] for _ in range(T)])
+    perm = torch.sort(sel.reshape(-1), stable=True).indices.int().cuda()
+    off = torch.zeros(S + 1, dtype=torch.int32)
+    off[1:] = torch.bincount(sel.reshape(-1), minlength=S).cumsum(0)
+    off = off.cuda()
+    w = torch.rand(T, k, generator=g).cuda()
+    ex = int8.Int8Experts.from_weights(*((torch.randn(S, *s, generator=g) / s[1] ** 0.5).cuda()
+                                         for s in ((I, H), (I, H), (H, I))))
+    order = rows.RowOrder(perm, T, k)
+    q, s = int8.quantize(x)
+
+    def chain(inner, row):
+        h = int8.matmul(q, s, ex.gate_up, ex.gate_up_scale, offsets=off, index=perm, index_div=k,
+                        swiglu=True, out_dtype=inner)
+        return int8.matmul(*int8.quantize(h), ex.down, ex.down_scale, offsets=off, out_dtype=row)
+
+    bf16, f32 = torch.bfloat16, torch.float32
+    assert torch.equal(ex.rows(x, off, perm, k), chain(bf16, f32))
+    assert torch.equal(ex.forward(x, off, perm, w), rows.combine(chain(bf16, dtype), order, w))
+    y = chain(f32, f32)
+    assert torch.equal(ex.rows(x, off, perm, k, inner_dtype=f32), y)
+    assert not torch.equal(y, chain(bf16, f32))
+    out = ex.forward(x, off, perm, w, row_dtype=f32, inner_dtype=f32)
+    assert out.dtype == dtype
+    terms = y.cpu().double()[order.pos.cpu().long()] * w.cpu().double().unsqueeze(2)
+    want, mag = terms.sum(1), terms.abs().sum(1)
+    eps = torch.finfo(dtype).eps / 2
+    bound = (k + 1) * 2.0 ** -24 * mag * (1 + eps) + eps * want.abs() + UNDER[dtype]
+    assert bool(((out.cpu().double() - want).abs() <= bound).all())
+    with pytest.raises(ValueError):
+        ex.forward(x, off, perm, w, row_dtype=torch.float64)
+    with pytest.raises(ValueError):
+        ex.forward(x, off, perm, w, inner_dtype=torch.int8)
