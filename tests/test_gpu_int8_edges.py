@@ -200,3 +200,71 @@ def test_types_between_the_products_are_the_callers(T, dtype):
         ex.forward(x, off, perm, w, row_dtype=torch.float64)
     with pytest.raises(ValueError):
         ex.forward(x, off, perm, w, inner_dtype=torch.int8)
+
+
+def block_mapping(M, N, swiglu, G=0):
+    """(tiles dealt to the XCDs in blocks?, items, columns), by the host's rule."""
+    cols = -(-N // (128 if swiglu else 256))
+    groups = min(G, M)
+    if G and (M // 320 + groups) * cols >= 256:
+        R = 320
+    else:
+        cost = {}
+        for r in (320, 256, 192, 128, 64):
+            items = M // r + groups if G else -(-M // r)
+            cost[r] = -(-items * cols // 256) * (r + 256)
+        R = min(cost, key=lambda r: (cost[r], -r))
+    items = M // R + (groups if G else 1)
+    return tiles_of(M, N, swiglu, G)[0] and M > 128 * max(G, 1) and items * cols >= 2048, items, cols
+
+
+@pytest.mark.parametrize("M,N,sizes", [
+    (5201, 33000, None),                                        # 17 items, 129 columns
+    (5120, 32768, None),
+    (2900, 60100, None),
+    (3209, 33000, [700, 0, 321, 64, 900, 1, 640, 574]),         # 18 items
+    (5127, 30000, [2500, 2618]),
+    (4099, 24600, [129, 1000, 0, 65, 320, 1, 191, 639, 4, 300, 257, 700]),
+])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_tiles_in_blocks(M, N, sizes, swiglu):
+    """Products of many tiles deal them to the XCDs in blocks of 8 x 4: every tile
+    is computed once, also at the ends of items and columns, and the rows behind the
+    last group are left.  Sums are below 2^24, so float64 has them exactly."""
+    from resident_expert_routing_amd import int8
+    K = 64
+    N = N // 2 if swiglu else N
+    G = len(sizes) if sizes else 0
+    in_blocks, items, cols = block_mapping(M, N, swiglu, G)
+    say(f"blocks M={M} N={N} G={G} swiglu={swiglu}: {items} items x {cols} columns")
+    assert in_blocks
+    dtype = DTYPES[(M + swiglu) % 2]
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    wide = 2 * N if swiglu else N
+    lead = (G,) if G else ()
+    a = torch.randint(-127, 128, (M, K), device="cuda", generator=gen, dtype=torch.int8)
+    b = torch.randint(-127, 128, (*lead, wide, K), device="cuda", generator=gen, dtype=torch.int8)
+    # y is up to 3, so that fp16 holds the products of gate and up
+    sa = torch.rand(M, device="cuda", generator=gen) * 1e-3 + 1e-4
+    sb = torch.rand(*lead, wide, device="cuda", generator=gen) * 1e-3 + 1e-4
+    edges = np.concatenate([[0], np.cumsum(sizes)]) if G else np.array([0, M])
+    off = torch.as_tensor(edges.astype(np.int32)).cuda() if G else None
+    out = torch.full((M, N), 77.0, dtype=dtype, device="cuda")
+    got = int8.matmul(a, sa, b, sb, offsets=off, swiglu=swiglu, out=out)
+    eps = torch.finfo(dtype).eps / 2
+    for g, (lo, hi) in enumerate(zip(edges, edges[1:])):
+        bg, sg = (b[g], sb[g]) if G else (b, sb)
+        for i in range(int(lo), int(hi), 1024):
+            rows = slice(i, min(i + 1024, int(hi)))
+            z = (a[rows].double() @ bg.double().t().contiguous()) * sa[rows].double()[:, None] * sg
+            if swiglu:
+                gate, up = z[:, :N], z[:, N:]
+                si = gate / (1 + torch.exp(-gate))
+                want = si * up
+                err = 1.1 * 3 * 2.0 ** -24 * (gate * up).abs() + \
+                    (1.5 * gate.abs() + 12) * 2.0 ** -24 * want.abs()
+            else:
+                want, err = z, 3.01 * 2.0 ** -24 * z.abs()
+            bound = err * 1.01 + eps * (want.abs() + err) + UNDER[dtype]
+            assert bool(((got[rows].double() - want).abs() <= bound).all()), (g, i)
+    assert bool((got[int(edges[-1]):] == 77.0).all())
