@@ -268,3 +268,70 @@ def test_tiles_in_blocks(M, N, sizes, swiglu):
             bound = err * 1.01 + eps * (want.abs() + err) + UNDER[dtype]
             assert bool(((got[rows].double() - want).abs() <= bound).all()), (g, i)
     assert bool((got[int(edges[-1]):] == 77.0).all())
+
+
+def small_layer(T, H=256, E=16, k=4, I=96, S=10, seed=1):
+    """layer_step_int8's arguments for a layer of S resident experts."""
+    from resident_expert_routing_amd import int8
+    from resident_expert_routing_amd import runtime as R
+    dev = torch.device("cuda", 0)
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    w_router = (torch.randn(E, H, generator=g) / H ** 0.5).cuda()
+    slot = torch.full((E,), -1, dtype=torch.int32)
+    slot[torch.randperm(E, generator=g)[:S]] = torch.arange(S, dtype=torch.int32)
+    w = [(torch.randn(S, *s, generator=g) / s[1] ** 0.5).cuda() for s in ((I, H), (I, H), (H, I))]
+    hist = torch.zeros(E, dtype=torch.float64, device="cuda")
+    return R.LayerBuffers(T, H, E, k, I, S, dev), x, w_router, None, slot.cuda(), hist, \
+        int8.Int8Experts.from_weights(*w)
+
+
+@pytest.mark.parametrize("T", [1, 33, 300])
+def test_layer_step_captured_and_replayed(T):
+    """The whole int8 layer step in a graph: every replay, with new rows and eager
+    steps between, gives the eager result; so does a step on another stream."""
+    from resident_expert_routing_amd import runtime as R
+    buf, x, w_router, _, slot, hist, ex = small_layer(T)
+    other = small_layer(T)[0]
+
+    def inputs(seed):
+        g = torch.Generator().manual_seed(seed)
+        return torch.randn(T, x.shape[1], generator=g).to(torch.bfloat16).cuda()
+
+    def eager(rows):
+        return R.layer_step_int8(other, rows, w_router, None, slot, torch.zeros_like(hist), ex)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = R.layer_step_int8(buf, x, w_router, None, slot, hist, ex)
+    side.synchronize()
+    assert torch.equal(got, eager(x))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = R.layer_step_int8(buf, x, w_router, None, slot, hist, ex)
+    for seed in (5, 6, 7, 5):
+        rows = inputs(seed)
+        x.copy_(rows)
+        torch.cuda.synchronize()
+        graph.replay()
+        want = eager(rows)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), seed
+
+
+def test_two_layers_at_once():
+    """Two layers on two streams, several steps each: neither sees the other's."""
+    from resident_expert_routing_amd import runtime as R
+    layers = [small_layer(40, seed=1), small_layer(200, I=160, seed=2)]
+    want = [R.layer_step_int8(*layer) for layer in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [[], []]
+    for _ in range(6):
+        for i, (layer, stream) in enumerate(zip(layers, streams)):
+            with torch.cuda.stream(stream):
+                got[i].append(R.layer_step_int8(*layer))
+    torch.cuda.synchronize()
+    for outs, ref in zip(got, want):
+        assert all(torch.equal(o, ref) for o in outs)

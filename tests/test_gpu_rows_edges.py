@@ -161,3 +161,38 @@ def test_sizes_past_32_bits_are_refused():
         int8.matmul(a, s, a, s, index=one.expand(wide))
     with pytest.raises(MoeError):
         int8.matmul(a[:1].expand(wide, 16), s[:1].expand(wide), a, s)
+
+
+def test_orders_and_weights_made_elsewhere():
+    """An order and weights made in inference mode, a backward pass taken twice,
+    recomputation and saved tensors kept on the host: the same gradients."""
+    from torch.utils.checkpoint import checkpoint
+    from resident_expert_routing_amd import rows
+    T, H, k = 30, 88, 4
+    g = torch.Generator().manual_seed(3)
+    perm = torch.randperm(T * k, generator=g).int().cuda()
+    with torch.inference_mode():
+        order = rows.RowOrder(perm.clone(), T, k)
+        routed = torch.rand(T, k, generator=g).cuda()
+    x = torch.randn(T, H, generator=g).cuda().requires_grad_()
+    w = torch.rand(T, k, generator=g).cuda().requires_grad_()
+    go = torch.randn(T, H, generator=g).cuda()
+
+    def layer(x, w):
+        return rows.combine(rows.dispatch(x, order, routed).tanh(), order, w)
+
+    out = layer(x, w)
+    want = torch.autograd.grad(out, [x, w], go, retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(out, [x, w], go), want))
+    again = torch.autograd.grad(checkpoint(layer, x, w, use_reentrant=False), [x, w], go)
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+    with torch.autograd.graph.save_on_cpu(pin_memory=False):
+        out = layer(x, w)
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(out, [x, w], go), want))
+    # the formula, in float64: each token's row goes to k places and comes back
+    xd, wd = x.detach().cpu().double().requires_grad_(), w.detach().cpu().double().requires_grad_()
+    r = routed.cpu().double()
+    ref = ((xd.unsqueeze(1) * r.unsqueeze(2)).tanh() * wd.unsqueeze(2)).sum(1)
+    for a, b in zip(want, torch.autograd.grad(ref, [xd, wd], go.cpu().double())):
+        # a dozen float32 roundings and tanh's few units, sums of at most 88 terms
+        assert float((a.cpu().double() - b).norm()) <= 128 * 2.0 ** -24 * 8 * float(b.norm())
