@@ -12,6 +12,7 @@ current stream of their tensors' device and synchronise nothing.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 from .rows import (DTYPES, RowOrder, combine, dtype_of, gpu_tensor, no_tangent, on_its_device,
@@ -55,7 +56,8 @@ def _laid_out(q: torch.Tensor) -> bool:
 
 
 def _no_gradient(call: str, *tensors) -> None:
-    no_tangent(call, *tensors)
+    if forward_ad._current_level >= 0:
+        no_tangent(call, *tensors)
     for t in tensors:
         if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{call} has no gradient: detach its tensors, or call it under "

@@ -65,8 +65,9 @@ def gpu_tensor(t, what: str, device: int | None = None) -> torch.Tensor:
 def no_tangent(call: str, *tensors) -> None:
     """Refuses tensors that carry a forward-mode tangent (None among them is none):
     the kernels see a tensor's values only, and a result without a tangent would
-    pass for one of derivative zero."""
-    if forward_ad._current_level < 0:  # outside every dual_level: no tensor has one
+    pass for one of derivative zero.  Outside every dual_level no tensor has one;
+    small calls look at forward_ad._current_level themselves, without this call."""
+    if forward_ad._current_level < 0:
         return
     for t in tensors:
         if t is not None and forward_ad.unpack_dual(t).tangent is not None:
@@ -210,7 +211,8 @@ class _Move(torch.autograd.Function):
 
 
 def _move(src, weight, order, there, back):
-    no_tangent("a call of dispatch or combine", src, weight)
+    if forward_ad._current_level >= 0:
+        no_tangent("a call of dispatch or combine", src, weight)
     if torch.is_grad_enabled() and (src.requires_grad
                                     or (weight is not None and weight.requires_grad)):
         return _Move.apply(src, weight, order, there, back)
