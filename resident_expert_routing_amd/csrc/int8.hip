@@ -7,6 +7,10 @@
 // The sums are exact 32-bit integers on the matrix cores, so neither the order
 // of the contraction nor how it is split over waves changes a result; the two
 // scales are applied to the finished sum in float32.
+//
+// Two times "A against B" in a comment are of one form against the other on one
+// card when that choice was made; the times at the head of a kernel's comment are
+// the present ones.
 #include <type_traits>
 
 #include "elements.hpp"
@@ -101,8 +105,9 @@ __device__ __forceinline__ uint32_t as_f32_bits(uint32_t top) {
 // One pass: the row stays in registers between its maximum and its rounding
 // (rows past 256 threads x 4 pieces are read again, from the cache), a wave for a
 // row of up to 4 KB, a workgroup for longer ones.  Bound by memory: 65536 rows of
-// 2048 bf16 take 75 us (403 MB, 5.4 TB/s), 8192 rows of 6144 31 us.  A row that holds an infinity or a NaN gets scale NaN and zeros, so
-// that everything computed from it is NaN.
+// 2048 bf16 take 72 to 74 us (403 MB, 5.4 to 5.6 TB/s).  A row that holds an
+// infinity or a NaN gets scale NaN and zeros, so that everything computed from it
+// is NaN.
 template <typename E>
 __global__ __launch_bounds__(kQThreads) void quantize_rows(const E* __restrict__ x, int M, int K,
                                                            size_t x_stride, int8_t* __restrict__ q,
@@ -365,10 +370,14 @@ __device__ __forceinline__ i32x4 mask_k(i32x4 v, int valid) {  // the first `val
 // group, its W waves the chunks of 64 along K in turn; the integer sums are added
 // through LDS.  b goes from memory straight to the registers of the matrix
 // instruction (lane l: row l % 16, bytes 16 (l / 16) of the chunk), since nothing
-// else in the workgroup uses it.  Bound by the latency of those loads, kSUnroll
-// chunks of a wave in flight: one row, K = 4096, 2N = 4096 (16.8 MB) takes 7.5 us
-// with eight waves, 7.8 with four, and 8.3 with four and half the chunks in
-// flight; one row each of eight such groups 33 us with eight waves, 29.8 with four.
+// else in the workgroup uses it.  One row, K = 4096, 2N = 4096 (16.8 MB) takes 7.3
+// us where the caches hold b and 8.7 from memory.  Bound by how much is in flight:
+// the loads of kSUnroll chunks stand before their products, but the compiler moves
+// them between, and the built kernel has those of two chunks (4 to 6 loads) under
+// way and 71 registers; and one row of 2N = 4096 is 128 workgroups, half the CUs.
+// Eight waves against four, one row: 7.5 us against 7.8; kSUnroll 8 against 4, four
+// waves: 7.8 against 8.3; one row each of eight such groups: 33 us with eight waves
+// against 29.8 with four.
 constexpr int kSUnroll = 8;
 
 template <int W, int MT, bool GLU>
@@ -510,9 +519,10 @@ void launch_stream(const MatArgs& p, bool glu, hipStream_t stream) {
 // hundred rows in each group it is the matrix cores that bound: they are busy 56 %
 // of the cycles of the long gate/up products, at the 1.6 to 1.7 GHz that they are
 // held to under that load; LDS conflicts are 1 % of its accesses.  Dense 8192^3
-// runs at 2.67 POPS, 65536 rows over 130 groups (K 6144, 2N 4096) at 2.06 POPS of
-// exact work, tiles' empty rows not counted.  With few rows in each group the
-// weights bound: 5.4 TB/s at one decode step, 5.2 TB/s at 16384 rows over 166.
+// takes 402 to 413 us (2.67 to 2.73 POPS), 65536 rows over 130 groups (K 6144, 2N
+// 4096) 1.59 to 1.62 ms (2.07 POPS of exact work, tiles' empty rows not counted;
+// 1.54 to 1.76 ms call by call under a trace).  With few rows in each group the
+// weights bound: 5.3 to 5.7 TB/s at one decode step, 5.2 at 16384 rows over 166.
 constexpr int kTWaves = 8;
 constexpr int kStep = 128;  // bytes of K a stage
 constexpr int kColRows = 256;

@@ -14,8 +14,11 @@
 // result on every call.
 //
 // All are bound by memory.  For 8192 tokens of 6144 bf16, top-8 (65536 rows, 805
-// MB): spread 183 us (906 MB, 4.9 TB/s), gather 156 us (5.8 TB/s), spread with
-// dot products 345 us (1.7 GB, 5.0 TB/s).  A copy of 1 GiB runs at 5.1 TB/s.
+// MB): spread 182 us (906 MB, 5.0 TB/s), gather 156 us (5.8 TB/s), spread with
+// dot products 342 us (1.7 GB, 5.0 TB/s).  A copy of 1 GiB runs at 4.7 to 5.1 TB/s.
+// Two times "A against B" below are of one form against the other when that choice
+// was made.  Small calls are bound by dependent loads, a token's picks one after
+// another: 32 tokens of 4096, top-8, spread 5.2 us, 8 tokens gather 4.0.
 #include "elements.hpp"
 
 using namespace moe;
@@ -174,8 +177,8 @@ __global__ __launch_bounds__(kThreads) void spread_rows(RowsArgs p) {
       spread_span<E, N, WEIGHT, false>(p, t, i0);
 }
 
-// gather: a thread sums a piece of a token row over its k rows, eight loads in
-// flight.  An absent pick's load goes to row 0 and its sum is skipped, never
+// gather: a thread sums a piece of a token row over its k rows, the loads of eight
+// rows in flight.  An absent pick's load goes to row 0 and its sum is skipped, never
 // multiplied, so what that row holds does not matter.
 template <typename E, int N>
 __global__ __launch_bounds__(kThreads) void gather_rows(RowsArgs p) {
@@ -290,8 +293,9 @@ __global__ __launch_bounds__(kDotThreads) void rows_dot(RowsArgs p) {
 
 // pos[perm[p]] = p, -1 for assignments that perm does not name.  Up to 4096
 // assignments one workgroup builds the array in LDS (4096: 3.0 us against 3.9 of a
-// fill and a scatter; 16384: 6.9 against 4.3); larger ones take those two.  Should perm name an assignment twice, the larger position
-// stands, whatever the order of the threads.
+// fill and a scatter; 16384: 6.9 against 4.3); larger ones take those two.  Should
+// perm name an assignment twice, the larger position stands, whatever the order of
+// the threads.
 __global__ __launch_bounds__(1024) void positions_lds(const int32_t* __restrict__ perm, int n,
                                                       int32_t* __restrict__ pos,
                                                       int32_t* __restrict__ copy) {

@@ -98,7 +98,11 @@ class RowOrder:
     inverse pos [T, k] (assignment -> row, -1 for none).  moe_positions computes
     pos and copies perm, so a later moe_route may write over the caller's; a pos
     that the caller already has is taken as it is, with perm, and both are
-    copied when a dispatch or combine is recorded for its backward pass."""
+    copied when a dispatch or combine is recorded for its backward pass; it has to
+    be the inverse of this perm.  An order used on another stream than the one it
+    was made on is kept until that stream is done with it, or announced to the
+    allocator as other tensors are (order.pos.record_stream(stream); of an order
+    with a pos of the caller's, order.perm too)."""
 
     def __init__(self, perm: torch.Tensor, T: int, k: int, pos: torch.Tensor | None = None):
         self.T, self.k = int(T), int(k)
