@@ -139,10 +139,10 @@ def matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: tor
     rows, gate then up, and out = silu(gate) * up.  `index` (int32 [M]) with
     index_div names the rows of a: r = index[p] // index_div; without it r = p.
     Rows of `out` in no group, or whose index is negative, are left as they
-    were (a new `out` starts undefined there).  b has to be laid out with its
-    rows at multiples of 16 bytes (quantize and pad_rows do); a is copied if it
-    is not.  There is no gradient: scales and an `out` that want one, or carry
-    a tangent, are refused.
+    were (a new `out` starts undefined there); `out` must not overlap an input.
+    b has to be laid out with its rows at multiples of 16 bytes (quantize and
+    pad_rows do); a is copied if it is not.  There is no gradient: scales and an
+    `out` that want one, or carry a tangent, are refused.
     """
     dev = gpu_tensor(a, "a").get_device()
     if a.dtype != torch.int8 or a.dim() != 2:
