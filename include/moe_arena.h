@@ -749,6 +749,104 @@ typedef struct moe_int8_matmul_args {
 int moe_int8_matmul(const moe_int8_matmul_args* args, hipStream_t stream);
 
 /*
+ * Grouped products in floating point: the experts of moe_route's bucketing in the
+ * model's own element type (bf16, fp16, fp32), for prompts and for training, between
+ * moe_dispatch (or rows named by index) and moe_combine.
+ *
+ * moe_grouped_matmul -- rows p of out [M][N], for offsets[g] <= p < offsets[g+1]:
+ *   z[p][n] = sum_i a[r][i] * b[g][n][i]   (b_across: b[g][i][n])
+ *   out[p][n] = z[p][n], or with swiglu (2N outputs, N gates and then N ups):
+ *               silu(z[p][n]) * z[p][N+n], silu(v) = v / (1 + exp(-v))
+ * with float32 sums and one rounding to the element type.  fp32 products are float32
+ * products.  silu is within (1.25 |v| + 8) * 2^-24 of its value down to v = -174,
+ * below which it is 0.
+ *   r = p, or with index: index[p] / index_div (moe_route's perm and k name the token
+ *   of a row).  Nothing is computed for rows whose r is outside [0, a_rows), nor for
+ *   rows in no group (before offsets[0], from offsets[G] on): with zero_rest they are
+ *   set to zero, without it left as they were.  Offsets have to ascend; they are cut
+ *   to [0, M].
+ * Inputs : a [a_rows][K], rows a_stride elements apart; offsets [G+1] int32; b: for
+ *          each group N (2N) rows of K elements b_stride apart, or with b_across K rows
+ *          of N (2N); groups b_group_stride elements apart (0: all groups share one).
+ * Outputs: out, rows out_stride elements apart (>= N); with swiglu pre (nullable), the
+ *          products z before SwiGLU [M][2N] in the element type, rows pre_stride apart,
+ *          for moe_swiglu_backward; written for computed rows only, and set to zero
+ *          or left for others as out is where their group's rows are.  Neither may
+ *          overlap an input or the other.  Everything may start at any element.
+ * Errors : MOE_EINVAL for null or misaligned pointers (the element's size; 4 bytes for
+ *          int32), a bad size, stride, dtype or flag, index without index_div >= 1,
+ *          fewer rows of a than M without index, or pre without swiglu;
+ *          MOE_EUNSUPPORTED for N or K > 2^24, M > 2^30 or G > MOE_MAX_S.
+ *          M = 0 is valid and does nothing.  No workspace.
+ * The gradient of a is this call too: da[p] = sum_n dz[p][n] * b[g][n] has dz for a and
+ * the other b_across.
+ */
+typedef struct moe_grouped_matmul_args {
+  int M, N, K, G, dtype;
+  int swiglu, b_across, zero_rest;
+  int a_rows;
+  const void* a;
+  size_t a_stride;
+  const int32_t* index;
+  int index_div;
+  const int32_t* offsets;
+  const void* b;
+  size_t b_stride;
+  size_t b_group_stride;
+  void* out;
+  size_t out_stride;
+  void* pre;
+  size_t pre_stride;
+} moe_grouped_matmul_args;
+
+int moe_grouped_matmul(const moe_grouped_matmul_args* args, hipStream_t stream);
+
+/*
+ * moe_grouped_outer -- the gradient of the groups' matrices:
+ *   out[g][l][r] = sum over offsets[g] <= p < offsets[g+1] of left[pl][l] * right[pr][r]
+ * with float32 sums over ascending p in a fixed order and one rounding; a group without
+ * rows gets zeros.  pl = p, or left_index[p] / left_div; pr likewise; a row p for which
+ * either is outside its array adds nothing.  With left = dz and right = a this is the
+ * gradient of b [N][K]; the other way round, that of b [K][N].
+ * Inputs : left [left_rows][L], right [right_rows][R], rows their strides apart;
+ *          offsets [G+1] int32, cut to [0, M].
+ * Output : out [G][L][R], rows out_stride elements apart, groups out_group_stride; must
+ *          not overlap an input.
+ * Errors : as moe_grouped_matmul.  M = 0 is valid and writes zeros (left and right may
+ *          then be NULL).
+ */
+typedef struct moe_grouped_outer_args {
+  int M, L, R, G, dtype;
+  int left_rows, right_rows;
+  const void* left;
+  size_t left_stride;
+  const int32_t* left_index;
+  int left_div;
+  const void* right;
+  size_t right_stride;
+  const int32_t* right_index;
+  int right_div;
+  const int32_t* offsets;
+  void* out;
+  size_t out_stride;
+  size_t out_group_stride;
+} moe_grouped_outer_args;
+
+int moe_grouped_outer(const moe_grouped_outer_args* args, hipStream_t stream);
+
+/*
+ * moe_swiglu_backward -- the gradient of h = silu(g) * u for rows of pre = [g | u]:
+ *   dpre[m][n] = dout[m][n] * u * (s + g * s * (1 - s)),  dpre[m][N+n] = dout[m][n] * g * s
+ * with s = 1 / (1 + exp(-g)) (0 from g = -88 down), in float32 and rounded once.
+ * pre and dpre [M][2N], dout [M][N] of one element type, rows their strides apart, at any
+ * element; dpre may be pre.  Errors : MOE_EINVAL, MOE_EUNSUPPORTED as above.  M = 0 is
+ * valid and does nothing.
+ */
+int moe_swiglu_backward(int M, int N, int dtype, const void* pre, size_t pre_stride,
+                        const void* dout, size_t dout_stride, void* dpre, size_t dpre_stride,
+                        hipStream_t stream);
+
+/*
  * moe_test_mxfp4_probe -- test-only: one wave runs one block-scaled MXFP4
  * matrix instruction on raw per-lane operands, so a test can check the
  * hardware's decoding of E2M1 codes and E8M0 scales and its lane layout.

@@ -51,6 +51,7 @@ EXPORTS = ("moe_status_string", "moe_mxfp4_row_bytes", "moe_act_row_bytes", "moe
            "moe_history_save", "moe_history_load", "moe_boot_plan", "moe_history_scale",
            "moe_positions", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
            "moe_combine_backward", "moe_int8_row_bytes", "moe_int8_quantize", "moe_int8_matmul",
+           "moe_grouped_matmul", "moe_grouped_outer", "moe_swiglu_backward",
            "arena_load_slot", "moe_hot_pick", "moe_hot_install", "moe_replan", "moe_test_mxfp4_probe",
            "moe_test_stream_read", "moe_test_mfma_loop")
 
@@ -107,6 +108,30 @@ class Int8MatmulArgs(ctypes.Structure):
                 ("b_group_stride", ctypes.c_size_t), ("b_scale", ctypes.c_void_p),
                 ("b_scale_group_stride", ctypes.c_size_t), ("out", ctypes.c_void_p),
                 ("out_stride", ctypes.c_size_t), ("out_dtype", ctypes.c_int)]
+
+
+class GroupedMatmulArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("G", ctypes.c_int), ("dtype", ctypes.c_int), ("swiglu", ctypes.c_int),
+                ("b_across", ctypes.c_int), ("zero_rest", ctypes.c_int),
+                ("a_rows", ctypes.c_int), ("a", ctypes.c_void_p), ("a_stride", ctypes.c_size_t),
+                ("index", ctypes.c_void_p), ("index_div", ctypes.c_int),
+                ("offsets", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("b_stride", ctypes.c_size_t), ("b_group_stride", ctypes.c_size_t),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_size_t),
+                ("pre", ctypes.c_void_p), ("pre_stride", ctypes.c_size_t)]
+
+
+class GroupedOuterArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("L", ctypes.c_int), ("R", ctypes.c_int),
+                ("G", ctypes.c_int), ("dtype", ctypes.c_int), ("left_rows", ctypes.c_int),
+                ("right_rows", ctypes.c_int), ("left", ctypes.c_void_p),
+                ("left_stride", ctypes.c_size_t), ("left_index", ctypes.c_void_p),
+                ("left_div", ctypes.c_int), ("right", ctypes.c_void_p),
+                ("right_stride", ctypes.c_size_t), ("right_index", ctypes.c_void_p),
+                ("right_div", ctypes.c_int), ("offsets", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_size_t),
+                ("out_group_stride", ctypes.c_size_t)]
 
 
 MOE_STAGE_EVENTS = 5
@@ -180,6 +205,12 @@ def load() -> ctypes.CDLL:
     lib.moe_int8_quantize.restype = i
     lib.moe_int8_matmul.argtypes = [ctypes.POINTER(Int8MatmulArgs), vp]
     lib.moe_int8_matmul.restype = i
+    lib.moe_grouped_matmul.argtypes = [ctypes.POINTER(GroupedMatmulArgs), vp]
+    lib.moe_grouped_matmul.restype = i
+    lib.moe_grouped_outer.argtypes = [ctypes.POINTER(GroupedOuterArgs), vp]
+    lib.moe_grouped_outer.restype = i
+    lib.moe_swiglu_backward.argtypes = [i, i, i, vp, sz, vp, sz, vp, sz, vp]
+    lib.moe_swiglu_backward.restype = i
     lib.moe_test_mxfp4_probe.argtypes = [i, vp, vp, vp, vp, vp, vp]
     lib.moe_test_mxfp4_probe.restype = i
     lib.moe_test_stream_read.argtypes = [vp, ctypes.c_size_t, vp, i, vp]
@@ -458,6 +489,41 @@ def moe_int8_matmul(M, N, K, G, swiglu, a_rows, a, a_stride, a_scale, index, ind
                           _ptr(b_scale), int(b_scale_group_stride), _ptr(out), int(out_stride),
                           int(out_dtype))
     return int(load().moe_int8_matmul(ctypes.byref(args), _stream(stream)))
+
+
+def moe_grouped_matmul(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, a, a_stride, index,
+                       index_div, offsets, b, b_stride, b_group_stride, out, out_stride, pre=None,
+                       pre_stride=0, stream=None) -> int:
+    if not fits(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, index_div):
+        return MOE_EUNSUPPORTED
+    args = GroupedMatmulArgs(int(M), int(N), int(K), int(G), int(dtype), int(swiglu),
+                             int(b_across), int(zero_rest), int(a_rows), _ptr(a), int(a_stride),
+                             _ptr(index), int(index_div), _ptr(offsets), _ptr(b), int(b_stride),
+                             int(b_group_stride), _ptr(out), int(out_stride), _ptr(pre),
+                             int(pre_stride))
+    return int(load().moe_grouped_matmul(ctypes.byref(args), _stream(stream)))
+
+
+def moe_grouped_outer(M, L, R, G, dtype, left_rows, right_rows, left, left_stride, left_index,
+                      left_div, right, right_stride, right_index, right_div, offsets, out,
+                      out_stride, out_group_stride, stream=None) -> int:
+    if not fits(M, L, R, G, dtype, left_rows, right_rows, left_div, right_div):
+        return MOE_EUNSUPPORTED
+    args = GroupedOuterArgs(int(M), int(L), int(R), int(G), int(dtype), int(left_rows),
+                            int(right_rows), _ptr(left), int(left_stride), _ptr(left_index),
+                            int(left_div), _ptr(right), int(right_stride), _ptr(right_index),
+                            int(right_div), _ptr(offsets), _ptr(out), int(out_stride),
+                            int(out_group_stride))
+    return int(load().moe_grouped_outer(ctypes.byref(args), _stream(stream)))
+
+
+def moe_swiglu_backward(M, N, dtype, pre, pre_stride, dout, dout_stride, dpre, dpre_stride,
+                        stream=None) -> int:
+    if not fits(M, N, dtype):
+        return MOE_EUNSUPPORTED
+    return int(load().moe_swiglu_backward(int(M), int(N), int(dtype), _ptr(pre), int(pre_stride),
+                                          _ptr(dout), int(dout_stride), _ptr(dpre),
+                                          int(dpre_stride), _stream(stream)))
 
 
 def moe_test_mxfp4_probe(shape, a, a_scale, b, b_scale, d, stream=None) -> int:

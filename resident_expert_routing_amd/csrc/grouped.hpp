@@ -1,0 +1,601 @@
+// Tiled products of ragged groups of rows in floating point: the kernels that
+// grouped_bf16.hip, grouped_fp16.hip and grouped_fp32.hip build for their type.
+//
+//   rows   out[p,n] = sum_k a[r(p),k] * b[g,n,k]     rows p of group g
+//   outer  out[g,l,r] = sum_p left[p,l] * right[p,r]
+//
+// Both are tiles of a left operand against a right one over a contraction.  An
+// operand lies with its contraction along the rows of memory (a, and b of layout
+// [N][K]) or across them (b of layout [K][N], left and right of outer).  It is
+// staged in LDS as it lies, in whole pieces of 16 bytes; one that lies across is
+// read from LDS by the transposing loads, four contraction steps a lane.
+#pragma once
+
+#include <type_traits>
+
+#include "groups.hpp"
+
+namespace moe {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+struct RowsProduct {
+  int M, N, K, G, a_rows, index_div;  // N: columns of out; with SwiGLU b has 2N
+  const void *a, *b;
+  void *out, *pre;  // pre: the products before SwiGLU, [M][2N], or null
+  const int32_t *index, *offsets;
+  size_t a_stride, b_stride, b_group_stride, out_stride, pre_stride;  // elements
+  bool zero_rest;  // rows that nothing is computed for become zero
+};
+
+struct OuterProduct {
+  int M, L, R, G, left_rows, right_rows, left_div, right_div;
+  const void *left, *right;
+  void* out;
+  const int32_t *left_index, *right_index, *offsets;
+  size_t left_stride, right_stride, out_stride, out_group_stride;  // elements
+};
+
+template <typename E>
+int launch_rows_product(const RowsProduct& p, bool across, bool glu, hipStream_t stream);
+template <typename E>
+int launch_outer_product(const OuterProduct& p, hipStream_t stream);
+
+// acc += products of 16 x 16 fragments over 64 bytes of contraction, sums in float32.
+// A lane holds 16 bytes of row (lane & 15) from byte 16 * (lane >> 4) on; it gets rows
+// 4 * (lane >> 4) .. + 3 of w against row (lane & 15) of x.
+template <typename E>
+__device__ __forceinline__ f32x4 mma(i32x4 w, i32x4 x, f32x4 acc);
+template <>
+__device__ __forceinline__ f32x4 mma<Bf16>(i32x4 w, i32x4 x, f32x4 acc) {
+  typedef __bf16 V __attribute__((ext_vector_type(8)));
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, w),
+                                                 __builtin_bit_cast(V, x), acc, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mma<Fp16>(i32x4 w, i32x4 x, f32x4 acc) {
+  typedef _Float16 V __attribute__((ext_vector_type(8)));
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, w),
+                                                __builtin_bit_cast(V, x), acc, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mma<float>(i32x4 w, i32x4 x, f32x4 acc) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(w[e]), __int_as_float(x[e]), acc, 0,
+                                               0, 0);
+  return acc;
+}
+
+constexpr int kTWaves = 8;     // two down by four across
+constexpr int kTThreads = kTWaves * kWave;
+constexpr int kStep = 128;     // bytes of contraction a stage
+constexpr int kCols = 256;     // columns of a tile
+constexpr int kMostRows = 320;
+constexpr int kOutBytes = 16384;  // LDS that a wave's results pass through
+constexpr int kTileLds = 2 * (kMostRows + kCols) * kStep;
+
+// Where an operand that lies across its contraction is in LDS: a stage is kStep /
+// sizeof(E) rows of W elements, 16-byte pieces of a row swapped so that the places
+// one read takes in 16 rows spread over the banks.
+template <typename E, int W>
+__device__ __forceinline__ int swap_piece(int piece, int row) {
+  if constexpr (sizeof(E) == 2) {
+    constexpr int kUnits = W / 16;  // 32 bytes, the 16 columns of a fragment
+    const int g = ((row & 3) | ((row >> 3) & 3) << 2) & (kUnits - 1);
+    return piece ^ (2 * g);
+  } else {
+    return piece ^ (4 * ((row >> 2) & 3));
+  }
+}
+
+// 16 bytes of contraction of the lane's column (lane & 15) from column `at` on, half
+// `half` of the stage.
+template <typename E, int W>
+__device__ __forceinline__ i32x4 read_across(const uint8_t* stage, int at, int half) {
+  const int lane = threadIdx.x & 63, x = lane & 15, quad = lane >> 4;
+  constexpr int kRow = W * (int)sizeof(E);
+  i32x4 v;
+  if constexpr (sizeof(E) == 2) {
+    typedef short V __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) V LV;
+    typedef int I2 __attribute__((ext_vector_type(2)));
+    const int row = 32 * half + 8 * quad + (x >> 2);
+    const int c = at / 8 + ((x & 3) >> 1);
+    const uint8_t* from =
+        stage + row * kRow + 16 * swap_piece<E, W>(c, row) + 8 * (x & 1);
+    const I2 lo = __builtin_bit_cast(I2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LV*)from));
+    const I2 hi =
+        __builtin_bit_cast(I2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LV*)(from + 4 * kRow)));
+    v[0] = lo[0], v[1] = lo[1], v[2] = hi[0], v[3] = hi[1];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = 16 * half + 4 * quad + e;
+      v[e] = *(const int*)(stage + row * kRow + 16 * swap_piece<E, W>((at + x) / 4, row) +
+                           4 * (x & 3));
+    }
+  }
+  return v;
+}
+
+// What a load of a stage takes: 16 bytes at p, of which n elements count (n <= 0: none).
+template <typename E>
+struct Src {
+  const E* p;
+  int n;
+};
+
+// The main loop.  A stage holds kRows rows (LEFT across: columns) of the left operand
+// and 256 of the right one, kStep bytes of contraction each, in a ring of S; from_left(i, j,
+// row, piece) and from_right say where the 16-byte piece of stage i is in memory that the
+// wave's load j of the operand takes, `row` the row (across: the contraction step) and
+// `piece` the piece in it.  DMA: loads go to
+// LDS directly, and pieces count whole or not at all; otherwise they pass through
+// registers, from any address and cut at any element.
+//
+// A wave has 16 * MF rows by 64 columns.  Its fragments are read two groups of products
+// ahead (the right operand's a half stage ahead), and the loads of stage i + S - 1 are
+// issued one for each group; a wave at its products goes before the SIMD's other one at
+// its loads.
+template <typename E, bool LEFT, bool RIGHT, bool SPLIT, int MF, int S, bool DMA, bool ONCE,
+          typename FL, typename FR>
+__device__ __forceinline__ void products(uint8_t* smem, int steps, FL from_left, FR from_right,
+                                         f32x4 (&acc)[MF][4]) {
+  constexpr int kRows = 32 * MF;
+  constexpr int kStage = (kRows + kCols) * kStep;
+  constexpr int kLoadsL = kRows / 8 / kTWaves, kLoadsR = kCols / 8 / kTWaves;
+  constexpr int kLoads = kLoadsL + kLoadsR;
+  constexpr int kPiece = 16 / (int)sizeof(E);
+  static_assert(S * kStage <= kTileLds, "LDS");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, quad = lane >> 4;
+  const int wm = wave >> 2, wn = wave & 3;
+
+  // load j of a wave: LDS bytes 1024 * (wave * n + j) + 16 * lane of the operand's part
+  auto source = [&](int i, int j) {
+    if (j < kLoadsR) {
+      const int u = (wave * kLoadsR + j) * 64 + lane;
+      if constexpr (RIGHT) {
+        const int row = u / (kCols / kPiece);
+        return from_right(i, j, row, swap_piece<E, kCols>(u % (kCols / kPiece), row));
+      } else {
+        return from_right(i, j, u / 8, (u & 7) ^ ((u >> 3) & 7));
+      }
+    }
+    const int u = (wave * kLoadsL + j - kLoadsR) * 64 + lane;
+    if constexpr (LEFT) {
+      const int row = u / (kRows / kPiece);
+      return from_left(i, j - kLoadsR, row, swap_piece<E, kRows>(u % (kRows / kPiece), row));
+    } else {
+      return from_left(i, j - kLoadsR, u / 8, (u & 7) ^ ((u >> 3) & 7));
+    }
+  };
+  auto place = [&](int i, int j) {  // of the wave's load j
+    return smem + (i % S) * kStage +
+           (j < kLoadsR ? kRows * kStep + (wave * kLoadsR + j) * 1024
+                        : (wave * kLoadsL + j - kLoadsR) * 1024);
+  };
+  auto load = [&](int i, int j) {
+    const Src<E> s = source(i, j);
+    const uint8_t* from = s.n > 0 ? (const uint8_t*)s.p : kZeros;
+    if (ONCE && j < kLoadsR)
+      dma16_past(from, place(i, j));
+    else
+      dma16(from, place(i, j));
+  };
+
+  auto stage = [&](int i, auto more) {
+    const uint8_t* at = smem + (i % S) * kStage;
+    const int slot[2] = {16 * (quad ^ (col & 7)), 16 * ((4 + quad) ^ (col & 7))};
+    auto frag = [&](int x) -> i32x4 {
+      if constexpr (LEFT)
+        return read_across<E, kRows>(at, (wm * MF + x % MF) * 16, x / MF);
+      else
+        return *(const i32x4*)(at + ((wm * MF + x % MF) * 16 + col) * kStep + slot[x / MF]);
+    };
+    auto weight = [&](int c, int s) -> i32x4 {
+      const uint8_t* r = at + kRows * kStep;
+      if constexpr (RIGHT)
+        return read_across<E, kCols>(
+            r, SPLIT ? (s >= 2 ? 128 : 0) + wn * 32 + 16 * (s & 1) : wn * 64 + 16 * s, c);
+      else
+        return *(const i32x4*)(r + (wn * 64 + 16 * s + col) * kStep + slot[c]);
+    };
+    i32x4 w[3], v[2][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[0][s] = weight(0, s);
+    w[0] = frag(0);
+    w[1] = frag(1);
+#pragma unroll
+    for (int x = 0; x < 2 * MF; ++x) {
+      if (x + 2 < 2 * MF) w[(x + 2) % 3] = frag(x + 2);
+#pragma unroll
+      for (int s = x; x < MF && s < 4; s += MF) v[1][s] = weight(1, s);
+      if constexpr (decltype(more)::value) {
+#pragma unroll
+        for (int j = x; j < kLoads; j += 2 * MF) load(i + S - 1, j);
+      }
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) acc[x % MF][s] = mma<E>(v[x / MF][s], w[x % 3], acc[x % MF][s]);
+      __builtin_amdgcn_s_setprio(0);
+    }
+  };
+
+  if constexpr (DMA) {
+    // At the top of stage i its loads, issued S - 1 stages ago, have to have landed
+    // (those of the S - 2 stages after it may still be in flight), and every wave has to
+    // be done with the stage before, whose place is loaded next.
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+      if (i < steps) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) load(i, j);
+      }
+    int i = 0;
+    for (; i + S - 1 < steps; ++i) {
+      wait_loads<(S - 2) * kLoads>();
+      barrier();
+      stage(i, std::true_type{});
+    }
+    wait_loads<0>();
+    barrier();
+    for (; i < steps; ++i) stage(i, std::false_type{});
+  } else {
+    Piece<E> u[kLoads];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const Src<E> s = source(i, j);
+        if (s.n > 0)
+          u[j].load_upto(s.p, s.n);
+        else
+          u[j] = Piece<E>{};
+      }
+    };
+    auto put = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) __builtin_memcpy(place(i, j) + 16 * lane, u[j].e, 16);
+    };
+    static_assert(S == 2, "two stages");
+    if (steps > 0) fetch(0), put(0);
+    for (int i = 0; i < steps; ++i) {
+      __syncthreads();  // stage i is in place, and nobody reads the one before
+      if (i + 1 < steps) fetch(i + 1);
+      stage(i, std::false_type{});
+      if (i + 1 < steps) put(i + 1);
+    }
+  }
+}
+
+// NS fragments of 16 columns of a wave's rows leave through its part of LDS, so that
+// lanes store consecutive bytes of a row of out: value(f, s, e) is column 4 * quad + e of
+// fragment s (JOIN: 4 * NS * quad + 4 * s + e) in row `col` of fragment f.  to(row, c)
+// says where the 16-byte piece c of the wave's row goes and how many of its elements (n
+// <= 0: none), and whether as zeros.  The stores pass the caches by.
+template <typename E>
+struct Dst {
+  E* p;
+  int n;
+  bool zero;
+};
+template <typename E, int MF, int NS, bool JOIN, typename V, typename T>
+__device__ __forceinline__ void store_rows(uint8_t* mine, V value, T to) {
+  constexpr int kRowBytes = 16 * NS * (int)sizeof(E), kPieces = kRowBytes / 16;
+  constexpr int kPart = part_of(MF, kOutBytes / kRowBytes / 16);
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+  auto place = [&](int x, int c) {
+    return mine + x * kRowBytes + 16 * (c ^ (x & (kPieces - 1) & 7));
+  };
+#pragma unroll
+  for (int f0 = 0; f0 < MF; f0 += kPart) {
+    wave_exchange();  // what was here has been read
+#pragma unroll
+    for (int f = f0; f < f0 + kPart; ++f)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        Piece<E, 4> o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.e[e] = from_f32<E>(value(f, s, e));
+        const int byte = (JOIN ? 4 * NS * quad + 4 * s : 16 * s + 4 * quad) * (int)sizeof(E);
+        __builtin_memcpy(place((f - f0) * 16 + col, byte / 16) + byte % 16, o.e, sizeof(o.e));
+      }
+    wave_exchange();
+    constexpr int kPer = 64 / kPieces;  // rows of a store instruction
+#pragma unroll
+    for (int x0 = 0; x0 < kPart * 16; x0 += kPer) {
+      const int x = x0 + lane / kPieces, c = lane % kPieces;
+      const Dst<E> d = to(f0 * 16 + x, c);
+      if (d.n <= 0) continue;
+      Piece<E> o{};
+      if (!d.zero) __builtin_memcpy(o.e, place(x, c), 16);
+      if (d.n >= Piece<E>::kN)
+        o.store_past(d.p);
+      else
+        o.store_head(d.p, d.n);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+struct Live {
+  uint8_t row[kMostRows];  // 1: computed, 2: set to zero, 0: left
+};
+
+template <typename E, bool ACROSS, bool GLU, int MF, int S, bool DMA, bool ONCE>
+__device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, int n0,
+                                          uint8_t* smem, Live& live) {
+  constexpr int kPiece = 16 / (int)sizeof(E);
+  constexpr int kC = kStep / (int)sizeof(E);  // contraction steps of a stage
+  constexpr bool JOIN = !ACROSS;              // a lane ends with consecutive columns
+  constexpr int kOut = GLU ? 8 : 16;          // how many
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave >> 2, wn = wave & 3;
+  const E* b = (const E*)p.b + (size_t)r.g * p.b_group_stride;
+
+  // the rows of a and (along) of b that the lane loads
+  constexpr int kLoadsL = MF / 2, kLoadsR = kCols / 64;
+  const E* arow[kLoadsL];
+#pragma unroll
+  for (int j = 0; j < kLoadsL; ++j) {
+    const int m = r.lo + (wave * kLoadsL + j) * 8 + (lane >> 3);
+    arow[j] = (const E*)p.a + (size_t)max(source_row(p, min(m, r.hi - 1)), 0) * p.a_stride;
+  }
+  const E* brow[ACROSS ? 1 : kLoadsR];
+  if constexpr (!ACROSS) {
+    // row 64 w + 16 s + x of b in LDS is the row that gives lane quad q of the result the
+    // columns kOut * q + 4 * s + i
+#pragma unroll
+    for (int j = 0; j < kLoadsR; ++j) {
+      const int l = (wave * kLoadsR + j) * 8 + (lane >> 3);
+      const int s = (l >> 4) & 3, x = l & 15;
+      const int n = n0 + (l >> 6) * 4 * kOut + kOut * (x >> 2) + 4 * (GLU ? s & 1 : s) + (x & 3);
+      brow[j] = b + (size_t)(min(n, p.N - 1) + (GLU && s >= 2 ? p.N : 0)) * p.b_stride;
+    }
+  }
+  auto from_left = [&](int i, int j, int, int piece) {
+    const int k = i * kC + piece * kPiece;
+    return Src<E>{arow[j] + k, p.K - k};
+  };
+  auto from_right = [&](int i, int j, int row, int piece) {
+    if constexpr (ACROSS) {
+      const int k = i * kC + row, c = piece * kPiece;
+      const int n = n0 + (GLU ? c & 127 : c);
+      return Src<E>{b + (size_t)k * p.b_stride + (GLU && c >= 128 ? p.N : 0) + n,
+                    k < p.K ? p.N - n : 0};
+    } else {
+      const int k = i * kC + piece * kPiece;
+      return Src<E>{brow[j] + k, p.K - k};
+    }
+  };
+
+  f32x4 acc[MF][4] = {};
+  for (int t = threadIdx.x; t < 32 * MF; t += kTThreads) {
+    const bool in = r.lo + t < r.hi;
+    live.row[t] = !in ? 0 : source_row(p, r.lo + t) >= 0 ? 1 : p.zero_rest ? 2 : 0;
+  }
+  products<E, false, ACROSS, GLU, MF, S, DMA, ONCE>(smem, (p.K + kC - 1) / kC, from_left,
+                                                    from_right, acc);
+  barrier();  // every wave has read the last stage
+  uint8_t* mine = smem + wave * kOutBytes;
+  auto to = [&](void* out, size_t stride, int at, int N, int row, int c) {
+    const int t = wm * MF * 16 + row, n = at + c * kPiece;
+    return Dst<E>{(E*)out + (size_t)(r.lo + t) * stride + n, live.row[t] ? N - n : 0,
+                  live.row[t] == 2};
+  };
+  if constexpr (GLU) {
+    const int n = n0 + wn * 32;
+    if (p.pre) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        store_rows<E, MF, 2, JOIN>(
+            mine, [&](int f, int s, int e) { return acc[f][2 * h + s][e]; },
+            [&](int row, int c) {
+              return to((E*)p.pre + (size_t)h * p.N, p.pre_stride, n, p.N, row, c);
+            });
+    }
+#pragma unroll
+    for (int f = 0; f < MF; ++f) {
+      float g[8], u[8], y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = acc[f][j / 4][j % 4], u[j] = acc[f][2 + j / 4][j % 4];
+      swiglu(g, u, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[f][j / 4][j % 4] = y[j];
+    }
+    store_rows<E, MF, 2, JOIN>(
+        mine, [&](int f, int s, int e) { return acc[f][s][e]; },
+        [&](int row, int c) { return to(p.out, p.out_stride, n, p.N, row, c); });
+  } else {
+    store_rows<E, MF, 4, JOIN>(
+        mine, [&](int f, int s, int e) { return acc[f][s][e]; },
+        [&](int row, int c) { return to(p.out, p.out_stride, n0 + wn * 64, p.N, row, c); });
+  }
+}
+
+// Rows that nothing is computed for.
+template <typename E>
+__device__ __forceinline__ void zero_rows(void* out, size_t stride, const Rows& r, int n0, int n1) {
+  constexpr int kPiece = 16 / (int)sizeof(E);
+  const int pieces = (n1 - n0 + kPiece - 1) / kPiece;
+  for (int t = threadIdx.x; t < (r.hi - r.lo) * pieces; t += blockDim.x) {
+    const int n = n0 + t % pieces * kPiece;
+    const Piece<E> o{};
+    o.store_upto((E*)out + (size_t)(r.lo + t / pieces) * stride + n, n1 - n);
+  }
+}
+
+template <typename E, bool ACROSS, bool GLU, bool DMA>
+__global__ __launch_bounds__(kTThreads, 2) void rows_tiles(RowsProduct p, int R, int cols,
+                                                          bool blocks, int64_t first) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kTileLds];
+  __shared__ Live live;
+  __shared__ int counts[kTWaves];
+  int64_t item, total = 0;
+  int col;
+  Rows r;
+  tile_of(first + blockIdx.x, blocks, cols, item, col);
+  if (col >= cols) return;
+  constexpr int kWide = GLU ? kCols / 2 : kCols;
+  const int n0 = col * kWide;
+  if (!find_rows(p, item, R, counts, r, total)) {
+    if (p.zero_rest && rest_rows(p, item - total, R, r))
+      zero_rows<E>(p.out, p.out_stride, r, n0, min(n0 + kWide, p.N));
+    return;
+  }
+  const int rows = r.hi - r.lo;
+  if constexpr (DMA) {
+    if (rows <= 64 && r.all)
+      rows_tile<E, ACROSS, GLU, 2, 3, true, true>(p, r, n0, smem, live);
+    else if (rows <= 64)
+      rows_tile<E, ACROSS, GLU, 2, 3, true, false>(p, r, n0, smem, live);
+    else if (rows <= 128)
+      rows_tile<E, ACROSS, GLU, 4, 3, true, false>(p, r, n0, smem, live);
+    else if (rows <= 192)
+      rows_tile<E, ACROSS, GLU, 6, 2, true, false>(p, r, n0, smem, live);
+    else if (rows <= 256)
+      rows_tile<E, ACROSS, GLU, 8, 2, true, false>(p, r, n0, smem, live);
+    else
+      rows_tile<E, ACROSS, GLU, 10, 2, true, false>(p, r, n0, smem, live);
+  } else {
+    if (rows <= 64)
+      rows_tile<E, ACROSS, GLU, 2, 2, false, false>(p, r, n0, smem, live);
+    else if (rows <= 128)
+      rows_tile<E, ACROSS, GLU, 4, 2, false, false>(p, r, n0, smem, live);
+    else
+      rows_tile<E, ACROSS, GLU, 8, 2, false, false>(p, r, n0, smem, live);
+  }
+}
+
+// Most rows of a tile: more rows share a load of b's, but a product of few tiles may
+// then leave more of the 256 CUs without one; its time goes as rounds * (rows + 256).
+inline int rows_of_tile(int M, int G, int cols, bool dma) {
+  const int64_t groups = G < M ? G : M;
+  const int most = dma ? kMostRows : 256;
+  if ((M / most + groups) * cols >= 256) return most;
+  int best = most;
+  int64_t least = INT64_MAX;
+  for (int R : {320, 256, 192, 128, 64}) {
+    if (R > most) continue;
+    const int64_t cost = ((M / R + groups) * cols + 255) / 256 * (R + 256);
+    if (cost < least) best = R, least = cost;
+  }
+  return best;
+}
+
+template <typename E, bool ACROSS, bool GLU>
+void launch_rows_tiles(const RowsProduct& p, bool dma, hipStream_t stream) {
+  const int per = GLU ? kCols / 2 : kCols, cols = (p.N + per - 1) / per;
+  const int R = rows_of_tile(p.M, p.G, cols, dma);
+  const int64_t items = max_items(p.M, p.G, R) + (p.zero_rest ? 2 : 0);
+  const bool blocks = p.M > 128 * (int64_t)p.G && items * cols >= 2048;
+  const int64_t tiles =
+      blocks ? (int64_t)up_to((items + kBlockItems - 1) / kBlockItems *
+                                  ((cols + kBlockCols - 1) / kBlockCols), 8) *
+                   kBlockItems * kBlockCols
+             : items * cols;
+  for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+    const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
+    if (dma)
+      rows_tiles<E, ACROSS, GLU, true><<<grid, kTThreads, 0, stream>>>(p, R, cols, blocks, first);
+    else
+      rows_tiles<E, ACROSS, GLU, false><<<grid, kTThreads, 0, stream>>>(p, R, cols, blocks, first);
+  }
+}
+
+// Whether rows of n elements, `stride` apart, consist of whole 16-byte pieces.
+template <typename E>
+inline bool whole_pieces(const void* p, size_t stride, size_t group_stride, int n) {
+  constexpr size_t kPiece = 16 / sizeof(E);
+  return aligned(p, 16) && stride % kPiece == 0 && group_stride % kPiece == 0 && n % kPiece == 0;
+}
+
+template <typename E>
+int launch_rows_product(const RowsProduct& p, bool across, bool glu, hipStream_t stream) {
+  const bool dma = whole_pieces<E>(p.a, p.a_stride, 0, p.K) &&
+                   whole_pieces<E>(p.b, p.b_stride, p.b_group_stride, across ? p.N : p.K);
+  if (across && glu)
+    launch_rows_tiles<E, true, true>(p, dma, stream);
+  else if (across)
+    launch_rows_tiles<E, true, false>(p, dma, stream);
+  else if (glu)
+    launch_rows_tiles<E, false, true>(p, dma, stream);
+  else
+    launch_rows_tiles<E, false, false>(p, dma, stream);
+  return hip_status();
+}
+
+// ---------------------------------------------------------------------------
+// outer
+// ---------------------------------------------------------------------------
+template <typename E, bool DMA>
+__global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int down, int across,
+                                                           int64_t first) {
+  constexpr int MF = 8;
+  constexpr int kPiece = 16 / (int)sizeof(E);
+  constexpr int kC = kStep / (int)sizeof(E);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kTileLds];
+  const int64_t id = first + blockIdx.x;
+  const int g = (int)(id / ((int64_t)down * across)), at = (int)(id % ((int64_t)down * across));
+  const int l0 = at / across * 256, r0 = at % across * kCols;
+  const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave >> 2, wn = wave & 3;
+
+  auto of = [](const int32_t* index, int div, int rows, int m) {
+    int r = m;
+    if (index) {
+      r = index[m];
+      r = r < 0 ? -1 : r / div;
+    }
+    return (unsigned)r < (unsigned)rows ? r : -1;
+  };
+  // a row that either operand lacks adds nothing
+  auto from = [&](bool left, int i, int row, int piece) {
+    const int m = lo + i * kC + row;
+    const int n = left ? l0 + piece * kPiece : r0 + piece * kPiece;
+    if (m >= hi) return Src<E>{nullptr, 0};
+    const int rl = of(p.left_index, p.left_div, p.left_rows, m);
+    const int rr = of(p.right_index, p.right_div, p.right_rows, m);
+    if (rl < 0 || rr < 0) return Src<E>{nullptr, 0};
+    return left ? Src<E>{(const E*)p.left + (size_t)rl * p.left_stride + n, p.L - n}
+                : Src<E>{(const E*)p.right + (size_t)rr * p.right_stride + n, p.R - n};
+  };
+  f32x4 acc[MF][4] = {};
+  products<E, true, true, false, MF, 2, DMA, false>(
+      smem, hi > lo ? (hi - lo + kC - 1) / kC : 0,
+      [&](int i, int, int row, int piece) { return from(true, i, row, piece); },
+      [&](int i, int, int row, int piece) { return from(false, i, row, piece); }, acc);
+  barrier();
+  E* out = (E*)p.out + (size_t)g * p.out_group_stride;
+  store_rows<E, MF, 4, false>(
+      smem + wave * kOutBytes, [&](int f, int s, int e) { return acc[f][s][e]; },
+      [&](int row, int c) {
+        const int l = l0 + wm * MF * 16 + row, n = r0 + wn * 64 + c * kPiece;
+        return Dst<E>{out + (size_t)l * p.out_stride + n, l < p.L ? p.R - n : 0, false};
+      });
+}
+
+template <typename E>
+int launch_outer_product(const OuterProduct& p, hipStream_t stream) {
+  const bool dma = whole_pieces<E>(p.left, p.left_stride, 0, p.L) &&
+                   whole_pieces<E>(p.right, p.right_stride, 0, p.R);
+  const int down = (p.L + 255) / 256, across = (p.R + kCols - 1) / kCols;
+  const int64_t tiles = (int64_t)p.G * down * across;
+  for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+    const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
+    if (dma)
+      outer_tiles<E, true><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
+    else
+      outer_tiles<E, false><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
+  }
+  return hip_status();
+}
+
+}  // namespace moe

@@ -1,0 +1,7 @@
+// The tiled products of grouped.hpp for fp16.
+#include "grouped.hpp"
+
+namespace moe {
+template int launch_rows_product<Fp16>(const RowsProduct&, bool, bool, hipStream_t);
+template int launch_outer_product<Fp16>(const OuterProduct&, hipStream_t);
+}  // namespace moe
