@@ -805,8 +805,8 @@ int moe_grouped_matmul(const moe_grouped_matmul_args* args, hipStream_t stream);
  * moe_grouped_outer -- the gradient of the groups' matrices:
  *   out[g][l][r] = sum over offsets[g] <= p < offsets[g+1] of left[pl][l] * right[pr][r]
  * with float32 sums over ascending p in a fixed order and one rounding; a group without
- * rows gets zeros.  pl = p, or left_index[p] / left_div; pr likewise; a row p for which
- * either is outside its array adds nothing.  With left = dz and right = a this is the
+ * rows gets zeros.  pl = p, or left_index[p] / left_div; pr likewise (at
+ * most one operand has an index); a row p for which it is outside its array adds nothing.  With left = dz and right = a this is the
  * gradient of b [N][K]; the other way round, that of b [K][N].
  * Inputs : left [left_rows][L], right [right_rows][R], rows their strides apart;
  *          offsets [G+1] int32, cut to [0, M].

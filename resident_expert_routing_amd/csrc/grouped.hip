@@ -109,6 +109,7 @@ int outer_status(const moe_grouped_outer_args* a) {
   if (!a->left || !a->right || !aligned(a->left, e) || !aligned(a->right, e) ||
       !aligned(a->left_index, 4) || !aligned(a->right_index, 4))
     return MOE_EINVAL;
+  if (a->left_index && a->right_index) return MOE_EINVAL;
   if (a->left_index ? a->left_div < 1 : a->left_rows < a->M) return MOE_EINVAL;
   if (a->right_index ? a->right_div < 1 : a->right_rows < a->M) return MOE_EINVAL;
   if (a->left_stride < (size_t)a->L || a->right_stride < (size_t)a->R) return MOE_EINVAL;

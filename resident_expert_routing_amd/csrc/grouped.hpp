@@ -131,7 +131,7 @@ struct Src {
 // and 256 of the right one, kStep bytes of contraction each, in a ring of S; from_left(i, j,
 // row, piece) and from_right say where the 16-byte piece of stage i is in memory that the
 // wave's load j of the operand takes, `row` the row (across: the contraction step) and
-// `piece` the piece in it.  DMA: loads go to
+// `piece` the piece in it; before(i) is called ahead of the loads of stage i.  DMA: loads go to
 // LDS directly, and pieces count whole or not at all; otherwise they pass through
 // registers, from any address and cut at any element.
 //
@@ -140,9 +140,9 @@ struct Src {
 // issued one for each group; a wave at its products goes before the SIMD's other one at
 // its loads.
 template <typename E, bool LEFT, bool RIGHT, bool SPLIT, int MF, int S, bool DMA, bool ONCE,
-          typename FL, typename FR>
-__device__ __forceinline__ void products(uint8_t* smem, int steps, FL from_left, FR from_right,
-                                         f32x4 (&acc)[MF][4]) {
+          typename FB, typename FL, typename FR>
+__device__ __forceinline__ void products(uint8_t* smem, int steps, FB before, FL from_left,
+                                         FR from_right, f32x4 (&acc)[MF][4]) {
   constexpr int kRows = 32 * MF;
   constexpr int kStage = (kRows + kCols) * kStep;
   constexpr int kLoadsL = kRows / 8 / kTWaves, kLoadsR = kCols / 8 / kTWaves;
@@ -205,6 +205,7 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FL from_left,
         return *(const i32x4*)(r + (wn * 64 + 16 * s + col) * kStep + slot[c]);
     };
     i32x4 w[3], v[2][4];
+    if constexpr (decltype(more)::value) before(i + S - 1);
 #pragma unroll
     for (int s = 0; s < 4; ++s) v[0][s] = weight(0, s);
     w[0] = frag(0);
@@ -232,6 +233,7 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FL from_left,
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
       if (i < steps) {
+        before(i);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) load(i, j);
       }
@@ -247,6 +249,7 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FL from_left,
   } else {
     Piece<E> u[kLoads];
     auto fetch = [&](int i) {
+      before(i);
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const Src<E> s = source(i, j);
@@ -380,8 +383,8 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
     const bool in = r.lo + t < r.hi;
     live.row[t] = !in ? 0 : source_row(p, r.lo + t) >= 0 ? 1 : p.zero_rest ? 2 : 0;
   }
-  products<E, false, ACROSS, GLU, MF, S, DMA, ONCE>(smem, (p.K + kC - 1) / kC, from_left,
-                                                    from_right, acc);
+  products<E, false, ACROSS, GLU, MF, S, DMA, ONCE>(
+      smem, (p.K + kC - 1) / kC, [](int) {}, from_left, from_right, acc);
   barrier();  // every wave has read the last stage
   uint8_t* mine = smem + wave * kOutBytes;
   auto to = [&](void* out, size_t stride, int at, int N, int row, int c) {
@@ -534,13 +537,21 @@ int launch_rows_product(const RowsProduct& p, bool across, bool glu, hipStream_t
 // ---------------------------------------------------------------------------
 // outer
 // ---------------------------------------------------------------------------
-template <typename E, bool DMA>
+// Rows of an indexed operand are looked up once, into a table in LDS: of kTable rows of
+// the group at a time, each with a run of the main loop of its own.  (An index read from
+// memory ahead of each load: 64 groups of 512 rows, 4096 x 4096, 3086 us.)
+constexpr int kTable = 2048;
+enum { kNone, kLeft, kRight };  // the operand that has an index
+
+template <typename E, bool DMA, int INDEXED>
 __global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int down, int across,
                                                            int64_t first) {
   constexpr int MF = 8;
   constexpr int kPiece = 16 / (int)sizeof(E);
   constexpr int kC = kStep / (int)sizeof(E);
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kTileLds];
+  constexpr int kLoads = 4;  // of each operand
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (256 + kCols) * kStep];
+  __shared__ int table[INDEXED == kNone ? 1 : kTable];
   const int64_t id = first + blockIdx.x;
   const int g = (int)(id / ((int64_t)down * across)), at = (int)(id % ((int64_t)down * across));
   const int l0 = at / across * 256, r0 = at % across * kCols;
@@ -548,30 +559,49 @@ __global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave >> 2, wn = wave & 3;
 
-  auto of = [](const int32_t* index, int div, int rows, int m) {
-    int r = m;
-    if (index) {
-      r = index[m];
-      r = r < 0 ? -1 : r / div;
-    }
-    return (unsigned)r < (unsigned)rows ? r : -1;
-  };
-  // a row that either operand lacks adds nothing
-  auto from = [&](bool left, int i, int row, int piece) {
-    const int m = lo + i * kC + row;
-    const int n = left ? l0 + piece * kPiece : r0 + piece * kPiece;
-    if (m >= hi) return Src<E>{nullptr, 0};
-    const int rl = of(p.left_index, p.left_div, p.left_rows, m);
-    const int rr = of(p.right_index, p.right_div, p.right_rows, m);
-    if (rl < 0 || rr < 0) return Src<E>{nullptr, 0};
-    return left ? Src<E>{(const E*)p.left + (size_t)rl * p.left_stride + n, p.L - n}
-                : Src<E>{(const E*)p.right + (size_t)rr * p.right_stride + n, p.R - n};
-  };
   f32x4 acc[MF][4] = {};
-  products<E, true, true, false, MF, 2, DMA, false>(
-      smem, hi > lo ? (hi - lo + kC - 1) / kC : 0,
-      [&](int i, int, int row, int piece) { return from(true, i, row, piece); },
-      [&](int i, int, int row, int piece) { return from(false, i, row, piece); }, acc);
+  constexpr int kRun = INDEXED == kNone ? 1 << 30 : kTable;
+  for (int m0 = lo; m0 < hi; m0 += kRun) {
+    const int n = min(hi - m0, kRun);
+    if constexpr (INDEXED != kNone) {
+      __syncthreads();  // the table and the last stage of the run before have been read
+      const int32_t* index = INDEXED == kLeft ? p.left_index : p.right_index;
+      const int div = INDEXED == kLeft ? p.left_div : p.right_div;
+      const int rows = INDEXED == kLeft ? p.left_rows : p.right_rows;
+      for (int t = threadIdx.x; t < n; t += kTThreads) {
+        int r = index[m0 + t];
+        r = r < 0 ? -1 : r / div;
+        table[t] = (unsigned)r < (unsigned)rows ? r : -1;
+      }
+      __syncthreads();
+    }
+    int row_of[kLoads];  // of the indexed operand, for each load of a stage
+    auto before = [&](int i) {
+      if constexpr (INDEXED != kNone) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const int row =
+              i * kC + ((wave * kLoads + j) * 64 + (int)(threadIdx.x & 63)) / (256 / kPiece);
+          row_of[j] = row < n ? table[row] : -1;
+        }
+      }
+    };
+    // both operands' loads j take the same rows, and a row that one lacks adds nothing
+    auto from_left = [&](int i, int j, int row, int piece) {
+      const int t = i * kC + row, c = l0 + piece * kPiece;
+      const bool in = INDEXED == kNone ? t < n : row_of[j] >= 0;
+      const int r = INDEXED == kLeft ? row_of[j] : m0 + t;
+      return Src<E>{(const E*)p.left + (size_t)r * p.left_stride + c, in ? p.L - c : 0};
+    };
+    auto from_right = [&](int i, int j, int row, int piece) {
+      const int t = i * kC + row, c = r0 + piece * kPiece;
+      const bool in = INDEXED == kNone ? t < n : row_of[j] >= 0;
+      const int r = INDEXED == kRight ? row_of[j] : m0 + t;
+      return Src<E>{(const E*)p.right + (size_t)r * p.right_stride + c, in ? p.R - c : 0};
+    };
+    products<E, true, true, false, MF, 2, DMA, false>(smem, (n + kC - 1) / kC, before, from_left,
+                                                      from_right, acc);
+  }
   barrier();
   E* out = (E*)p.out + (size_t)g * p.out_group_stride;
   store_rows<E, MF, 4, false>(
@@ -582,8 +612,8 @@ __global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int 
       });
 }
 
-template <typename E>
-int launch_outer_product(const OuterProduct& p, hipStream_t stream) {
+template <typename E, int INDEXED>
+void launch_outer_tiles(const OuterProduct& p, hipStream_t stream) {
   const bool dma = whole_pieces<E>(p.left, p.left_stride, 0, p.L) &&
                    whole_pieces<E>(p.right, p.right_stride, 0, p.R);
   const int down = (p.L + 255) / 256, across = (p.R + kCols - 1) / kCols;
@@ -591,10 +621,20 @@ int launch_outer_product(const OuterProduct& p, hipStream_t stream) {
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (dma)
-      outer_tiles<E, true><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
+      outer_tiles<E, true, INDEXED><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
     else
-      outer_tiles<E, false><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
+      outer_tiles<E, false, INDEXED><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
   }
+}
+
+template <typename E>
+int launch_outer_product(const OuterProduct& p, hipStream_t stream) {
+  if (p.left_index)
+    launch_outer_tiles<E, kLeft>(p, stream);
+  else if (p.right_index)
+    launch_outer_tiles<E, kRight>(p, stream);
+  else
+    launch_outer_tiles<E, kNone>(p, stream);
   return hip_status();
 }
 
