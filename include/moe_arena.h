@@ -587,7 +587,7 @@ int moe_history_scale(double* hist, size_t n, double factor, hipStream_t stream)
  * perm.
  */
 
-/* Element types (moe_rows_args.dtype, moe_int8_quantize, moe_int8_matmul). */
+/* Element types (moe_rows_args.dtype, and of the products below). */
 #define MOE_DT_BF16 0
 #define MOE_DT_FP16 1
 #define MOE_DT_FP32 2
@@ -845,6 +845,90 @@ int moe_grouped_outer(const moe_grouped_outer_args* args, hipStream_t stream);
 int moe_swiglu_backward(int M, int N, int dtype, const void* pre, size_t pre_stride,
                         const void* dout, size_t dout_stride, void* dpre, size_t dpre_stride,
                         hipStream_t stream);
+
+/*
+ * Products with 4-bit weights and a scale (and, where given, a zero point) for each group
+ * of 32, 64 or 128 consecutive weights of a row: experts, or a dense layer, of small
+ * weights at few rows, next to the 8-bit ones.  Activations stay in their own type.
+ *
+ * int4 matrix of N rows of K weights, weight i of row n = scale * (code - zero):
+ *   codes : tiles of 16 rows by 128 weights, 1024 bytes each, the tiles of 16 rows one after
+ *           another along K (moe_int4_code_bytes(N, K) bytes in all, N and K padded).  In a
+ *           tile a row has 64 consecutive bytes, sixteen little-endian words of eight
+ *           consecutive weights: weight 2j of a word at bit 4j, weight 2j+1 at bit 16+4j.
+ *   scale : bf16 or fp16, [N/16][groups][16] (rows in sixteens; groups: of the padded K;
+ *           moe_int4_scale_count(N, K, group) values).
+ *   zero  : 0..15 in a byte each, laid out as the scales; NULL: all 8.
+ * Padding may hold anything.
+ */
+size_t moe_int4_code_bytes(int N, int K);               /* 0 for a size <= 0 or past 2^24 (N: 2^25) */
+size_t moe_int4_scale_count(int N, int K, int group);   /* 0 likewise, or for another group */
+
+/*
+ * moe_int4_quantize -- w [N][K] (rows w_stride elements apart, at any element, of the type
+ * `dtype`) as an int4 matrix.  For each group of weights, in float32:
+ *   zero NULL : scale = max |w| / 7, code = w / scale + 8
+ *   otherwise : lo = min(w, 0), hi = max(w, 0), scale = (hi - lo) / 15,
+ *               zero = -lo / scale, code = w / scale + zero
+ * where scale is first rounded to its type and divides from then on, and zero and the
+ * quotients are rounded to the nearest integer, ties to even, and cut to 0 .. 15.  A group
+ * of zeros (or whose scale rounds to zero) has scale 0 and codes of 8; a group with an infinity or a NaN, or
+ * whose scale its type does not hold, has scale NaN.  Padding weights count as zeros.
+ * Errors : MOE_EINVAL for null or misaligned pointers (codes 16 bytes, scale 8, zero 4), N
+ *          < 0, K <= 0, w_stride < K, an unknown dtype, scale_dtype or group;
+ *          MOE_EUNSUPPORTED for K > 2^24 or N > 2^25.  N = 0 is valid and does nothing.
+ */
+int moe_int4_quantize(const void* w, int N, int K, size_t w_stride, int dtype, int group,
+                      uint8_t* codes, void* scale, int scale_dtype, uint8_t* zero,
+                      hipStream_t stream);
+
+/*
+ * moe_int4_matmul -- rows p of out [M][N], over the groups of a bucketing or dense:
+ *   y[p][n] = sum_i a[r][i] * w[g][n][i]
+ *   out[p][n] = y[p][n], or with swiglu (2N rows of weights, N gate rows and then N up
+ *               rows): silu(y[p][n]) * y[p][N+n], as in moe_int8_matmul
+ * with float32 sums of exact products, within each group of weights first, then with its
+ * scale over the groups, and one rounding to out_dtype.  (fp32 activations are three bf16
+ * parts whose sum they are exactly.)  A group's sum is taken of a * (16 + code) and
+ * corrected, so its error is that of a float32 sum of magnitudes up to 31 |a|; values of a
+ * above 2^110 may overflow.
+ *   G, offsets, index, index_div, and which rows of out are left as they were: as in
+ *   moe_int8_matmul.  Made for few rows of each group: weights are read and widened again for
+ *   every 64 rows of a group.
+ * Inputs : a [a_rows][K], rows a_stride elements apart, at any element; for each group an
+ *          int4 matrix (its parts codes_group_stride bytes, scale_group_stride and
+ *          zero_group_stride values apart).
+ * Output : out, rows out_stride elements apart, at any element; must not overlap an input.
+ * Errors : MOE_EINVAL for null or misaligned pointers (codes 16 bytes, scale 8, zero 4;
+ *          group strides likewise), a bad size, stride, dtype, group or flag, offsets
+ *          without G or G without offsets, index without index_div >= 1, or fewer rows of
+ *          a than M without index; MOE_EUNSUPPORTED for K or N > 2^24, M > 2^30 or G >
+ *          MOE_MAX_S.  M = 0 is valid and does nothing.  No workspace.
+ */
+typedef struct moe_int4_matmul_args {
+  int M, N, K, G;
+  int swiglu;
+  int a_rows;
+  const void* a;
+  size_t a_stride;
+  int a_dtype;
+  const int32_t* index;
+  int index_div;
+  const int32_t* offsets;
+  int group;
+  const uint8_t* codes;
+  size_t codes_group_stride;
+  const void* scale;
+  size_t scale_group_stride;
+  int scale_dtype;
+  const uint8_t* zero;
+  size_t zero_group_stride;
+  void* out;
+  size_t out_stride;
+  int out_dtype;
+} moe_int4_matmul_args;
+
+int moe_int4_matmul(const moe_int4_matmul_args* args, hipStream_t stream);
 
 /*
  * moe_test_mxfp4_probe -- test-only: one wave runs one block-scaled MXFP4

@@ -52,6 +52,7 @@ EXPORTS = ("moe_status_string", "moe_mxfp4_row_bytes", "moe_act_row_bytes", "moe
            "moe_positions", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
            "moe_combine_backward", "moe_int8_row_bytes", "moe_int8_quantize", "moe_int8_matmul",
            "moe_grouped_matmul", "moe_grouped_outer", "moe_swiglu_backward",
+           "moe_int4_code_bytes", "moe_int4_scale_count", "moe_int4_quantize", "moe_int4_matmul",
            "arena_load_slot", "moe_hot_pick", "moe_hot_install", "moe_replan", "moe_test_mxfp4_probe",
            "moe_test_stream_read", "moe_test_mfma_loop")
 
@@ -134,6 +135,19 @@ class GroupedOuterArgs(ctypes.Structure):
                 ("out_group_stride", ctypes.c_size_t)]
 
 
+class Int4MatmulArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("G", ctypes.c_int), ("swiglu", ctypes.c_int), ("a_rows", ctypes.c_int),
+                ("a", ctypes.c_void_p), ("a_stride", ctypes.c_size_t), ("a_dtype", ctypes.c_int),
+                ("index", ctypes.c_void_p), ("index_div", ctypes.c_int),
+                ("offsets", ctypes.c_void_p), ("group", ctypes.c_int),
+                ("codes", ctypes.c_void_p), ("codes_group_stride", ctypes.c_size_t),
+                ("scale", ctypes.c_void_p), ("scale_group_stride", ctypes.c_size_t),
+                ("scale_dtype", ctypes.c_int), ("zero", ctypes.c_void_p),
+                ("zero_group_stride", ctypes.c_size_t), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_size_t), ("out_dtype", ctypes.c_int)]
+
+
 MOE_STAGE_EVENTS = 5
 _lib = None
 
@@ -205,6 +219,14 @@ def load() -> ctypes.CDLL:
     lib.moe_int8_quantize.restype = i
     lib.moe_int8_matmul.argtypes = [ctypes.POINTER(Int8MatmulArgs), vp]
     lib.moe_int8_matmul.restype = i
+    lib.moe_int4_code_bytes.argtypes = [i, i]
+    lib.moe_int4_code_bytes.restype = sz
+    lib.moe_int4_scale_count.argtypes = [i, i, i]
+    lib.moe_int4_scale_count.restype = sz
+    lib.moe_int4_quantize.argtypes = [vp, i, i, sz, i, i, vp, vp, i, vp, vp]
+    lib.moe_int4_quantize.restype = i
+    lib.moe_int4_matmul.argtypes = [ctypes.POINTER(Int4MatmulArgs), vp]
+    lib.moe_int4_matmul.restype = i
     lib.moe_grouped_matmul.argtypes = [ctypes.POINTER(GroupedMatmulArgs), vp]
     lib.moe_grouped_matmul.restype = i
     lib.moe_grouped_outer.argtypes = [ctypes.POINTER(GroupedOuterArgs), vp]
@@ -524,6 +546,40 @@ def moe_swiglu_backward(M, N, dtype, pre, pre_stride, dout, dout_stride, dpre, d
     return int(load().moe_swiglu_backward(int(M), int(N), int(dtype), _ptr(pre), int(pre_stride),
                                           _ptr(dout), int(dout_stride), _ptr(dpre),
                                           int(dpre_stride), _stream(stream)))
+
+
+def moe_int4_code_bytes(N: int, K: int) -> int:
+    if not fits(N, K):
+        return 0
+    return int(load().moe_int4_code_bytes(int(N), int(K)))
+
+
+def moe_int4_scale_count(N: int, K: int, group: int) -> int:
+    if not fits(N, K, group):
+        return 0
+    return int(load().moe_int4_scale_count(int(N), int(K), int(group)))
+
+
+def moe_int4_quantize(w, N, K, w_stride, dtype, group, codes, scale, scale_dtype, zero=None,
+                      stream=None) -> int:
+    if not fits(N, K, dtype, group, scale_dtype):
+        return MOE_EUNSUPPORTED
+    return int(load().moe_int4_quantize(_ptr(w), int(N), int(K), int(w_stride), int(dtype),
+                                        int(group), _ptr(codes), _ptr(scale), int(scale_dtype),
+                                        _ptr(zero), _stream(stream)))
+
+
+def moe_int4_matmul(M, N, K, G, swiglu, a_rows, a, a_stride, a_dtype, index, index_div, offsets,
+                    group, codes, codes_group_stride, scale, scale_group_stride, scale_dtype,
+                    zero, zero_group_stride, out, out_stride, out_dtype, stream=None) -> int:
+    if not fits(M, N, K, G, swiglu, a_rows, a_dtype, index_div, group, scale_dtype, out_dtype):
+        return MOE_EUNSUPPORTED
+    args = Int4MatmulArgs(int(M), int(N), int(K), int(G), int(swiglu), int(a_rows), _ptr(a),
+                          int(a_stride), int(a_dtype), _ptr(index), int(index_div),
+                          _ptr(offsets), int(group), _ptr(codes), int(codes_group_stride),
+                          _ptr(scale), int(scale_group_stride), int(scale_dtype), _ptr(zero),
+                          int(zero_group_stride), _ptr(out), int(out_stride), int(out_dtype))
+    return int(load().moe_int4_matmul(ctypes.byref(args), _stream(stream)))
 
 
 def moe_test_mxfp4_probe(shape, a, a_scale, b, b_scale, d, stream=None) -> int:

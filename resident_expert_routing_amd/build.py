@@ -22,7 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_arena.so")
 SOURCES = ["capi.cpp", "route.hip", "demand.hip", "experts.hip", "plan.hip", "rows.hip",
            "int8.hip", "grouped.hip", "grouped_bf16.hip", "grouped_fp16.hip", "grouped_fp32.hip",
-           "replan.cpp", "history.cpp", "probe.hip"]
+           "int4.hip", "replan.cpp", "history.cpp", "probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
