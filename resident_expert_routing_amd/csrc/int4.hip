@@ -41,23 +41,29 @@ struct Int4Args {
   size_t a_stride, codes_group_stride, scale_group_stride, zero_group_stride, out_stride;
 };
 
-// Eight codes of a word (code 2j at bit 4j, 2j + 1 at bit 16 + 4j) as 16 + c.
+// The masks and exponents that widen codes, where one instruction can take both: the
+// mask from a scalar register and the exponents from a vector register (as literals they
+// take two).
 template <bool HALF>
-__device__ __forceinline__ i32x4 widen(uint32_t w) {
-  i32x4 v;
-  if constexpr (HALF) {
-    v[0] = (int)((w << 6 & 0x03C003C0u) | 0x4C004C00u);
-    v[1] = (int)((w << 2 & 0x03C003C0u) | 0x4C004C00u);
-    v[2] = (int)((w >> 2 & 0x03C003C0u) | 0x4C004C00u);
-    v[3] = (int)((w >> 6 & 0x03C003C0u) | 0x4C004C00u);
-  } else {
-    v[0] = (int)((w << 3 & 0x00780078u) | 0x41804180u);
-    v[1] = (int)((w >> 1 & 0x00780078u) | 0x41804180u);
-    v[2] = (int)((w >> 5 & 0x00780078u) | 0x41804180u);
-    v[3] = (int)((w >> 9 & 0x00780078u) | 0x41804180u);
+struct Widen {
+  uint32_t mask, exponents;
+  __device__ __forceinline__ Widen() {
+    mask = HALF ? 0x03C003C0u : 0x00780078u;
+    exponents = HALF ? 0x4C004C00u : 0x41804180u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(exponents));
   }
-  return v;
-}
+  // eight codes of a word (code 2j at bit 4j, 2j + 1 at bit 16 + 4j) as 16 + c
+  __device__ __forceinline__ i32x4 operator()(uint32_t w) const {
+    constexpr int kUp = HALF ? 6 : 3;  // code 0 to the top of the mantissa
+    const uint32_t at[4] = {w << kUp, HALF ? w << 2 : w >> 1, HALF ? w >> 2 : w >> 5,
+                            HALF ? w >> 6 : w >> 9};
+    i32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (int)((at[j] & mask) | exponents);
+    return v;
+  }
+};
 
 template <bool HALF>
 __device__ __forceinline__ f32x4 mma(i32x4 w, i32x4 x, f32x4 acc) {
@@ -91,41 +97,44 @@ __device__ __forceinline__ void exchange(uint32_t (&w)[4]) {
   swap16(w[2], w[3]);
 }
 
-// Eight activations as the matrix instruction takes them.  float32 ones become three
-// bf16 parts that add up to them exactly.
+// Eight activations: loaded as they lie (as whole words: kept as single elements they
+// would take a register each), and the operands that the matrix instruction takes of
+// them.  float32 ones become three bf16 parts that add up to them exactly.
 template <typename E>
 struct Acts {
-  static constexpr int kParts = 1;
-  i32x4 v[1];
-  __device__ __forceinline__ void load(const E* p, int n) {
-    Piece<E> u;
-    u.load_upto(p, n);
-    __builtin_memcpy(&v[0], u.e, 16);
+  static constexpr int kWords = 2 * (int)sizeof(E), kParts = sizeof(E) == 4 ? 3 : 1;
+  i32x4 raw[kWords / 4];
+  __device__ __forceinline__ void load(const E* p) {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+      raw[i] = __builtin_bit_cast(i32x4, *(const u32x4*)(p + i * (16 / sizeof(E))));
   }
-};
-template <>
-struct Acts<float> {
-  static constexpr int kParts = 3;
-  i32x4 v[3];
-  __device__ __forceinline__ void load(const float* p, int n) {
-    Piece<float> u[2];
-    u[0].load_upto(p, n);
-    if (n > 4)
-      u[1].load_upto(p + 4, n - 4);
-    else
-      u[1] = Piece<float>{};
-    uint16_t b[3][8];
+  __device__ __forceinline__ void load_head(const E* p, int n) {  // n elements, then zeros
+    constexpr int kN = Piece<E>::kN;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x = u[i / 4].e[i % 4];
-#pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        b[t][i] = from_f32<Bf16>(x).bits;
-        x -= bf16_to_f32(b[t][i]);
-      }
+    for (int i = 0; i < kWords / 4; ++i) {
+      Piece<E> u{};
+      if (n > i * kN) u.load_upto(p + i * kN, n - i * kN);
+      __builtin_memcpy(&raw[i], u.e, 16);
     }
+  }
+  __device__ __forceinline__ void parts(i32x4 (&v)[kParts]) const {
+    if constexpr (kParts == 1) {
+      v[0] = raw[0];
+    } else {
+      uint16_t b[3][8];
 #pragma unroll
-    for (int t = 0; t < 3; ++t) __builtin_memcpy(&v[t], b[t], 16);
+      for (int i = 0; i < 8; ++i) {
+        float x = __int_as_float(raw[i / 4][i % 4]);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          b[t][i] = from_f32<Bf16>(x).bits;
+          x -= bf16_to_f32(b[t][i]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) __builtin_memcpy(&v[t], b[t], 16);
+    }
   }
 };
 
@@ -146,214 +155,283 @@ __device__ __forceinline__ void store_out(const Int4Args& p, int m, int n, const
     store4<float>(p, m, n, y);
 }
 
-// A workgroup takes 32 rows of weights (with SwiGLU, 16 gate rows and their 16 up rows)
-// and up to 16 * MT rows of one group of `a`, its W waves the tiles along K in turn; the
-// waves' sums are added through LDS in a fixed order.  Codes go from memory straight to
-// registers, 1 KB of consecutive bytes a load.  QUADS: groups of weights in a tile.
-template <typename E, int W, int MT, bool GLU, int QUADS>
+// One word of each quad's lanes as the words of all four quads in every lane.
+__device__ __forceinline__ void spread(uint32_t w, uint32_t (&all)[4]) {
+  const auto h = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+  all[0] = lo[0], all[1] = lo[1], all[2] = hi[0], all[3] = hi[1];
+}
+
+// What a workgroup of WK * WN waves computes: up to 16 * MT rows of one group of `a`
+// against 16 * NT rows of weights for each of WN waves (with SwiGLU half of them gate
+// rows and half their up rows); WK waves share the tiles along K, each a run of them.
+template <int MT_, int NT_, int WK_, int WN_>
+struct Form {
+  static constexpr int MT = MT_, NT = NT_, WK = WK_, WN = WN_, W = WK * WN;
+  static constexpr int kCols = 16 * NT * WN;  // rows of weights
+};
+
+// Codes go from memory straight to registers, 1 KB of consecutive bytes a load, kCodesAhead
+// tiles before their products, and activations kActsAhead quarters of a tile before
+// theirs; a lane loads the scale and zero point of one group of four, its quad's.  The
+// waves' sums over K are added through LDS in a fixed order.  QUADS: groups in a tile.
+template <typename E, typename F, bool GLU, int QUADS>
 __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int n0,
                                           f32x4* part) {
   constexpr bool HALF = std::is_same_v<E, Fp16>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
-  const int col = lane & 15, quad = lane >> 4;
+  constexpr int MT = F::MT, NT = F::NT, WK = F::WK;
+  constexpr int kRing = 8 / NT, kCodesAhead = kRing - 1;
+  constexpr int kActs = 128 / (MT * (int)sizeof(Acts<E>)) > 4 ? 4 : 128 / (MT * (int)sizeof(Acts<E>));
+  constexpr int kActsAhead = kActs - 1;
+  constexpr int kRun = 4 / QUADS;  // tiles of four groups
+  static_assert(kRing >= 2 && kActs >= 2, "rings");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, quad = lane >> 4, wn = wave / WK, wk = wave % WK;
+  const Widen<HALF> widen;
+  const int first = n0 + wn * (GLU ? NT / 2 : NT) * 16;  // the wave's first column of out
 
-  const uint8_t* codes[2];
-  int at4[2];  // of the lane's four results: the first row, for scales and zero points
+  const uint8_t* codes[NT];
+  const uint16_t* scale[NT];
+  const uint8_t* zero[NT];
+  const bool zeros = p.zero != nullptr;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int first = GLU ? n0 + (s ? p.N : 0) : n0 + 16 * s;
-    const int row = min(first + col, p.rows - 1);
-    codes[s] = p.codes + (size_t)r.g * p.codes_group_stride +
-               ((size_t)(row / kBlock) * p.chunks * kBlock + row % kBlock) * (kCodes / 2) +
-               16 * quad;
-    at4[s] = first + 4 * quad;
+  for (int s = 0; s < NT; ++s) {
+    const bool up = GLU && s >= NT / 2;
+    const int row =
+        min(first + 16 * (up ? s - NT / 2 : s) + (up ? p.N : 0) + col, p.rows - 1);
+    const size_t block = (size_t)(row / kBlock) * p.chunks;
+    codes[s] = p.codes + (size_t)r.g * p.codes_group_stride + block * kTileBytes +
+               row % kBlock * (kCodes / 2) + 16 * quad;
+    const size_t at = block * QUADS * kBlock + row % kBlock;
+    scale[s] = p.scale + (size_t)r.g * p.scale_group_stride + at;
+    // without zero points any bytes are read in their place, those of the scales
+    zero[s] = zeros ? p.zero + (size_t)r.g * p.zero_group_stride + at : (const uint8_t*)scale[s];
   }
-  const uint16_t* scale = p.scale + (size_t)r.g * p.scale_group_stride;
-  const uint8_t* zero = p.zero ? p.zero + (size_t)r.g * p.zero_group_stride : nullptr;
-  const bool four = !GLU || p.N % 4 == 0;  // a lane's four rows lie side by side
-  const int groups = p.chunks * QUADS;
-  auto place = [&](int row, int q) {  // of a row's scale and zero point of group q
-    return ((size_t)(row / kBlock) * groups + q) * kBlock + row % kBlock;
-  };
-  auto as_scale = [&](uint16_t b) {
-    return p.scale_dtype == MOE_DT_BF16 ? bf16_to_f32(b) : to_f32<Fp16>(Fp16{b});
-  };
-
   const E* arow[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int src = source_row(p, min(r.lo + 16 * t + col, r.hi - 1));
     arow[t] = (const E*)p.a + (size_t)max(src, 0) * p.a_stride + 8 * quad;
   }
-
   i32x4 ones;
 #pragma unroll
   for (int i = 0; i < 4; ++i) ones[i] = HALF ? 0x3C003C00 : 0x3F803F80;
-  f32x4 acc[MT][2] = {};
 
-  struct Tile {
-    i32x4 c[2];
-    uint16_t s[2][QUADS][4];
-    uint8_t z[2][QUADS][4];
+  struct Side {
+    uint16_t s[NT];
+    uint8_t z[NT];
   };
-  auto load = [&](Tile& w, int c) {
+  // masks in place of branches, which would cut the loop's loads and products to pieces
+  const uint32_t is_bf16 = p.scale_dtype == MOE_DT_BF16 ? ~0u : 0u;
+  const uint32_t given = zeros ? 0xFFu : 0u, offset = zeros ? 16u : 24u;
+  auto load_codes = [&](i32x4 (&w)[NT], int c) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) w.c[s] = *(const i32x4*)(codes[s] + (size_t)c * kTileBytes);
+    for (int s = 0; s < NT; ++s) w[s] = *(const i32x4*)(codes[s] + (size_t)c * kTileBytes);
+  };
+  auto load_side = [&](Side& w, int group) {  // of groups group .. + 3
+    const size_t at = (size_t)min(group + quad, p.chunks * QUADS - 1) * kBlock;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < NT; ++s) w.s[s] = scale[s][at], w.z[s] = zero[s][at];
+  };
+  f32x4 acc[MT][NT] = {}, dot[MT][NT], sum[MT];
+  // products of quarter j of a tile; the first of a group of weights starts its sums
+  auto multiply = [&](const uint32_t (&word)[NT][4], int j, const Acts<E> (&x)[MT]) {
+    const bool fresh = j % (4 / QUADS) == 0;
+    i32x4 wide[NT];
 #pragma unroll
-      for (int q = 0; q < QUADS; ++q) {
-        if (four) {
-          const size_t at = place(min(at4[s], p.rows - 4), c * QUADS + q);
-          __builtin_memcpy(w.s[s][q], __builtin_assume_aligned(scale + at, 8), 8);
-          if (zero) __builtin_memcpy(w.z[s][q], __builtin_assume_aligned(zero + at, 4), 4);
-        } else {
+    for (int s = 0; s < NT; ++s) wide[s] = widen(word[s][j]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const size_t at = place(min(at4[s] + i, p.rows - 1), c * QUADS + q);
-            w.s[s][q][i] = scale[at];
-            if (zero) w.z[s][q][i] = zero[at];
-          }
-        }
+    for (int t = 0; t < MT; ++t) {
+      i32x4 v[Acts<E>::kParts];
+      x[t].parts(v);
+#pragma unroll
+      for (int u = 0; u < Acts<E>::kParts; ++u) {
+        sum[t] = mma<HALF>(v[u], ones, fresh && u == 0 ? f32x4{} : sum[t]);
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+          dot[t][s] = mma<HALF>(v[u], wide[s], fresh && u == 0 ? f32x4{} : dot[t][s]);
       }
+    }
   };
-  auto multiply = [&](const Tile& w, int c, auto whole) {
-    uint32_t word[2][4];
+  auto finish = [&](const uint32_t (&side)[NT][4], int q) {  // a group's sums
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      __builtin_memcpy(word[s], &w.c[s], 16);
+    for (int s = 0; s < NT; ++s) {
+      const uint32_t bits = side[s][q] & 0xFFFFu;
+      const float half = to_f32<Fp16>(Fp16{(uint16_t)bits});
+      const float sc = __uint_as_float((bits << 16 & is_bf16) | (__float_as_uint(half) & ~is_bf16));
+      const float off = (float)(side[s][q] >> 16);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[t][s][i] = fmaf(sc, fmaf(-off, sum[t][i], dot[t][s][i]), acc[t][s][i]);
+    }
+  };
+  auto spread_side = [&](const Side& w, uint32_t (&side)[NT][4]) {
+#pragma unroll
+    for (int s = 0; s < NT; ++s)
+      spread((uint32_t)w.s[s] | ((w.z[s] & given) + offset) << 16, side[s]);
+  };
+  auto words = [&](const i32x4 (&w)[NT], uint32_t (&word)[NT][4]) {
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+      __builtin_memcpy(word[s], &w[s], 16);
       exchange(word[s]);
     }
+  };
+
+  // The wave's whole tiles [lo, hi).  Loads past its last repeat that one, so that nothing
+  // branches between loads and products.
+  const int full = p.K / kCodes;
+  const int lo = (int)((int64_t)full * wk / WK), hi = (int)((int64_t)full * (wk + 1) / WK);
+  if (lo < hi) {
+    i32x4 w[kRing][NT];
+    Acts<E> x[kActs][MT];
+    Side next;
+    const int last = 4 * (hi - lo) - 1;  // quarter of a tile
+    auto load_acts = [&](Acts<E> (&to)[MT], int step) {
+      const int k = lo * kCodes + 32 * min(step, last);
 #pragma unroll
-    for (int q = 0; q < QUADS; ++q) {
-      // a group behind the row has no scale; its weights are padding
-      if (!decltype(whole)::value && c * kCodes + q * (kCodes / QUADS) >= p.K) break;
-      f32x4 dot[MT][2] = {}, sum[MT] = {};
+      for (int t = 0; t < MT; ++t) to[t].load(arow[t] + k);
+    };
 #pragma unroll
-      for (int j = q * 4 / QUADS; j < (q + 1) * 4 / QUADS; ++j) {
-        const int k = c * kCodes + 32 * j;
-        i32x4 wide[2];
+    for (int u = 0; u < kCodesAhead; ++u) load_codes(w[u], min(lo + u, hi - 1));
+    load_side(next, lo * QUADS);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) wide[s] = widen<HALF>(word[s][j]);
+    for (int u = 0; u < kActsAhead; ++u) load_acts(x[u], u);
+    for (int c0 = lo; c0 < hi; c0 += 4) {
+      uint32_t side[NT][4];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          Acts<E> x;
-          const int n = decltype(whole)::value ? 8 : p.K - k - 8 * quad;
-          if (n > 0)
-            x.load(arow[t] + k, n);
-          else
-            x = Acts<E>{};
+      for (int u = 0; u < 4; ++u) {
+        const int c = c0 + u;
+        if (c >= hi) break;
+        load_codes(w[(u + kCodesAhead) % kRing], min(c + kCodesAhead, hi - 1));
+        if (u % kRun == 0) {
+          spread_side(next, side);
+          load_side(next, (c + kRun) * QUADS);
+        }
+        uint32_t word[NT][4];
+        words(w[u % kRing], word);
 #pragma unroll
-          for (int u = 0; u < Acts<E>::kParts; ++u) {
-            sum[t] = mma<HALF>(ones, x.v[u], sum[t]);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) dot[t][s] = mma<HALF>(wide[s], x.v[u], dot[t][s]);
-          }
+        for (int j = 0; j < 4; ++j) {
+          load_acts(x[(4 * u + j + kActsAhead) % kActs], 4 * (c - lo) + j + kActsAhead);
+          multiply(word, j, x[(4 * u + j) % kActs]);
+          if ((j + 1) % (4 / QUADS) == 0)
+            finish(side, (u % kRun) * QUADS + j / (4 / QUADS));
+          __builtin_amdgcn_sched_barrier(0);  // keep to this order: registers
         }
       }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float sc = as_scale(w.s[s][q][i]);
-          const float off = zero ? 16.0f + (float)w.z[s][q][i] : 24.0f;
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-            acc[t][s][i] = fmaf(sc, fmaf(-off, sum[t][i], dot[t][s][i]), acc[t][s][i]);
-        }
     }
-  };
-  constexpr int U = 2;  // tiles of a wave under way
-  const int full = p.K / kCodes;
-  int c = wave;
-  for (; c + W * (U - 1) < full; c += W * U) {
-    Tile w[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(w[u], c + W * u);
-#pragma unroll
-    for (int u = 0; u < U; ++u) multiply(w[u], c + W * u, std::true_type{});
   }
-  for (; c < p.chunks; c += W) {
-    Tile w;
-    load(w, c);
-    multiply(w, c, std::false_type{});
+  if (full < p.chunks && wk == WK - 1) {  // the tile that the end of the rows cuts
+    i32x4 w[NT];
+    Side s;
+    uint32_t word[NT][4], side[NT][4];
+    load_codes(w, full);
+    load_side(s, full * QUADS);
+    words(w, word);
+    spread_side(s, side);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = full * kCodes + 32 * j;
+      Acts<E> x[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) x[t].load_head(arow[t] + k, p.K - k - 8 * quad);
+      multiply(word, j, x);
+      // a group that begins behind the row has no scale: its weights are padding
+      const int q = j / (4 / QUADS);
+      if ((j + 1) % (4 / QUADS) == 0 && full * kCodes + q * (kCodes / QUADS) < p.K)
+        finish(side, q);
+    }
   }
 
+  // A lane has rows 4 * quad .. + 3 of `a` against row `col` of the weights, and leaves
+  // with row `col` of out and columns 4 * quad .. + 3, after the sum over the WK waves.
+  const float* sums = (const float*)(part + wn * WK * NT * kWave);
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+  for (int t = 0; t < MT; ++t) {
+    if (t) __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 2; ++s) part[(wave * MT * 2 + t * 2 + s) * kWave + lane] = acc[t][s];
-  __syncthreads();
-  for (int t = wave; t < MT; t += W) {
-    f32x4 sum[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      sum[s] = part[(t * 2 + s) * kWave + lane];
-#pragma unroll
-      for (int w = 1; w < W; ++w) sum[s] += part[(w * MT * 2 + t * 2 + s) * kWave + lane];
-    }
-    // lane: row `col` of out, columns 4 * quad .. + 3 of each 16
+    for (int s = 0; s < NT; ++s) part[(wave * NT + s) * kWave + lane] = acc[t][s];
+    __syncthreads();
     const int m = r.lo + 16 * t + col;
-    if (m >= r.hi || source_row(p, m) < 0) continue;
-    float y[2][4];
+    const bool live = m < r.hi && source_row(p, m) >= 0;
+    constexpr int kSets = GLU ? NT / 2 : NT;  // sixteens of columns, dealt to the WK waves
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s0 = 0; s0 < kSets; s0 += WK) {
+      const int s = s0 + wk, n = first + 16 * s + 4 * quad;
+      if (!live || s >= kSets || n >= p.N) continue;
+      float y[GLU ? 2 : 1][4] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[s][i] = sum[s][i];
-    const int n = n0 + 4 * quad;
-    if (GLU) {
-      float h[4];
-      swiglu(y[0], y[1], h);
-      if (n < p.N) store_out(p, m, n, h);
-    } else {
+      for (int h = 0; h < (GLU ? 2 : 1); ++h)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (n + 16 * s < p.N) store_out(p, m, n + 16 * s, y[s]);
+        for (int k = 0; k < WK; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[h][i] += sums[((k * NT + s + h * (NT / 2)) * kWave + col / 4 * 16 + 4 * quad + i) * 4 +
+                            col % 4];
+      if constexpr (GLU) {
+        float h[4];
+        swiglu(y[0], y[1], h);
+        store_out(p, m, n, h);
+      } else {
+        store_out(p, m, n, y[0]);
+      }
     }
   }
 }
 
-template <typename E, int W, int MT, bool GLU, int QUADS>
-__global__ __launch_bounds__(W* kWave) void int4_stream(Int4Args p, int cols, int64_t first) {
-  __shared__ f32x4 part[W * MT * 2 * kWave];
-  __shared__ int counts[W];
+template <typename E, typename F, bool GLU, int QUADS>
+__global__ __launch_bounds__(F::W* kWave, F::MT == 1 ? 4 : 2) void int4_stream(Int4Args p,
+                                                                              int cols,
+                                                                              int64_t first) {
+  __shared__ f32x4 part[F::W * F::NT * kWave];
+  __shared__ int counts[F::W];
   const int64_t w = first + blockIdx.x;
   Rows r;
-  if (!find_rows(p, w / cols, 16 * MT, counts, r)) return;
-  const int n0 = (int)(w % cols) * (GLU ? 16 : 32), rows = r.hi - r.lo;
-  if (MT == 1 || rows <= 16)
-    int4_tile<E, W, 1, GLU, QUADS>(p, r, n0, part);
-  else if (MT == 2 || rows <= 32)
-    int4_tile<E, W, 2, GLU, QUADS>(p, r, n0, part);
-  else
-    int4_tile<E, W, MT, GLU, QUADS>(p, r, n0, part);
+  if (!find_rows(p, w / cols, 16 * F::MT, counts, r)) return;
+  int4_tile<E, F, GLU, QUADS>(p, r, (int)(w % cols) * (GLU ? F::kCols / 2 : F::kCols), part);
 }
 
-template <typename E, int W, int MT, bool GLU>
-void launch_of(const Int4Args& p, int group, int cols, int64_t tiles, hipStream_t stream) {
+template <typename F, bool GLU>
+int columns(const Int4Args& p) {
+  return (p.N + (GLU ? F::kCols / 2 : F::kCols) - 1) / (GLU ? F::kCols / 2 : F::kCols);
+}
+
+template <typename E, typename F, bool GLU>
+void launch_form(const Int4Args& p, int group, hipStream_t stream) {
+  const int cols = columns<F, GLU>(p);
+  const int64_t tiles = max_items(p.M, p.G, 16 * F::MT) * cols;
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (group == 128)
-      int4_stream<E, W, MT, GLU, 1><<<grid, W * kWave, 0, stream>>>(p, cols, first);
+      int4_stream<E, F, GLU, 1><<<grid, F::W * kWave, 0, stream>>>(p, cols, first);
     else if (group == 64)
-      int4_stream<E, W, MT, GLU, 2><<<grid, W * kWave, 0, stream>>>(p, cols, first);
+      int4_stream<E, F, GLU, 2><<<grid, F::W * kWave, 0, stream>>>(p, cols, first);
     else
-      int4_stream<E, W, MT, GLU, 4><<<grid, W * kWave, 0, stream>>>(p, cols, first);
+      int4_stream<E, F, GLU, 4><<<grid, F::W * kWave, 0, stream>>>(p, cols, first);
   }
 }
 
 template <typename E, bool GLU>
 void launch_matmul(const Int4Args& p, int group, hipStream_t stream) {
-  const int per = GLU ? 16 : 32, cols = (p.N + per - 1) / per;
+  using Few = Form<1, 2, 8, 1>;
+  using Thin = Form<1, 2, 4, 1>;
+  using Wide = Form<2, 4, 1, 4>;
+  using Tall = Form<4, 4, 1, 4>;
   const int64_t groups = p.G > 0 ? (p.G < p.M ? p.G : p.M) : 1;
-  if (p.M <= 16 || p.M < 4 * groups) {
-    const int64_t tiles = max_items(p.M, p.G, 16) * cols;
-    if (tiles <= 512)
-      launch_of<E, 8, 1, GLU>(p, group, cols, tiles, stream);
-    else
-      launch_of<E, 4, 1, GLU>(p, group, cols, tiles, stream);
+  const bool thin = p.M <= 16 || p.M < 4 * groups;
+  if (!thin && groups * columns<Wide, GLU>(p) >= 256) {
+    if (sizeof(E) == 4 || p.M < 24 * groups)
+      launch_form<E, Wide, GLU>(p, group, stream);
+    else if constexpr (sizeof(E) == 2)
+      launch_form<E, Tall, GLU>(p, group, stream);
+  } else if (max_items(p.M, p.G, 16) * columns<Thin, GLU>(p) <= 512) {
+    launch_form<E, Few, GLU>(p, group, stream);
   } else {
-    launch_of<E, 4, 4, GLU>(p, group, cols, max_items(p.M, p.G, 64) * cols, stream);
+    launch_form<E, Thin, GLU>(p, group, stream);
   }
 }
 
