@@ -228,7 +228,7 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
   const uint32_t given = zeros ? 0xFFu : 0u, offset = zeros ? 16u : 24u;
   auto load_codes = [&](i32x4 (&w)[NT], int c) {
 #pragma unroll
-    for (int s = 0; s < NT; ++s) w[s] = *(const i32x4*)(codes[s] + (size_t)c * kTileBytes);
+    for (int s = 0; s < NT; ++s) w[s] = __builtin_nontemporal_load((const i32x4*)(codes[s] + (size_t)c * kTileBytes));
   };
   auto load_side = [&](Side& w, int group) {  // of groups group .. + 3
     const size_t at = (size_t)min(group + quad, p.chunks * QUADS - 1) * kBlock;
@@ -384,7 +384,7 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
 }
 
 template <typename E, typename F, bool GLU, int QUADS>
-__global__ __launch_bounds__(F::W* kWave, F::MT == 1 ? 4 : 2) void int4_stream(Int4Args p,
+__global__ __launch_bounds__(F::W* kWave, F::NT == 2 ? 4 : 2) void int4_stream(Int4Args p,
                                                                               int cols,
                                                                               int64_t first) {
   __shared__ f32x4 part[F::W * F::NT * kWave];
@@ -415,21 +415,32 @@ void launch_form(const Int4Args& p, int group, hipStream_t stream) {
   }
 }
 
+// Which form.  With few rows in each group the weights bound, and a wave that takes 64 rows
+// of them over all of K has the most under way for the least start (one decode step's
+// gate/up, 64 rows over 44 groups, 376 MB: 68 us; four waves sharing K, 32 rows of weights
+// each, 93; two 87).  That needs enough groups: below kEnough workgroups the waves share K
+// (8 groups of one row: 24 us in the first form, 20 with four waves), all eight of them
+// where even then CUs would be left without a workgroup (one token, 8.4 MB: 6.1 us).  Groups
+// of more rows take tiles of 32 or 64 rows, for which weights are widened once.
 template <typename E, bool GLU>
 void launch_matmul(const Int4Args& p, int group, hipStream_t stream) {
   using Few = Form<1, 2, 8, 1>;
-  using Thin = Form<1, 2, 4, 1>;
+  using Mid = Form<1, 2, 4, 1>;
+  using Thin = Form<1, 4, 1, 2>;
   using Wide = Form<2, 4, 1, 4>;
   using Tall = Form<4, 4, 1, 4>;
+  constexpr int kEnough = 640, kCUs = 256;
   const int64_t groups = p.G > 0 ? (p.G < p.M ? p.G : p.M) : 1;
   const bool thin = p.M <= 16 || p.M < 4 * groups;
-  if (!thin && groups * columns<Wide, GLU>(p) >= 256) {
+  if (!thin && groups * columns<Wide, GLU>(p) >= kCUs) {
     if (sizeof(E) == 4 || p.M < 24 * groups)
       launch_form<E, Wide, GLU>(p, group, stream);
     else if constexpr (sizeof(E) == 2)
       launch_form<E, Tall, GLU>(p, group, stream);
-  } else if (max_items(p.M, p.G, 16) * columns<Thin, GLU>(p) <= 512) {
+  } else if (max_items(p.M, p.G, 16) * columns<Mid, GLU>(p) <= kCUs) {
     launch_form<E, Few, GLU>(p, group, stream);
+  } else if (max_items(p.M, p.G, 16) * columns<Thin, GLU>(p) < kEnough) {
+    launch_form<E, Mid, GLU>(p, group, stream);
   } else {
     launch_form<E, Thin, GLU>(p, group, stream);
   }
