@@ -837,7 +837,7 @@ int moe_grouped_outer(const moe_grouped_outer_args* args, hipStream_t stream);
 /*
  * moe_swiglu_backward -- the gradient of h = silu(g) * u for rows of pre = [g | u]:
  *   dpre[m][n] = dout[m][n] * u * (s + g * s * (1 - s)),  dpre[m][N+n] = dout[m][n] * g * s
- * with s = 1 / (1 + exp(-g)) (0 from g = -88 down), in float32 and rounded once.
+ * with s = 1 / (1 + exp(-g)) (0 below g = -174), in float32 and rounded once.
  * pre and dpre [M][2N], dout [M][N] of one element type, rows their strides apart, at any
  * element; dpre may be pre.  Errors : MOE_EINVAL, MOE_EUNSUPPORTED as above.  M = 0 is
  * valid and does nothing.

@@ -21,8 +21,10 @@ constexpr int kMaxRows = 1 << 30;
 
 // The gradient of silu(g) * u:
 //   dg = d * u * (s + v * (1 - s)),  du = d * v,  s = 1 / (1 + exp(-g)), v = g * s
-// s from exp(-|g|), which cannot overflow.  Bound by memory: five rows of N are read or
-// written.
+// s from exp(-|g|), which cannot overflow.  Below kLow, where 1 - s is 1 in float32, exp(g)
+// is applied as two factors exp(g / 2), so that a gradient that is still a normal number
+// keeps its value to g = -174.  Bound by memory: five rows of N are read or written (32768
+// rows of 2048 bf16, 671 MB: 118 us, 5.7 TB/s).
 template <typename E>
 __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const E* pre,
                                                             size_t pre_stride, const E* dout,
@@ -38,18 +40,32 @@ __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const 
   const int64_t m = id / chunks * per + t;
   if (t >= per || c >= pieces || m >= M) return;
   const int n = c * kN, left = N - n;
+  constexpr float kLow = -64.0f;
   Piece<E> g, u, d, dg, du;
+  float least = 0.0f;
   g.load_upto(pre + m * pre_stride + n, left);
   u.load_upto(pre + m * pre_stride + N + n, left);
   d.load_upto(dout + m * dout_stride + n, left);
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
     const float gf = to_f32<E>(g.e[i]), uf = to_f32<E>(u.e[i]), df = to_f32<E>(d.e[i]);
+    least = fminf(least, gf);
     const float e = __expf(-fabsf(gf)), near = 1.0f / (1.0f + e), far = e * near;
     const float s = gf < 0.0f ? far : near, rest = gf < 0.0f ? near : far;
     const float v = gf * s;
     dg.e[i] = from_f32<E>(df * uf * fmaf(v, rest, s));
     du.e[i] = from_f32<E>(df * v);
+  }
+  if (__builtin_expect(least < kLow, 0)) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float gf = to_f32<E>(g.e[i]), uf = to_f32<E>(u.e[i]), df = to_f32<E>(d.e[i]);
+      const float h = __expf(0.5f * gf);
+      if (gf < kLow) {
+        dg.e[i] = from_f32<E>((df * h) * (uf * (1.0f + gf) * h));
+        du.e[i] = from_f32<E>((df * h) * (gf * h));
+      }
+    }
   }
   dg.store_upto(dpre + m * dpre_stride + n, left);
   du.store_upto(dpre + m * dpre_stride + N + n, left);

@@ -328,6 +328,37 @@ def layer_step_int8(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row,
                                     row_dtype=row_dtype, inner_dtype=inner_dtype)
 
 
+def _layer_step(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, experts):
+    """Routes with demand and runs `experts` on the bucketing, after the checks that keep
+    what does not fit from being counted."""
+    experts.check(x, buf.T)
+    if x.dtype != torch.bfloat16 or not x.is_contiguous():
+        raise ValueError("x must be contiguous bfloat16 rows")
+    if (experts.S, experts.H) != (buf.S, buf.H):
+        raise ValueError(f"experts of {experts.S} slots and H = {experts.H} do not fit buffers of "
+                         f"{buf.S} and {buf.H}")
+    with torch.cuda.device(x.device):
+        route(buf, x, w_router, bias, expert_slot, torch.cuda.current_stream(), hist_row=hist_row)
+        return experts.forward(x, buf.slot_offsets, buf.perm, buf.sel_weight)
+
+
+def layer_step_int4(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, int4_experts):
+    """One pass of the layer with its experts in 4 bits (int4.Int4Experts, one group for each
+    of buf's S slots): route with demand, the experts on the rows of the bucketing, combine.
+    x [T, H] bf16, contiguous; returns [T, H] bf16.  On the current stream of x's device.
+    What does not fit is refused before the demand is counted."""
+    return _layer_step(buf, x, w_router, bias, expert_slot, hist_row, int4_experts)
+
+
+def layer_step_grouped(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row,
+                       grouped_experts):
+    """One pass of the layer with its experts in bf16 (grouped.GroupedExperts, one group for
+    each of buf's S slots), as layer_step_int4.  Gradients pass to the experts' matrices and,
+    through them, to x; the routing itself (the picks and their weights) is computed
+    without a gradient."""
+    return _layer_step(buf, x, w_router, bias, expert_slot, hist_row, grouped_experts)
+
+
 class SharedArena:
     """One arena shared by L layers: the [L][E] slot table and the [L][E]
     float64 demand history on the device, plus the re-plan flow.

@@ -113,3 +113,11 @@ def worst(got, want, tol):
     ratio = torch.where(d <= 0, torch.zeros_like(d), d / tol.clamp_min(1e-300))
     return float(torch.where(torch.isfinite(got.double()), ratio,
                              torch.full_like(ratio, float("inf"))).max())
+
+
+def within(got, want, tol) -> bool:
+    """worst() at most 1 (a name of its own, so that a failure prints one number)."""
+    ratio = worst(got, want, tol)
+    if not ratio <= 1:
+        print(f"off by {ratio:.3f} of the bound", flush=True)
+    return ratio <= 1
