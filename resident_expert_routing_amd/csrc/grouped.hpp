@@ -68,13 +68,15 @@ __device__ __forceinline__ f32x4 mma<float>(i32x4 w, i32x4 x, f32x4 acc) {
   return acc;
 }
 
-constexpr int kTWaves = 8;     // two down by four across
-constexpr int kTThreads = kTWaves * kWave;
 constexpr int kStep = 128;     // bytes of contraction a stage
-constexpr int kCols = 256;     // columns of a tile
 constexpr int kMostRows = 320;
-constexpr int kOutBytes = 16384;  // LDS that a wave's results pass through
-constexpr int kTileLds = 2 * (kMostRows + kCols) * kStep;
+
+// A workgroup has two waves down by WA across; a wave has 64 columns.
+template <int WA>
+struct Wide {
+  static constexpr int kCols = 64 * WA, kWaves = 2 * WA, kThreads = kWaves * kWave;
+};
+constexpr int kSmall = 1, kLarge = 4;  // WA of products of few tiles, and of the others
 
 // Where an operand that lies across its contraction is in LDS: a stage is kStep /
 // sizeof(E) rows of W elements, 16-byte pieces of a row swapped so that the places
@@ -127,8 +129,8 @@ struct Src {
   int n;
 };
 
-// The main loop.  A stage holds kRows rows (LEFT across: columns) of the left operand
-// and 256 of the right one, kStep bytes of contraction each, in a ring of S; from_left(i, j,
+// The main loop.  A stage holds 32 * MF rows (LEFT across: columns) of the left
+// operand and 64 * WA of the right one, kStep bytes of contraction each, in a ring of S; from_left(i, j,
 // row, piece) and from_right say where the 16-byte piece of stage i is in memory that the
 // wave's load j of the operand takes, `row` the row (across: the contraction step) and
 // `piece` the piece in it; before(i) is called ahead of the loads of stage i.  DMA: loads go to
@@ -139,20 +141,20 @@ struct Src {
 // ahead (the right operand's a half stage ahead), and the loads of stage i + S - 1 are
 // issued one for each group; a wave at its products goes before the SIMD's other one at
 // its loads.
-template <typename E, bool LEFT, bool RIGHT, bool SPLIT, int MF, int S, bool DMA, bool ONCE,
-          typename FB, typename FL, typename FR>
+template <typename E, bool LEFT, bool RIGHT, bool SPLIT, int WA, int MF, int S, bool DMA,
+          bool ONCE, typename FB, typename FL, typename FR>
 __device__ __forceinline__ void products(uint8_t* smem, int steps, FB before, FL from_left,
                                          FR from_right, f32x4 (&acc)[MF][4]) {
-  constexpr int kRows = 32 * MF;
+  constexpr int kRows = 32 * MF, kCols = Wide<WA>::kCols, kWaves = Wide<WA>::kWaves;
   constexpr int kStage = (kRows + kCols) * kStep;
-  constexpr int kLoadsL = kRows / 8 / kTWaves, kLoadsR = kCols / 8 / kTWaves;
+  constexpr int kLoadsL = kRows / 8 / kWaves, kLoadsR = kCols / 8 / kWaves;
+  static_assert(kLoadsL * 8 * kWaves == kRows, "whole loads");
   constexpr int kLoads = kLoadsL + kLoadsR;
   constexpr int kPiece = 16 / (int)sizeof(E);
-  static_assert(S * kStage <= kTileLds, "LDS");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane & 15, quad = lane >> 4;
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / WA, wn = wave % WA;
 
   // load j of a wave: LDS bytes 1024 * (wave * n + j) + 16 * lane of the operand's part
   auto source = [&](int i, int j) {
@@ -200,7 +202,7 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FB before, FL
       const uint8_t* r = at + kRows * kStep;
       if constexpr (RIGHT)
         return read_across<E, kCols>(
-            r, SPLIT ? (s >= 2 ? 128 : 0) + wn * 32 + 16 * (s & 1) : wn * 64 + 16 * s, c);
+            r, SPLIT ? (s >= 2 ? kCols / 2 : 0) + wn * 32 + 16 * (s & 1) : wn * 64 + 16 * s, c);
       else
         return *(const i32x4*)(r + (wn * 64 + 16 * s + col) * kStep + slot[c]);
     };
@@ -274,7 +276,7 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FB before, FL
   }
 }
 
-// NS fragments of 16 columns of a wave's rows leave through its part of LDS, so that
+// NS fragments of 16 columns of a wave's rows leave through its BYTES of LDS, so that
 // lanes store consecutive bytes of a row of out: value(f, s, e) is column 4 * quad + e of
 // fragment s (JOIN: 4 * NS * quad + 4 * s + e) in row `col` of fragment f.  to(row, c)
 // says where the 16-byte piece c of the wave's row goes and how many of its elements (n
@@ -285,10 +287,10 @@ struct Dst {
   int n;
   bool zero;
 };
-template <typename E, int MF, int NS, bool JOIN, typename V, typename T>
+template <typename E, int MF, int NS, bool JOIN, int BYTES, typename V, typename T>
 __device__ __forceinline__ void store_rows(uint8_t* mine, V value, T to) {
   constexpr int kRowBytes = 16 * NS * (int)sizeof(E), kPieces = kRowBytes / 16;
-  constexpr int kPart = part_of(MF, kOutBytes / kRowBytes / 16);
+  constexpr int kPart = part_of(MF, BYTES / kRowBytes / 16);
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   auto place = [&](int x, int c) {
     return mine + x * kRowBytes + 16 * (c ^ (x & (kPieces - 1) & 7));
@@ -330,7 +332,7 @@ struct Live {
   uint8_t row[kMostRows];  // 1: computed, 2: set to zero, 0: left
 };
 
-template <typename E, bool ACROSS, bool GLU, int MF, int S, bool DMA, bool ONCE>
+template <typename E, bool ACROSS, bool GLU, int WA, int MF, int S, bool DMA, bool ONCE>
 __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, int n0,
                                           uint8_t* smem, Live& live) {
   constexpr int kPiece = 16 / (int)sizeof(E);
@@ -339,11 +341,12 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
   constexpr int kOut = GLU ? 8 : 16;          // how many
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / WA, wn = wave % WA;
   const E* b = (const E*)p.b + (size_t)r.g * p.b_group_stride;
 
   // the rows of a and (along) of b that the lane loads
-  constexpr int kLoadsL = MF / 2, kLoadsR = kCols / 64;
+  constexpr int kCols = Wide<WA>::kCols, kHalf = kCols / 2;
+  constexpr int kLoadsL = 2 * MF / WA, kLoadsR = kCols / 16 / WA;  // 8 rows each
   const E* arow[kLoadsL];
 #pragma unroll
   for (int j = 0; j < kLoadsL; ++j) {
@@ -369,8 +372,8 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
   auto from_right = [&](int i, int j, int row, int piece) {
     if constexpr (ACROSS) {
       const int k = i * kC + row, c = piece * kPiece;
-      const int n = n0 + (GLU ? c & 127 : c);
-      return Src<E>{b + (size_t)k * p.b_stride + (GLU && c >= 128 ? p.N : 0) + n,
+      const int n = n0 + (GLU ? c % kHalf : c);
+      return Src<E>{b + (size_t)k * p.b_stride + (GLU && c >= kHalf ? p.N : 0) + n,
                     k < p.K ? p.N - n : 0};
     } else {
       const int k = i * kC + piece * kPiece;
@@ -379,14 +382,15 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
   };
 
   f32x4 acc[MF][4] = {};
-  for (int t = threadIdx.x; t < 32 * MF; t += kTThreads) {
+  for (int t = threadIdx.x; t < 32 * MF; t += Wide<WA>::kThreads) {
     const bool in = r.lo + t < r.hi;
     live.row[t] = !in ? 0 : source_row(p, r.lo + t) >= 0 ? 1 : p.zero_rest ? 2 : 0;
   }
-  products<E, false, ACROSS, GLU, MF, S, DMA, ONCE>(
+  products<E, false, ACROSS, GLU, WA, MF, S, DMA, ONCE>(
       smem, (p.K + kC - 1) / kC, [](int) {}, from_left, from_right, acc);
   barrier();  // every wave has read the last stage
-  uint8_t* mine = smem + wave * kOutBytes;
+  constexpr int kBytes = WA == kLarge ? 16384 : 8192;  // LDS that a wave's results pass through
+  uint8_t* mine = smem + wave * kBytes;
   auto to = [&](void* out, size_t stride, int at, int N, int row, int c) {
     const int t = wm * MF * 16 + row, n = at + c * kPiece;
     return Dst<E>{(E*)out + (size_t)(r.lo + t) * stride + n, live.row[t] ? N - n : 0,
@@ -397,7 +401,7 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
     if (p.pre) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        store_rows<E, MF, 2, JOIN>(
+        store_rows<E, MF, 2, JOIN, kBytes>(
             mine, [&](int f, int s, int e) { return acc[f][2 * h + s][e]; },
             [&](int row, int c) {
               return to((E*)p.pre + (size_t)h * p.N, p.pre_stride, n, p.N, row, c);
@@ -412,11 +416,11 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[f][j / 4][j % 4] = y[j];
     }
-    store_rows<E, MF, 2, JOIN>(
+    store_rows<E, MF, 2, JOIN, kBytes>(
         mine, [&](int f, int s, int e) { return acc[f][s][e]; },
         [&](int row, int c) { return to(p.out, p.out_stride, n, p.N, row, c); });
   } else {
-    store_rows<E, MF, 4, JOIN>(
+    store_rows<E, MF, 4, JOIN, kBytes>(
         mine, [&](int f, int s, int e) { return acc[f][s][e]; },
         [&](int row, int c) { return to(p.out, p.out_stride, n0 + wn * 64, p.N, row, c); });
   }
@@ -434,46 +438,71 @@ __device__ __forceinline__ void zero_rows(void* out, size_t stride, const Rows& 
   }
 }
 
+// The rows of a workgroup, or the rest that it sets to zero.
+template <typename E, int WA, bool GLU>
+__device__ __forceinline__ bool tile_rows(const RowsProduct& p, int R, int64_t item, int n0,
+                                          int* counts, Rows& r) {
+  int64_t total = 0;
+  if (find_rows(p, item, R, counts, r, total)) return true;
+  constexpr int kWide = Wide<WA>::kCols / (GLU ? 2 : 1);
+  if (p.zero_rest && rest_rows(p, item - total, R, r))
+    zero_rows<E>(p.out, p.out_stride, r, n0, min(n0 + kWide, p.N));
+  return false;
+}
+
 template <typename E, bool ACROSS, bool GLU, bool DMA>
-__global__ __launch_bounds__(kTThreads, 2) void rows_tiles(RowsProduct p, int R, int cols,
-                                                          bool blocks, int64_t first) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kTileLds];
+__global__ __launch_bounds__(Wide<kLarge>::kThreads, 2) void rows_tiles(RowsProduct p, int R,
+                                                                       int cols, bool blocks,
+                                                                       int64_t first) {
+  constexpr int WA = kLarge;
+  __shared__ __attribute__((aligned(1024))) uint8_t
+      smem[2 * (kMostRows + Wide<WA>::kCols) * kStep];
   __shared__ Live live;
-  __shared__ int counts[kTWaves];
-  int64_t item, total = 0;
+  __shared__ int counts[Wide<WA>::kWaves];
+  int64_t item;
   int col;
   Rows r;
   tile_of(first + blockIdx.x, blocks, cols, item, col);
   if (col >= cols) return;
-  constexpr int kWide = GLU ? kCols / 2 : kCols;
-  const int n0 = col * kWide;
-  if (!find_rows(p, item, R, counts, r, total)) {
-    if (p.zero_rest && rest_rows(p, item - total, R, r))
-      zero_rows<E>(p.out, p.out_stride, r, n0, min(n0 + kWide, p.N));
-    return;
-  }
+  const int n0 = col * (Wide<WA>::kCols / (GLU ? 2 : 1));
+  if (!tile_rows<E, WA, GLU>(p, R, item, n0, counts, r)) return;
   const int rows = r.hi - r.lo;
   if constexpr (DMA) {
     if (rows <= 64 && r.all)
-      rows_tile<E, ACROSS, GLU, 2, 3, true, true>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 2, 3, true, true>(p, r, n0, smem, live);
     else if (rows <= 64)
-      rows_tile<E, ACROSS, GLU, 2, 3, true, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 2, 3, true, false>(p, r, n0, smem, live);
     else if (rows <= 128)
-      rows_tile<E, ACROSS, GLU, 4, 3, true, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 4, 3, true, false>(p, r, n0, smem, live);
     else if (rows <= 192)
-      rows_tile<E, ACROSS, GLU, 6, 2, true, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 6, 2, true, false>(p, r, n0, smem, live);
     else if (rows <= 256)
-      rows_tile<E, ACROSS, GLU, 8, 2, true, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 8, 2, true, false>(p, r, n0, smem, live);
     else
-      rows_tile<E, ACROSS, GLU, 10, 2, true, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 10, 2, true, false>(p, r, n0, smem, live);
   } else {
     if (rows <= 64)
-      rows_tile<E, ACROSS, GLU, 2, 2, false, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 2, 2, false, false>(p, r, n0, smem, live);
     else if (rows <= 128)
-      rows_tile<E, ACROSS, GLU, 4, 2, false, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 4, 2, false, false>(p, r, n0, smem, live);
     else
-      rows_tile<E, ACROSS, GLU, 8, 2, false, false>(p, r, n0, smem, live);
+      rows_tile<E, ACROSS, GLU, WA, 8, 2, false, false>(p, r, n0, smem, live);
   }
+}
+
+// Products of few tiles: 64 rows by 64 columns, two waves.
+template <typename E, bool ACROSS, bool GLU>
+__global__ __launch_bounds__(Wide<kSmall>::kThreads, 2) void rows_small(RowsProduct p, int cols,
+                                                                       int64_t first) {
+  constexpr int WA = kSmall;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (64 + Wide<WA>::kCols) * kStep];
+  __shared__ Live live;
+  __shared__ int counts[Wide<WA>::kWaves];
+  const int64_t id = first + blockIdx.x;
+  const int n0 = (int)(id % cols) * (Wide<WA>::kCols / (GLU ? 2 : 1));
+  Rows r;
+  if (!tile_rows<E, WA, GLU>(p, 64, id / cols, n0, counts, r)) return;
+  rows_tile<E, ACROSS, GLU, WA, 2, 2, false, false>(p, r, n0, smem, live);
 }
 
 // Most rows of a tile: more rows share a load of b's, but a product of few tiles may
@@ -492,9 +521,23 @@ inline int rows_of_tile(int M, int G, int cols, bool dma) {
   return best;
 }
 
+// Below so many tiles, of 64 rows even, most of the 256 CUs would be left without one.
+constexpr int kFewTiles = 192;
+
 template <typename E, bool ACROSS, bool GLU>
 void launch_rows_tiles(const RowsProduct& p, bool dma, hipStream_t stream) {
-  const int per = GLU ? kCols / 2 : kCols, cols = (p.N + per - 1) / per;
+  constexpr int per = Wide<kLarge>::kCols / (GLU ? 2 : 1);
+  const int cols = (p.N + per - 1) / per;
+  if ((p.M / 64 + (int64_t)(p.G < p.M ? p.G : p.M)) * cols < kFewTiles) {
+    constexpr int small = Wide<kSmall>::kCols / (GLU ? 2 : 1);
+    const int scols = (p.N + small - 1) / small;
+    const int64_t all = (max_items(p.M, p.G, 64) + (p.zero_rest ? 2 : 0)) * scols;
+    for (int64_t first = 0; first < all; first += kMaxGrid) {
+      const unsigned grid = (unsigned)(all - first < kMaxGrid ? all - first : kMaxGrid);
+      rows_small<E, ACROSS, GLU><<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, scols, first);
+    }
+    return;
+  }
   const int R = rows_of_tile(p.M, p.G, cols, dma);
   const int64_t items = max_items(p.M, p.G, R) + (p.zero_rest ? 2 : 0);
   const bool blocks = p.M > 128 * (int64_t)p.G && items * cols >= 2048;
@@ -506,9 +549,9 @@ void launch_rows_tiles(const RowsProduct& p, bool dma, hipStream_t stream) {
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (dma)
-      rows_tiles<E, ACROSS, GLU, true><<<grid, kTThreads, 0, stream>>>(p, R, cols, blocks, first);
+      rows_tiles<E, ACROSS, GLU, true><<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, R, cols, blocks, first);
     else
-      rows_tiles<E, ACROSS, GLU, false><<<grid, kTThreads, 0, stream>>>(p, R, cols, blocks, first);
+      rows_tiles<E, ACROSS, GLU, false><<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, R, cols, blocks, first);
   }
 }
 
@@ -543,21 +586,23 @@ int launch_rows_product(const RowsProduct& p, bool across, bool glu, hipStream_t
 constexpr int kTable = 2048;
 enum { kNone, kLeft, kRight };  // the operand that has an index
 
-template <typename E, bool DMA, int INDEXED>
-__global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int down, int across,
-                                                           int64_t first) {
-  constexpr int MF = 8;
+template <typename E, int WA, int MF, bool DMA, int INDEXED>
+__global__ __launch_bounds__(Wide<WA>::kThreads, 2) void outer_tiles(OuterProduct p, int down,
+                                                                    int across, int64_t first) {
+  constexpr int kRows = 32 * MF, kCols = Wide<WA>::kCols, kThreads = Wide<WA>::kThreads;
   constexpr int kPiece = 16 / (int)sizeof(E);
   constexpr int kC = kStep / (int)sizeof(E);
-  constexpr int kLoads = 4;  // of each operand
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (256 + kCols) * kStep];
+  constexpr int kLoads = 2 * MF / WA;  // of each operand
+  static_assert(kRows == kCols, "both operands' loads take the same rows");
+  constexpr int kBytes = 2 * (kRows + kCols) * kStep;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kBytes];
   __shared__ int table[INDEXED == kNone ? 1 : kTable];
   const int64_t id = first + blockIdx.x;
   const int g = (int)(id / ((int64_t)down * across)), at = (int)(id % ((int64_t)down * across));
-  const int l0 = at / across * 256, r0 = at % across * kCols;
+  const int l0 = at / across * kRows, r0 = at % across * kCols;
   const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / WA, wn = wave % WA;
 
   f32x4 acc[MF][4] = {};
   constexpr int kRun = INDEXED == kNone ? 1 << 30 : kTable;
@@ -568,7 +613,7 @@ __global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int 
       const int32_t* index = INDEXED == kLeft ? p.left_index : p.right_index;
       const int div = INDEXED == kLeft ? p.left_div : p.right_div;
       const int rows = INDEXED == kLeft ? p.left_rows : p.right_rows;
-      for (int t = threadIdx.x; t < n; t += kTThreads) {
+      for (int t = threadIdx.x; t < n; t += kThreads) {
         int r = index[m0 + t];
         r = r < 0 ? -1 : r / div;
         table[t] = (unsigned)r < (unsigned)rows ? r : -1;
@@ -581,7 +626,7 @@ __global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int 
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           const int row =
-              i * kC + ((wave * kLoads + j) * 64 + (int)(threadIdx.x & 63)) / (256 / kPiece);
+              i * kC + ((wave * kLoads + j) * 64 + (int)(threadIdx.x & 63)) / (kCols / kPiece);
           row_of[j] = row < n ? table[row] : -1;
         }
       }
@@ -599,13 +644,14 @@ __global__ __launch_bounds__(kTThreads, 2) void outer_tiles(OuterProduct p, int 
       const int r = INDEXED == kRight ? row_of[j] : m0 + t;
       return Src<E>{(const E*)p.right + (size_t)r * p.right_stride + c, in ? p.R - c : 0};
     };
-    products<E, true, true, false, MF, 2, DMA, false>(smem, (n + kC - 1) / kC, before, from_left,
+    products<E, true, true, false, WA, MF, 2, DMA, false>(smem, (n + kC - 1) / kC, before, from_left,
                                                       from_right, acc);
   }
   barrier();
   E* out = (E*)p.out + (size_t)g * p.out_group_stride;
-  store_rows<E, MF, 4, false>(
-      smem + wave * kOutBytes, [&](int f, int s, int e) { return acc[f][s][e]; },
+  constexpr int kMine = kBytes / Wide<WA>::kWaves;
+  store_rows<E, MF, 4, false, kMine>(
+      smem + wave * kMine, [&](int f, int s, int e) { return acc[f][s][e]; },
       [&](int row, int c) {
         const int l = l0 + wm * MF * 16 + row, n = r0 + wn * 64 + c * kPiece;
         return Dst<E>{out + (size_t)l * p.out_stride + n, l < p.L ? p.R - n : 0, false};
@@ -616,14 +662,21 @@ template <typename E, int INDEXED>
 void launch_outer_tiles(const OuterProduct& p, hipStream_t stream) {
   const bool dma = whole_pieces<E>(p.left, p.left_stride, 0, p.L) &&
                    whole_pieces<E>(p.right, p.right_stride, 0, p.R);
-  const int down = (p.L + 255) / 256, across = (p.R + kCols - 1) / kCols;
-  const int64_t tiles = (int64_t)p.G * down * across;
+  auto tiles_of = [&](int n) { return (int64_t)p.G * ((p.L + n - 1) / n) * ((p.R + n - 1) / n); };
+  const bool few = tiles_of(256) < kFewTiles;
+  const int side = few ? 64 : 256, down = (p.L + side - 1) / side, across = (p.R + side - 1) / side;
+  const int64_t tiles = tiles_of(side);
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
-    if (dma)
-      outer_tiles<E, true, INDEXED><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
+    if (few)
+      outer_tiles<E, kSmall, 2, false, INDEXED>
+          <<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, down, across, first);
+    else if (dma)
+      outer_tiles<E, kLarge, 8, true, INDEXED>
+          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, first);
     else
-      outer_tiles<E, false, INDEXED><<<grid, kTThreads, 0, stream>>>(p, down, across, first);
+      outer_tiles<E, kLarge, 8, false, INDEXED>
+          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, first);
   }
 }
 
