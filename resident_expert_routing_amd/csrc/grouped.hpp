@@ -505,6 +505,128 @@ __global__ __launch_bounds__(Wide<kSmall>::kThreads, 2) void rows_small(RowsProd
   rows_tile<E, ACROSS, GLU, WA, 2, 2, false, false>(p, r, n0, smem, live);
 }
 
+// Streaming form, for few rows in few groups, b along its rows: a workgroup takes 32 rows of b
+// (with SwiGLU, 16 gate rows and their 16 up rows) and up to 16 rows of one group, its
+// waves each a run of K; the sums are added through LDS in a fixed order.  b goes from
+// memory straight to the registers of the matrix instruction (lane l: row l % 16, bytes 16
+// (l / 16) of 64), from any address, kAhead steps before its products.
+constexpr int kSWaves = 8;
+
+template <typename E, bool GLU>
+__global__ __launch_bounds__(kSWaves* kWave) void rows_stream(RowsProduct p, int cols,
+                                                             int64_t first) {
+  constexpr int kPiece = 16 / (int)sizeof(E), kC = kStep / (int)sizeof(E);
+  constexpr int kRing = 4, kAhead = kRing - 1;
+  __shared__ f32x4 part[kSWaves][2][kWave];
+  __shared__ int counts[kSWaves];
+  const int64_t id = first + blockIdx.x;
+  const int n0 = (int)(id % cols) * (GLU ? 16 : 32);
+  Rows r;
+  int64_t total = 0;
+  if (!find_rows(p, id / cols, 16, counts, r, total)) {
+    if (p.zero_rest && rest_rows(p, id / cols - total, 16, r))
+      zero_rows<E>(p.out, p.out_stride, r, n0, min(n0 + (GLU ? 16 : 32), p.N));
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane & 15, quad = lane >> 4;
+  const E* b = (const E*)p.b + (size_t)r.g * p.b_group_stride + kPiece * quad;
+  const E* row[3];  // two of b, one of a
+  row[0] = b + (size_t)min(n0 + col, p.N - 1) * p.b_stride;
+  row[1] = b + (size_t)(GLU ? p.N + min(n0 + col, p.N - 1) : min(n0 + 16 + col, p.N - 1)) *
+                   p.b_stride;
+  const int src = source_row(p, min(r.lo + col, r.hi - 1));
+  row[2] = (const E*)p.a + (size_t)max(src, 0) * p.a_stride + kPiece * quad;
+
+  struct Step {
+    i32x4 v[3][2];
+  };
+  auto load = [&](Step& w, int c) {
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w.v[s][h] = __builtin_bit_cast(i32x4, *(const u32x4*)(row[s] + c * kC + h * (kC / 2)));
+  };
+  f32x4 acc[2] = {};
+  auto multiply = [&](const Step& w) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) acc[s] = mma<E>(w.v[s][h], w.v[2][h], acc[s]);
+  };
+  // the wave's whole steps [lo, hi); loads past its last repeat that one
+  const int full = p.K / kC;
+  const int lo = (int)((int64_t)full * wave / kSWaves);
+  const int hi = (int)((int64_t)full * (wave + 1) / kSWaves);
+  if (lo < hi) {
+    Step w[kRing];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(w[u], min(lo + u, hi - 1));
+    for (int c0 = lo; c0 < hi; c0 += kRing) {
+#pragma unroll
+      for (int u = 0; u < kRing; ++u) {
+        if (c0 + u >= hi) break;
+        load(w[(u + kAhead) % kRing], min(c0 + u + kAhead, hi - 1));
+        multiply(w[u]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  if (p.K % kC && wave == kSWaves - 1) {  // what the end of the rows leaves of a step
+    Step w;
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = full * kC + h * (kC / 2), n = p.K - k - kPiece * quad;
+        Piece<E> u{};
+        if (n > 0) u.load_upto(row[s] + k, n);
+        __builtin_memcpy(&w.v[s][h], u.e, 16);
+      }
+    multiply(w);
+  }
+
+#pragma unroll
+  for (int s = 0; s < 2; ++s) part[wave][s][lane] = acc[s];
+  __syncthreads();
+  // lane: row `col` of out, columns 4 * quad .. + 3 of each 16
+  const int m = r.lo + col, n = n0 + 4 * quad;
+  const bool live = m < r.hi && src >= 0;
+  if (wave > 0 || m >= r.hi || !(live || p.zero_rest)) return;
+  f32x4 sum[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    sum[s] = part[0][s][lane];
+#pragma unroll
+    for (int w = 1; w < kSWaves; ++w) sum[s] += part[w][s][lane];
+  }
+  auto store = [&](void* out, size_t stride, int at, const float (&y)[4]) {
+    Piece<E, 4> o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.e[i] = from_f32<E>(live ? y[i] : 0.0f);
+    if (at < p.N) o.store_upto((E*)out + (size_t)m * stride + at, p.N - at);
+  };
+  float y[2][4];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[s][i] = sum[s][i];
+  if constexpr (GLU) {
+    if (p.pre) {
+      store(p.pre, p.pre_stride, n, y[0]);
+      store((E*)p.pre + p.N, p.pre_stride, n, y[1]);
+    }
+    float h[4];
+    swiglu(y[0], y[1], h);
+    store(p.out, p.out_stride, n, h);
+  } else {
+    store(p.out, p.out_stride, n, y[0]);
+    store(p.out, p.out_stride, n + 16, y[1]);
+  }
+}
+
 // Most rows of a tile: more rows share a load of b's, but a product of few tiles may
 // then leave more of the 256 CUs without one; its time goes as rounds * (rows + 256).
 inline int rows_of_tile(int M, int G, int cols, bool dma) {
@@ -521,14 +643,28 @@ inline int rows_of_tile(int M, int G, int cols, bool dma) {
   return best;
 }
 
-// Below so many tiles, of 64 rows even, most of the 256 CUs would be left without one.
+// Below so many tiles, of 64 rows even, most of the 256 CUs would be left without one: then
+// 64 x 64 tiles, or with few rows in each group the streaming form (8 groups of one row, K
+// 4096, 2N 4096: 51 us, 5.2 TB/s; at 16 groups, 256 tiles, it takes 100 where tiles take 81).
 constexpr int kFewTiles = 192;
 
 template <typename E, bool ACROSS, bool GLU>
 void launch_rows_tiles(const RowsProduct& p, bool dma, hipStream_t stream) {
   constexpr int per = Wide<kLarge>::kCols / (GLU ? 2 : 1);
   const int cols = (p.N + per - 1) / per;
-  if ((p.M / 64 + (int64_t)(p.G < p.M ? p.G : p.M)) * cols < kFewTiles) {
+  const int64_t groups = p.G < p.M ? p.G : p.M, few = (p.M / 64 + groups) * cols;
+  if constexpr (!ACROSS) {
+    if (few < kFewTiles && (p.M <= 16 || p.M < 4 * groups)) {
+      const int scols = (p.N + (GLU ? 15 : 31)) / (GLU ? 16 : 32);
+      const int64_t all = (max_items(p.M, p.G, 16) + (p.zero_rest ? 2 : 0)) * scols;
+      for (int64_t first = 0; first < all; first += kMaxGrid) {
+        const unsigned grid = (unsigned)(all - first < kMaxGrid ? all - first : kMaxGrid);
+        rows_stream<E, GLU><<<grid, kSWaves * kWave, 0, stream>>>(p, scols, first);
+      }
+      return;
+    }
+  }
+  if (few < kFewTiles) {
     constexpr int small = Wide<kSmall>::kCols / (GLU ? 2 : 1);
     const int scols = (p.N + small - 1) / small;
     const int64_t all = (max_items(p.M, p.G, 64) + (p.zero_rest ? 2 : 0)) * scols;
@@ -588,7 +724,8 @@ enum { kNone, kLeft, kRight };  // the operand that has an index
 
 template <typename E, int WA, int MF, bool DMA, int INDEXED>
 __global__ __launch_bounds__(Wide<WA>::kThreads, 2) void outer_tiles(OuterProduct p, int down,
-                                                                    int across, int64_t first) {
+                                                                    int across, bool blocks,
+                                                                    int64_t first) {
   constexpr int kRows = 32 * MF, kCols = Wide<WA>::kCols, kThreads = Wide<WA>::kThreads;
   constexpr int kPiece = 16 / (int)sizeof(E);
   constexpr int kC = kStep / (int)sizeof(E);
@@ -597,9 +734,12 @@ __global__ __launch_bounds__(Wide<WA>::kThreads, 2) void outer_tiles(OuterProduc
   constexpr int kBytes = 2 * (kRows + kCols) * kStep;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kBytes];
   __shared__ int table[INDEXED == kNone ? 1 : kTable];
-  const int64_t id = first + blockIdx.x;
-  const int g = (int)(id / ((int64_t)down * across)), at = (int)(id % ((int64_t)down * across));
-  const int l0 = at / across * kRows, r0 = at % across * kCols;
+  int64_t item;
+  int col;
+  tile_of(first + blockIdx.x, blocks, across, item, col);
+  const int64_t group = item / down;
+  if (col >= across || group >= p.G) return;
+  const int g = (int)group, l0 = (int)(item % down) * kRows, r0 = col * kCols;
   const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WA, wn = wave % WA;
@@ -665,18 +805,28 @@ void launch_outer_tiles(const OuterProduct& p, hipStream_t stream) {
   auto tiles_of = [&](int n) { return (int64_t)p.G * ((p.L + n - 1) / n) * ((p.R + n - 1) / n); };
   const bool few = tiles_of(256) < kFewTiles;
   const int side = few ? 64 : 256, down = (p.L + side - 1) / side, across = (p.R + side - 1) / side;
-  const int64_t tiles = tiles_of(side);
+  // Blocks of tiles for each XCD, whose L2 then serves each operand's columns several times,
+  // pay where there are many tiles of many rows (64 groups of 512 rows, 4096 x 4096: 1424 us
+  // against 1367), and cost where there are fewer (32 of 460, 2048 x 4096: 296 against 311) or
+  // only zeros are written (230 groups without rows: 1190 against 1300).
+  const bool blocks = tiles_of(side) >= 8192 && p.M >= 256 * (int64_t)p.G;
+  const int64_t items = (int64_t)p.G * down;
+  const int64_t tiles =
+      blocks ? (int64_t)up_to((items + kBlockItems - 1) / kBlockItems *
+                                  ((across + kBlockCols - 1) / kBlockCols), 8) *
+                   kBlockItems * kBlockCols
+             : items * across;
   for (int64_t first = 0; first < tiles; first += kMaxGrid) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (few)
       outer_tiles<E, kSmall, 2, false, INDEXED>
-          <<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, down, across, first);
+          <<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, down, across, blocks, first);
     else if (dma)
       outer_tiles<E, kLarge, 8, true, INDEXED>
-          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, first);
+          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, blocks, first);
     else
       outer_tiles<E, kLarge, 8, false, INDEXED>
-          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, first);
+          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, blocks, first);
   }
 }
 
