@@ -769,8 +769,9 @@ int moe_int8_matmul(const moe_int8_matmul_args* args, hipStream_t stream);
  *          each group N (2N) rows of K elements b_stride apart, or with b_across K rows
  *          of N (2N); groups b_group_stride elements apart (0: all groups share one).
  * Outputs: out, rows out_stride elements apart (>= N); with swiglu pre (nullable), the
- *          products z before SwiGLU [M][2N] in the element type, rows pre_stride apart,
- *          for moe_swiglu_backward; written for computed rows only, and set to zero
+ *          products z before SwiGLU, float [M][2N], rows pre_stride apart, for
+ *          moe_swiglu_backward (rounded to 16 bits they would double the error of the
+ *          gradients); written for computed rows only, and set to zero
  *          or left for others as out is where their group's rows are.  Neither may
  *          overlap an input or the other.  Everything may start at any element.
  * Errors : MOE_EINVAL for null or misaligned pointers (the element's size; 4 bytes for
@@ -795,7 +796,7 @@ typedef struct moe_grouped_matmul_args {
   size_t b_group_stride;
   void* out;
   size_t out_stride;
-  void* pre;
+  float* pre;
   size_t pre_stride;
 } moe_grouped_matmul_args;
 
@@ -838,11 +839,11 @@ int moe_grouped_outer(const moe_grouped_outer_args* args, hipStream_t stream);
  * moe_swiglu_backward -- the gradient of h = silu(g) * u for rows of pre = [g | u]:
  *   dpre[m][n] = dout[m][n] * u * (s + g * s * (1 - s)),  dpre[m][N+n] = dout[m][n] * g * s
  * with s = 1 / (1 + exp(-g)) (0 below g = -174), in float32 and rounded once.
- * pre and dpre [M][2N], dout [M][N] of one element type, rows their strides apart, at any
- * element; dpre may be pre.  Errors : MOE_EINVAL, MOE_EUNSUPPORTED as above.  M = 0 is
+ * pre float [M][2N]; dpre [M][2N] and dout [M][N] of the type `dtype`; rows their strides
+ * apart, at any element.  Errors : MOE_EINVAL, MOE_EUNSUPPORTED as above.  M = 0 is
  * valid and does nothing.
  */
-int moe_swiglu_backward(int M, int N, int dtype, const void* pre, size_t pre_stride,
+int moe_swiglu_backward(int M, int N, int dtype, const float* pre, size_t pre_stride,
                         const void* dout, size_t dout_stride, void* dpre, size_t dpre_stride,
                         hipStream_t stream);
 
@@ -888,10 +889,10 @@ int moe_int4_quantize(const void* w, int N, int K, size_t w_stride, int dtype, i
  *   out[p][n] = y[p][n], or with swiglu (2N rows of weights, N gate rows and then N up
  *               rows): silu(y[p][n]) * y[p][N+n], as in moe_int8_matmul
  * with float32 sums of exact products, within each group of weights first, then with its
- * scale over the groups, and one rounding to out_dtype.  (fp32 activations are three bf16
- * parts whose sum they are exactly.)  A group's sum is taken of a * (16 + code) and
- * corrected, so its error is that of a float32 sum of magnitudes up to 31 |a|; values of a
- * above 2^110 may overflow.
+ * scale over the groups, and one rounding to out_dtype.  For 16-bit activations a group's
+ * sum is taken of a * (16 + code) and corrected, so its error is that of a float32 sum of
+ * magnitudes up to 31 |a|; values of a above 2^110 may overflow.  fp32 activations are three
+ * bf16 parts whose sum they are exactly, against code - zero.
  *   G, offsets, index, index_div, and which rows of out are left as they were: as in
  *   moe_int8_matmul.  Made for few rows of each group: weights are read and widened again for
  *   every 64 rows of a group.

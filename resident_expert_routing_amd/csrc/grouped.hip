@@ -23,10 +23,9 @@ constexpr int kMaxRows = 1 << 30;
 //   dg = d * u * (s + v * (1 - s)),  du = d * v,  s = 1 / (1 + exp(-g)), v = g * s
 // s from exp(-|g|), which cannot overflow.  Below kLow, where 1 - s is 1 in float32, exp(g)
 // is applied as two factors exp(g / 2), so that a gradient that is still a normal number
-// keeps its value to g = -174.  Bound by memory: five rows of N are read or written (32768
-// rows of 2048 bf16, 671 MB: 118 us, 5.7 TB/s).
+// keeps its value to g = -174.  Bound by memory.
 template <typename E>
-__global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const E* pre,
+__global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const float* pre,
                                                             size_t pre_stride, const E* dout,
                                                             size_t dout_stride, E* dpre,
                                                             size_t dpre_stride, int chunks,
@@ -41,14 +40,21 @@ __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const 
   if (t >= per || c >= pieces || m >= M) return;
   const int n = c * kN, left = N - n;
   constexpr float kLow = -64.0f;
-  Piece<E> g, u, d, dg, du;
+  Piece<E> d, dg, du;
+  float g[kN], u[kN];
   float least = 0.0f;
-  g.load_upto(pre + m * pre_stride + n, left);
-  u.load_upto(pre + m * pre_stride + N + n, left);
+  const float* z = pre + m * pre_stride + n;
+#pragma unroll
+  for (int i = 0; i < kN; i += 4) {
+    Piece<float> a{}, b{};
+    if (left > i) a.load_upto(z + i, left - i), b.load_upto(z + N + i, left - i);
+    __builtin_memcpy(g + i, a.e, 16);
+    __builtin_memcpy(u + i, b.e, 16);
+  }
   d.load_upto(dout + m * dout_stride + n, left);
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
-    const float gf = to_f32<E>(g.e[i]), uf = to_f32<E>(u.e[i]), df = to_f32<E>(d.e[i]);
+    const float gf = g[i], uf = u[i], df = to_f32<E>(d.e[i]);
     least = fminf(least, gf);
     const float e = __expf(-fabsf(gf)), near = 1.0f / (1.0f + e), far = e * near;
     const float s = gf < 0.0f ? far : near, rest = gf < 0.0f ? near : far;
@@ -59,7 +65,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const 
   if (__builtin_expect(least < kLow, 0)) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const float gf = to_f32<E>(g.e[i]), uf = to_f32<E>(u.e[i]), df = to_f32<E>(d.e[i]);
+      const float gf = g[i], uf = u[i], df = to_f32<E>(d.e[i]);
       const float h = __expf(0.5f * gf);
       if (gf < kLow) {
         dg.e[i] = from_f32<E>((df * h) * (uf * (1.0f + gf) * h));
@@ -72,7 +78,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const 
 }
 
 template <typename E>
-void launch_swiglu_backward(int M, int N, const void* pre, size_t pre_stride, const void* dout,
+void launch_swiglu_backward(int M, int N, const float* pre, size_t pre_stride, const void* dout,
                             size_t dout_stride, void* dpre, size_t dpre_stride,
                             hipStream_t stream) {
   const int pieces = (N + Piece<E>::kN - 1) / Piece<E>::kN;
@@ -80,7 +86,7 @@ void launch_swiglu_backward(int M, int N, const void* pre, size_t pre_stride, co
   const int64_t blocks = ((int64_t)M + per - 1) / per * chunks;
   for (int64_t first = 0; first < blocks; first += kMaxGrid) {
     const unsigned grid = (unsigned)(blocks - first < kMaxGrid ? blocks - first : kMaxGrid);
-    swiglu_backward_rows<E><<<grid, 256, 0, stream>>>(M, N, (const E*)pre, pre_stride,
+    swiglu_backward_rows<E><<<grid, 256, 0, stream>>>(M, N, pre, pre_stride,
                                                       (const E*)dout, dout_stride, (E*)dpre,
                                                       dpre_stride, chunks, first);
   }
@@ -99,7 +105,7 @@ int matmul_status(const moe_grouped_matmul_args* a) {
   if (!a->a || !a->b || !a->out || !a->offsets || a->a_rows == 0) return MOE_EINVAL;
   if (a->index ? a->index_div < 1 : a->a_rows < a->M) return MOE_EINVAL;
   if (a->pre && !a->swiglu) return MOE_EINVAL;
-  if (!aligned(a->a, e) || !aligned(a->b, e) || !aligned(a->out, e) || !aligned(a->pre, e) ||
+  if (!aligned(a->a, e) || !aligned(a->b, e) || !aligned(a->out, e) || !aligned(a->pre, 4) ||
       !aligned(a->offsets, 4) || !aligned(a->index, 4))
     return MOE_EINVAL;
   const size_t wide = (size_t)a->N * (a->swiglu ? 2 : 1);
@@ -167,7 +173,7 @@ extern "C" MOE_EXPORT int moe_grouped_outer(const moe_grouped_outer_args* a, hip
   return launch_outer_product<float>(p, stream);
 }
 
-extern "C" MOE_EXPORT int moe_swiglu_backward(int M, int N, int dtype, const void* pre,
+extern "C" MOE_EXPORT int moe_swiglu_backward(int M, int N, int dtype, const float* pre,
                                               size_t pre_stride, const void* dout,
                                               size_t dout_stride, void* dpre, size_t dpre_stride,
                                               hipStream_t stream) {
@@ -175,7 +181,7 @@ extern "C" MOE_EXPORT int moe_swiglu_backward(int M, int N, int dtype, const voi
   if (M < 0 || N <= 0 || e == 0) return MOE_EINVAL;
   if (M > kMaxRows || N > kMaxWide) return MOE_EUNSUPPORTED;
   if (M == 0) return MOE_OK;
-  if (!pre || !dout || !dpre || !aligned(pre, e) || !aligned(dout, e) || !aligned(dpre, e))
+  if (!pre || !dout || !dpre || !aligned(pre, 4) || !aligned(dout, e) || !aligned(dpre, e))
     return MOE_EINVAL;
   if (pre_stride < 2 * (size_t)N || dpre_stride < 2 * (size_t)N || dout_stride < (size_t)N)
     return MOE_EINVAL;

@@ -23,7 +23,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 struct RowsProduct {
   int M, N, K, G, a_rows, index_div;  // N: columns of out; with SwiGLU b has 2N
   const void *a, *b;
-  void *out, *pre;  // pre: the products before SwiGLU, [M][2N], or null
+  void* out;
+  float* pre;  // the products before SwiGLU, [M][2N], or null
   const int32_t *index, *offsets;
   size_t a_stride, b_stride, b_group_stride, out_stride, pre_stride;  // elements
   bool zero_rest;  // rows that nothing is computed for become zero
@@ -77,6 +78,8 @@ struct Wide {
   static constexpr int kCols = 64 * WA, kWaves = 2 * WA, kThreads = kWaves * kWave;
 };
 constexpr int kSmall = 1, kLarge = 4;  // WA of products of few tiles, and of the others
+template <typename E>
+constexpr int kOuter = sizeof(E) == 4 ? 2 : 4;  // of outer products: tiles of 64 kOuter squared
 
 // Where an operand that lies across its contraction is in LDS: a stage is kStep /
 // sizeof(E) rows of W elements, 16-byte pieces of a row swapped so that the places
@@ -189,6 +192,16 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FB before, FL
       dma16(from, place(i, j));
   };
 
+  // float32 products are summed stage by stage: a chain of K / 32 and eight additions in
+  // place of K / 4 (K 2900: relative error 1.2e-6 of an output against 5e-7)
+  constexpr bool kApart = sizeof(E) == 4;
+  f32x4 total[kApart ? MF : 1][4];
+  if constexpr (kApart) {
+#pragma unroll
+    for (int f = 0; f < MF; ++f)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) total[f][s] = acc[f][s], acc[f][s] = f32x4{};
+  }
   auto stage = [&](int i, auto more) {
     const uint8_t* at = smem + (i % S) * kStage;
     const int slot[2] = {16 * (quad ^ (col & 7)), 16 * ((4 + quad) ^ (col & 7))};
@@ -225,6 +238,12 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FB before, FL
 #pragma unroll
       for (int s = 0; s < 4; ++s) acc[x % MF][s] = mma<E>(v[x / MF][s], w[x % 3], acc[x % MF][s]);
       __builtin_amdgcn_s_setprio(0);
+    }
+    if constexpr (kApart) {
+#pragma unroll
+      for (int f = 0; f < MF; ++f)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) total[f][s] += acc[f][s], acc[f][s] = f32x4{};
     }
   };
 
@@ -273,6 +292,12 @@ __device__ __forceinline__ void products(uint8_t* smem, int steps, FB before, FL
       stage(i, std::false_type{});
       if (i + 1 < steps) put(i + 1);
     }
+  }
+  if constexpr (kApart) {
+#pragma unroll
+    for (int f = 0; f < MF; ++f)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) acc[f][s] = total[f][s];
   }
 }
 
@@ -391,9 +416,10 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
   barrier();  // every wave has read the last stage
   constexpr int kBytes = WA == kLarge ? 16384 : 8192;  // LDS that a wave's results pass through
   uint8_t* mine = smem + wave * kBytes;
-  auto to = [&](void* out, size_t stride, int at, int N, int row, int c) {
-    const int t = wm * MF * 16 + row, n = at + c * kPiece;
-    return Dst<E>{(E*)out + (size_t)(r.lo + t) * stride + n, live.row[t] ? N - n : 0,
+  auto to = [&](auto* out, size_t stride, int at, int row, int c) {
+    using O = std::remove_pointer_t<decltype(out)>;
+    const int t = wm * MF * 16 + row, n = at + c * (16 / (int)sizeof(O));
+    return Dst<O>{out + (size_t)(r.lo + t) * stride + n, live.row[t] ? p.N - n : 0,
                   live.row[t] == 2};
   };
   if constexpr (GLU) {
@@ -401,11 +427,9 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
     if (p.pre) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        store_rows<E, MF, 2, JOIN, kBytes>(
+        store_rows<float, MF, 2, JOIN, kBytes>(
             mine, [&](int f, int s, int e) { return acc[f][2 * h + s][e]; },
-            [&](int row, int c) {
-              return to((E*)p.pre + (size_t)h * p.N, p.pre_stride, n, p.N, row, c);
-            });
+            [&](int row, int c) { return to(p.pre + (size_t)h * p.N, p.pre_stride, n, row, c); });
     }
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
@@ -418,11 +442,11 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
     }
     store_rows<E, MF, 2, JOIN, kBytes>(
         mine, [&](int f, int s, int e) { return acc[f][s][e]; },
-        [&](int row, int c) { return to(p.out, p.out_stride, n, p.N, row, c); });
+        [&](int row, int c) { return to((E*)p.out, p.out_stride, n, row, c); });
   } else {
     store_rows<E, MF, 4, JOIN, kBytes>(
         mine, [&](int f, int s, int e) { return acc[f][s][e]; },
-        [&](int row, int c) { return to(p.out, p.out_stride, n0 + wn * 64, p.N, row, c); });
+        [&](int row, int c) { return to((E*)p.out, p.out_stride, n0 + wn * 64, row, c); });
   }
 }
 
@@ -467,7 +491,12 @@ __global__ __launch_bounds__(Wide<kLarge>::kThreads, 2) void rows_tiles(RowsProd
   const int n0 = col * (Wide<WA>::kCols / (GLU ? 2 : 1));
   if (!tile_rows<E, WA, GLU>(p, R, item, n0, counts, r)) return;
   const int rows = r.hi - r.lo;
-  if constexpr (DMA) {
+  if constexpr (sizeof(E) == 4) {  // two sets of sums
+    if (rows <= 64)
+      rows_tile<E, ACROSS, GLU, WA, 2, 2, DMA, false>(p, r, n0, smem, live);
+    else
+      rows_tile<E, ACROSS, GLU, WA, 4, 2, DMA, false>(p, r, n0, smem, live);
+  } else if constexpr (DMA) {
     if (rows <= 64 && r.all)
       rows_tile<E, ACROSS, GLU, WA, 2, 3, true, true>(p, r, n0, smem, live);
     else if (rows <= 64)
@@ -602,11 +631,12 @@ __global__ __launch_bounds__(kSWaves* kWave) void rows_stream(RowsProduct p, int
 #pragma unroll
     for (int w = 1; w < kSWaves; ++w) sum[s] += part[w][s][lane];
   }
-  auto store = [&](void* out, size_t stride, int at, const float (&y)[4]) {
-    Piece<E, 4> o;
+  auto store = [&](auto* out, size_t stride, int at, const float (&y)[4]) {
+    using O = std::remove_pointer_t<decltype(out)>;
+    Piece<O, 4> o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.e[i] = from_f32<E>(live ? y[i] : 0.0f);
-    if (at < p.N) o.store_upto((E*)out + (size_t)m * stride + at, p.N - at);
+    for (int i = 0; i < 4; ++i) o.e[i] = from_f32<O>(live ? y[i] : 0.0f);
+    if (at < p.N) o.store_upto(out + (size_t)m * stride + at, p.N - at);
   };
   float y[2][4];
 #pragma unroll
@@ -616,22 +646,21 @@ __global__ __launch_bounds__(kSWaves* kWave) void rows_stream(RowsProduct p, int
   if constexpr (GLU) {
     if (p.pre) {
       store(p.pre, p.pre_stride, n, y[0]);
-      store((E*)p.pre + p.N, p.pre_stride, n, y[1]);
+      store(p.pre + p.N, p.pre_stride, n, y[1]);
     }
     float h[4];
     swiglu(y[0], y[1], h);
-    store(p.out, p.out_stride, n, h);
+    store((E*)p.out, p.out_stride, n, h);
   } else {
-    store(p.out, p.out_stride, n, y[0]);
-    store(p.out, p.out_stride, n + 16, y[1]);
+    store((E*)p.out, p.out_stride, n, y[0]);
+    store((E*)p.out, p.out_stride, n + 16, y[1]);
   }
 }
 
 // Most rows of a tile: more rows share a load of b's, but a product of few tiles may
 // then leave more of the 256 CUs without one; its time goes as rounds * (rows + 256).
-inline int rows_of_tile(int M, int G, int cols, bool dma) {
+inline int rows_of_tile(int M, int G, int cols, int most) {
   const int64_t groups = G < M ? G : M;
-  const int most = dma ? kMostRows : 256;
   if ((M / most + groups) * cols >= 256) return most;
   int best = most;
   int64_t least = INT64_MAX;
@@ -674,7 +703,7 @@ void launch_rows_tiles(const RowsProduct& p, bool dma, hipStream_t stream) {
     }
     return;
   }
-  const int R = rows_of_tile(p.M, p.G, cols, dma);
+  const int R = rows_of_tile(p.M, p.G, cols, sizeof(E) == 4 ? 128 : dma ? kMostRows : 256);
   const int64_t items = max_items(p.M, p.G, R) + (p.zero_rest ? 2 : 0);
   const bool blocks = p.M > 128 * (int64_t)p.G && items * cols >= 2048;
   const int64_t tiles =
@@ -803,8 +832,9 @@ void launch_outer_tiles(const OuterProduct& p, hipStream_t stream) {
   const bool dma = whole_pieces<E>(p.left, p.left_stride, 0, p.L) &&
                    whole_pieces<E>(p.right, p.right_stride, 0, p.R);
   auto tiles_of = [&](int n) { return (int64_t)p.G * ((p.L + n - 1) / n) * ((p.R + n - 1) / n); };
-  const bool few = tiles_of(256) < kFewTiles;
-  const int side = few ? 64 : 256, down = (p.L + side - 1) / side, across = (p.R + side - 1) / side;
+  constexpr int WA = kOuter<E>;
+  const bool few = tiles_of(64 * WA) < kFewTiles;
+  const int side = few ? 64 : 64 * WA, down = (p.L + side - 1) / side, across = (p.R + side - 1) / side;
   // Blocks of tiles for each XCD, whose L2 then serves each operand's columns several times,
   // pay where there are many tiles of many rows (64 groups of 512 rows, 4096 x 4096: 1424 us
   // against 1367), and cost where there are fewer (32 of 460, 2048 x 4096: 296 against 311) or
@@ -822,11 +852,11 @@ void launch_outer_tiles(const OuterProduct& p, hipStream_t stream) {
       outer_tiles<E, kSmall, 2, false, INDEXED>
           <<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, down, across, blocks, first);
     else if (dma)
-      outer_tiles<E, kLarge, 8, true, INDEXED>
-          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, blocks, first);
+      outer_tiles<E, WA, 2 * WA, true, INDEXED>
+          <<<grid, Wide<WA>::kThreads, 0, stream>>>(p, down, across, blocks, first);
     else
-      outer_tiles<E, kLarge, 8, false, INDEXED>
-          <<<grid, Wide<kLarge>::kThreads, 0, stream>>>(p, down, across, blocks, first);
+      outer_tiles<E, WA, 2 * WA, false, INDEXED>
+          <<<grid, Wide<WA>::kThreads, 0, stream>>>(p, down, across, blocks, first);
   }
 }
 

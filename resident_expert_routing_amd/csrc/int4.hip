@@ -8,7 +8,8 @@
 //   sum_i a[r,i] * (16 + c[i])  -  (16 + z) * sum_i a[r,i]
 // with the second sum from the same instruction against ones, and only finished group
 // sums meet the scales, all in float32.  16 is the smallest offset that lets all sixteen
-// codes share an exponent, so the subtraction costs about two bits of float32.
+// codes share an exponent, so the subtraction costs about two bits of float32; activations
+// of 32 bits, whose result would show that, take c - z itself, with more instructions.
 #include <type_traits>
 
 #include "groups.hpp"
@@ -155,6 +156,17 @@ __device__ __forceinline__ void store_out(const Int4Args& p, int m, int n, const
     store4<float>(p, m, n, y);
 }
 
+// Eight codes less their zero point: small integers, exact in bf16.
+__device__ __forceinline__ i32x4 centered(uint32_t w, float zero) {
+  i32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float lo = (float)(w >> (4 * j) & 15u) - zero, hi = (float)(w >> (16 + 4 * j) & 15u) - zero;
+    v[j] = (int)__builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+  }
+  return v;
+}
+
 // One word of each quad's lanes as the words of all four quads in every lane.
 __device__ __forceinline__ void spread(uint32_t w, uint32_t (&all)[4]) {
   const auto h = __builtin_amdgcn_permlane32_swap(w, w, false, false);
@@ -180,6 +192,7 @@ template <typename E, typename F, bool GLU, int QUADS>
 __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int n0,
                                           f32x4* part) {
   constexpr bool HALF = std::is_same_v<E, Fp16>;
+  constexpr bool kExact = sizeof(E) == 4;  // codes less their zero points, no correction
   constexpr int MT = F::MT, NT = F::NT, WK = F::WK;
   constexpr int kRing = 8 / NT, kCodesAhead = kRing - 1;
   constexpr int kActs = 128 / (MT * (int)sizeof(Acts<E>)) > 4 ? 4 : 128 / (MT * (int)sizeof(Acts<E>));
@@ -225,7 +238,8 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
   };
   // masks in place of branches, which would cut the loop's loads and products to pieces
   const uint32_t is_bf16 = p.scale_dtype == MOE_DT_BF16 ? ~0u : 0u;
-  const uint32_t given = zeros ? 0xFFu : 0u, offset = zeros ? 16u : 24u;
+  constexpr uint32_t kOffset = kExact ? 0 : 16;
+  const uint32_t given = zeros ? 0xFFu : 0u, offset = zeros ? kOffset : kOffset + 8;
   auto load_codes = [&](i32x4 (&w)[NT], int c) {
 #pragma unroll
     for (int s = 0; s < NT; ++s) w[s] = __builtin_nontemporal_load((const i32x4*)(codes[s] + (size_t)c * kTileBytes));
@@ -237,18 +251,20 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
   };
   f32x4 acc[MT][NT] = {}, dot[MT][NT], sum[MT];
   // products of quarter j of a tile; the first of a group of weights starts its sums
-  auto multiply = [&](const uint32_t (&word)[NT][4], int j, const Acts<E> (&x)[MT]) {
+  auto multiply = [&](const uint32_t (&word)[NT][4], const uint32_t (&side)[NT][4], int q, int j,
+                      const Acts<E> (&x)[MT]) {
     const bool fresh = j % (4 / QUADS) == 0;
     i32x4 wide[NT];
 #pragma unroll
-    for (int s = 0; s < NT; ++s) wide[s] = widen(word[s][j]);
+    for (int s = 0; s < NT; ++s)
+      wide[s] = kExact ? centered(word[s][j], (float)(side[s][q] >> 16)) : widen(word[s][j]);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       i32x4 v[Acts<E>::kParts];
       x[t].parts(v);
 #pragma unroll
       for (int u = 0; u < Acts<E>::kParts; ++u) {
-        sum[t] = mma<HALF>(v[u], ones, fresh && u == 0 ? f32x4{} : sum[t]);
+        if constexpr (!kExact) sum[t] = mma<HALF>(v[u], ones, fresh && u == 0 ? f32x4{} : sum[t]);
 #pragma unroll
         for (int s = 0; s < NT; ++s)
           dot[t][s] = mma<HALF>(v[u], wide[s], fresh && u == 0 ? f32x4{} : dot[t][s]);
@@ -266,7 +282,8 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          acc[t][s][i] = fmaf(sc, fmaf(-off, sum[t][i], dot[t][s][i]), acc[t][s][i]);
+          acc[t][s][i] = fmaf(sc, kExact ? dot[t][s][i] : fmaf(-off, sum[t][i], dot[t][s][i]),
+                              acc[t][s][i]);
     }
   };
   auto spread_side = [&](const Side& w, uint32_t (&side)[NT][4]) {
@@ -317,9 +334,9 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           load_acts(x[(4 * u + j + kActsAhead) % kActs], 4 * (c - lo) + j + kActsAhead);
-          multiply(word, j, x[(4 * u + j) % kActs]);
-          if ((j + 1) % (4 / QUADS) == 0)
-            finish(side, (u % kRun) * QUADS + j / (4 / QUADS));
+          const int q = (u % kRun) * QUADS + j / (4 / QUADS);
+          multiply(word, side, q, j, x[(4 * u + j) % kActs]);
+          if ((j + 1) % (4 / QUADS) == 0) finish(side, q);
           __builtin_amdgcn_sched_barrier(0);  // keep to this order: registers
         }
       }
@@ -339,9 +356,9 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
       Acts<E> x[MT];
 #pragma unroll
       for (int t = 0; t < MT; ++t) x[t].load_head(arow[t] + k, p.K - k - 8 * quad);
-      multiply(word, j, x);
       // a group that begins behind the row has no scale: its weights are padding
       const int q = j / (4 / QUADS);
+      multiply(word, side, q, j, x);
       if ((j + 1) % (4 / QUADS) == 0 && full * kCodes + q * (kCodes / QUADS) < p.K)
         finish(side, q);
     }

@@ -8,7 +8,8 @@
 `GroupedExperts` does these for a layer.  Rows and matrices are of one type (bf16, fp16 or
 fp32; sums are float32), and gradients go to both (moe_grouped_matmul, moe_grouped_outer,
 moe_swiglu_backward).  A call that is recorded keeps copies of the offsets and of the
-order, which the next moe_route may write over; rows and matrices are kept as they are.
+order, which the next moe_route may write over, and with SwiGLU the products before it in
+float32; rows and matrices are kept as they are.
 There is no forward-mode derivative: tensors that carry a tangent are refused.  Calls run
 on the current stream of their tensors' device and synchronise nothing.  A gradient
 captured into a graph is taken with torch.autograd.grad, or with no graph made outside the
@@ -45,7 +46,7 @@ def _products(a, b, offsets, index, index_div, M, N, swiglu, out, zero, keep):
     b, across, down, group = b
     a, stride = row_major(a)
     K, G = a.shape[1], offsets.numel() - 1
-    pre = torch.empty((M, 2 * N), dtype=a.dtype, device=a.device) if keep else None
+    pre = torch.empty((M, 2 * N), dtype=torch.float32, device=a.device) if keep else None
     st = _lib.moe_grouped_matmul(B.GroupedMatmulArgs(
         M, N, K, G, dtype_of(a, "a"), swiglu, across, zero, a.shape[0], a.data_ptr(), stride,
         None if index is None else index.data_ptr(), index_div, offsets.data_ptr(), b.data_ptr(),
@@ -77,8 +78,8 @@ def _outer(left, left_index, left_div, right, right_index, right_div, offsets, M
 def _swiglu_backward(dout, pre):
     dout, stride = row_major(dout)
     M, N = dout.shape
-    dpre = torch.empty_like(pre)
-    st = _lib.moe_swiglu_backward(M, N, dtype_of(pre, "pre"), pre.data_ptr(), 2 * N,
+    dpre = torch.empty((M, 2 * N), dtype=dout.dtype, device=dout.device)
+    st = _lib.moe_swiglu_backward(M, N, dtype_of(dout, "the gradient"), pre.data_ptr(), 2 * N,
                                   dout.data_ptr(), stride, dpre.data_ptr(), 2 * N,
                                   stream_of(pre))
     if st != B.MOE_OK:

@@ -77,8 +77,7 @@ class Reference:
                 continue
             d = d_all[p]
             if swiglu:
-                # kept before SwiGLU in the element type, then the gradient rounded to it
-                eg, eu = eg + rounding(gt.abs() + eg, dtype), eu + rounding(up.abs() + eu, dtype)
+                # kept before SwiGLU in float32; the gradient through it is rounded to the type
                 dz = torch.cat([d * up * dsilu(gt), d * silu(gt)], 1)
                 f32 = 2.0 ** -24 * (24 + 2.5 * gt.abs())
                 e = torch.cat([

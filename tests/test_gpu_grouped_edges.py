@@ -205,7 +205,7 @@ def test_saturating_gates_backward(dtype):
     from resident_expert_routing_amd import grouped
     n = 181
     g = torch.arange(n, device="cuda").float() - 90
-    pre = torch.cat([g, torch.linspace(-3, 3, n, device="cuda")])[None].to(dtype)
+    pre = torch.cat([g, torch.linspace(-3, 3, n, device="cuda")])[None]
     d = torch.linspace(0.5, 2, n, device="cuda")[None].to(dtype)
     got = grouped._swiglu_backward(d, pre).double()
     gd, u, dd = pre[:, :n].double(), pre[:, n:].double(), d.double()

@@ -21,7 +21,7 @@ E, U = B.MOE_EINVAL, B.MOE_EUNSUPPORTED
     (dict(a_stride=99), E), (dict(b_stride=99), E), (dict(out_stride=63), E),
     (dict(b_across=1, b_stride=63), E), (dict(b_across=1, swiglu=1, b_stride=127), E),
     (dict(pre=FAKE, pre_stride=128), E), (dict(swiglu=1, pre=FAKE, pre_stride=127), E),
-    (dict(swiglu=1, pre=FAKE + 1, pre_stride=128), E),
+    (dict(swiglu=1, pre=FAKE + 2, pre_stride=128), E),
     (dict(N=(1 << 24) + 1, out_stride=1 << 25), U), (dict(K=(1 << 24) + 1, a_stride=1 << 25), U),
     (dict(M=(1 << 30) + 1, a_rows=(1 << 30) + 1), U), (dict(G=8193), U),
     (dict(M=WIDE), U), (dict(N=WIDE + 64), U), (dict(index_div=WIDE), U),
@@ -54,7 +54,7 @@ def test_grouped_outer_refusals(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(pre=None), E), (dict(dout=None), E), (dict(dpre=None), E), (dict(pre=FAKE + 1), E),
+    (dict(pre=None), E), (dict(dout=None), E), (dict(dpre=None), E), (dict(pre=FAKE + 2), E),
     (dict(M=-1), E), (dict(N=0), E), (dict(dtype=3), E), (dict(pre_stride=127), E),
     (dict(dout_stride=63), E), (dict(dpre_stride=100), E), (dict(N=(1 << 24) + 1), U),
     (dict(M=WIDE), U), (dict(M=0, pre=None, dout=None, dpre=None), B.MOE_OK),
