@@ -895,7 +895,7 @@ int moe_int4_quantize(const void* w, int N, int K, size_t w_stride, int dtype, i
  * bf16 parts whose sum they are exactly, against code - zero.
  *   G, offsets, index, index_div, and which rows of out are left as they were: as in
  *   moe_int8_matmul.  Made for few rows of each group: weights are read and widened again for
- *   every 64 rows of a group.
+ *   every 16 or 32 rows of a group.
  * Inputs : a [a_rows][K], rows a_stride elements apart, at any element; for each group an
  *          int4 matrix (its parts codes_group_stride bytes, scale_group_stride and
  *          zero_group_stride values apart).

@@ -438,22 +438,20 @@ void launch_form(const Int4Args& p, int group, hipStream_t stream) {
 // each, 93; two 87).  That needs enough groups: below kEnough workgroups the waves share K
 // (8 groups of one row: 24 us in the first form, 20 with four waves), all eight of them
 // where even then CUs would be left without a workgroup (one token, 8.4 MB: 6.1 us).  Groups
-// of more rows take tiles of 32 or 64 rows, for which weights are widened once.
+// of more rows take tiles of 32, for which weights are widened once (8192 rows over 166
+// groups: 790 us against 961; 2048 rows: 501 against 443); tiles of 64 do not fit the
+// registers (1005).
 template <typename E, bool GLU>
 void launch_matmul(const Int4Args& p, int group, hipStream_t stream) {
   using Few = Form<1, 2, 8, 1>;
   using Mid = Form<1, 2, 4, 1>;
   using Thin = Form<1, 4, 1, 2>;
   using Wide = Form<2, 4, 1, 4>;
-  using Tall = Form<4, 4, 1, 4>;
   constexpr int kEnough = 640, kCUs = 256;
   const int64_t groups = p.G > 0 ? (p.G < p.M ? p.G : p.M) : 1;
-  const bool thin = p.M <= 16 || p.M < 4 * groups;
+  const bool thin = p.M <= 16 || p.M < 24 * groups;
   if (!thin && groups * columns<Wide, GLU>(p) >= kCUs) {
-    if (sizeof(E) == 4 || p.M < 24 * groups)
-      launch_form<E, Wide, GLU>(p, group, stream);
-    else if constexpr (sizeof(E) == 2)
-      launch_form<E, Tall, GLU>(p, group, stream);
+    launch_form<E, Wide, GLU>(p, group, stream);
   } else if (max_items(p.M, p.G, 16) * columns<Mid, GLU>(p) <= kCUs) {
     launch_form<E, Few, GLU>(p, group, stream);
   } else if (max_items(p.M, p.G, 16) * columns<Thin, GLU>(p) < kEnough) {
