@@ -757,8 +757,8 @@ int moe_int8_matmul(const moe_int8_matmul_args* args, hipStream_t stream);
  *   z[p][n] = sum_i a[r][i] * b[g][n][i]   (b_across: b[g][i][n])
  *   out[p][n] = z[p][n], or with swiglu (2N outputs, N gates and then N ups):
  *               silu(z[p][n]) * z[p][N+n], silu(v) = v / (1 + exp(-v))
- * with float32 sums and one rounding to the element type.  fp32 products are float32
- * products.  silu is within (1.25 |v| + 8) * 2^-24 of its value down to v = -174,
+ * with float32 sums and one rounding to out_dtype, which is the element type or
+ * MOE_DT_FP32.  fp32 products are float32 products.  silu is within (1.25 |v| + 8) * 2^-24 of its value down to v = -174,
  * below which it is 0.
  *   r = p, or with index: index[p] / index_div (moe_route's perm and k name the token
  *   of a row).  Nothing is computed for rows whose r is outside [0, a_rows), nor for
@@ -798,6 +798,7 @@ typedef struct moe_grouped_matmul_args {
   size_t out_stride;
   float* pre;
   size_t pre_stride;
+  int out_dtype;
 } moe_grouped_matmul_args;
 
 int moe_grouped_matmul(const moe_grouped_matmul_args* args, hipStream_t stream);

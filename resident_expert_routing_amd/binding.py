@@ -120,7 +120,8 @@ class GroupedMatmulArgs(ctypes.Structure):
                 ("offsets", ctypes.c_void_p), ("b", ctypes.c_void_p),
                 ("b_stride", ctypes.c_size_t), ("b_group_stride", ctypes.c_size_t),
                 ("out", ctypes.c_void_p), ("out_stride", ctypes.c_size_t),
-                ("pre", ctypes.c_void_p), ("pre_stride", ctypes.c_size_t)]
+                ("pre", ctypes.c_void_p), ("pre_stride", ctypes.c_size_t),
+                ("out_dtype", ctypes.c_int)]
 
 
 class GroupedOuterArgs(ctypes.Structure):
@@ -515,14 +516,15 @@ def moe_int8_matmul(M, N, K, G, swiglu, a_rows, a, a_stride, a_scale, index, ind
 
 def moe_grouped_matmul(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, a, a_stride, index,
                        index_div, offsets, b, b_stride, b_group_stride, out, out_stride, pre=None,
-                       pre_stride=0, stream=None) -> int:
-    if not fits(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, index_div):
+                       pre_stride=0, out_dtype=None, stream=None) -> int:
+    out_dtype = dtype if out_dtype is None else out_dtype
+    if not fits(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, index_div, out_dtype):
         return MOE_EUNSUPPORTED
     args = GroupedMatmulArgs(int(M), int(N), int(K), int(G), int(dtype), int(swiglu),
                              int(b_across), int(zero_rest), int(a_rows), _ptr(a), int(a_stride),
                              _ptr(index), int(index_div), _ptr(offsets), _ptr(b), int(b_stride),
                              int(b_group_stride), _ptr(out), int(out_stride), _ptr(pre),
-                             int(pre_stride))
+                             int(pre_stride), int(out_dtype))
     return int(load().moe_grouped_matmul(ctypes.byref(args), _stream(stream)))
 
 

@@ -94,9 +94,10 @@ void launch_swiglu_backward(int M, int N, const float* pre, size_t pre_stride, c
 
 int matmul_status(const moe_grouped_matmul_args* a) {
   if (!a) return MOE_EINVAL;
-  const size_t e = dtype_bytes(a->dtype);
+  const size_t e = dtype_bytes(a->dtype), o = dtype_bytes(a->out_dtype);
   if (a->M < 0 || a->N <= 0 || a->K <= 0 || a->G <= 0 || a->a_rows < 0 || e == 0)
     return MOE_EINVAL;
+  if (a->out_dtype != a->dtype && a->out_dtype != MOE_DT_FP32) return MOE_EINVAL;
   for (int flag : {a->swiglu, a->b_across, a->zero_rest})
     if (flag != 0 && flag != 1) return MOE_EINVAL;
   if (a->N > kMaxWide || a->K > kMaxWide || a->M > kMaxRows || a->G > MOE_MAX_S)
@@ -105,7 +106,7 @@ int matmul_status(const moe_grouped_matmul_args* a) {
   if (!a->a || !a->b || !a->out || !a->offsets || a->a_rows == 0) return MOE_EINVAL;
   if (a->index ? a->index_div < 1 : a->a_rows < a->M) return MOE_EINVAL;
   if (a->pre && !a->swiglu) return MOE_EINVAL;
-  if (!aligned(a->a, e) || !aligned(a->b, e) || !aligned(a->out, e) || !aligned(a->pre, 4) ||
+  if (!aligned(a->a, e) || !aligned(a->b, e) || !aligned(a->out, o) || !aligned(a->pre, 4) ||
       !aligned(a->offsets, 4) || !aligned(a->index, 4))
     return MOE_EINVAL;
   const size_t wide = (size_t)a->N * (a->swiglu ? 2 : 1);
@@ -152,6 +153,7 @@ extern "C" MOE_EXPORT int moe_grouped_matmul(const moe_grouped_matmul_args* a,
   p.a_stride = a->a_stride, p.b_stride = a->b_stride, p.b_group_stride = a->b_group_stride;
   p.out_stride = a->out_stride, p.pre_stride = a->pre_stride;
   p.zero_rest = a->zero_rest;
+  p.out_f32 = a->out_dtype == MOE_DT_FP32;
   if (a->dtype == MOE_DT_BF16) return launch_rows_product<Bf16>(p, a->b_across, a->swiglu, stream);
   if (a->dtype == MOE_DT_FP16) return launch_rows_product<Fp16>(p, a->b_across, a->swiglu, stream);
   return launch_rows_product<float>(p, a->b_across, a->swiglu, stream);

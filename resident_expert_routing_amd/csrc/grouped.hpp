@@ -28,6 +28,7 @@ struct RowsProduct {
   const int32_t *index, *offsets;
   size_t a_stride, b_stride, b_group_stride, out_stride, pre_stride;  // elements
   bool zero_rest;  // rows that nothing is computed for become zero
+  bool out_f32;    // out is float32 whatever the element type
 };
 
 struct OuterProduct {
@@ -440,19 +441,27 @@ __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, i
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[f][j / 4][j % 4] = y[j];
     }
-    store_rows<E, MF, 2, JOIN, kBytes>(
-        mine, [&](int f, int s, int e) { return acc[f][s][e]; },
-        [&](int row, int c) { return to((E*)p.out, p.out_stride, n, row, c); });
-  } else {
-    store_rows<E, MF, 4, JOIN, kBytes>(
-        mine, [&](int f, int s, int e) { return acc[f][s][e]; },
-        [&](int row, int c) { return to((E*)p.out, p.out_stride, n0 + wn * 64, row, c); });
   }
+  auto leave = [&](auto* out) {
+    store_rows<std::remove_pointer_t<decltype(out)>, MF, GLU ? 2 : 4, JOIN, kBytes>(
+        mine, [&](int f, int s, int e) { return acc[f][s][e]; },
+        [&](int row, int c) {
+          return to(out, p.out_stride, n0 + wn * (GLU ? 32 : 64), row, c);
+        });
+  };
+  if (p.out_f32)
+    leave((float*)p.out);
+  else
+    leave((E*)p.out);
 }
 
 // Rows that nothing is computed for.
 template <typename E>
-__device__ __forceinline__ void zero_rows(void* out, size_t stride, const Rows& r, int n0, int n1) {
+__device__ __forceinline__ void zero_rows(const RowsProduct& p, const Rows& r, int n0, int n1) {
+  if constexpr (sizeof(E) != 4)
+    if (p.out_f32) return zero_rows<float>(p, r, n0, n1);
+  void* out = p.out;
+  const size_t stride = p.out_stride;
   constexpr int kPiece = 16 / (int)sizeof(E);
   const int pieces = (n1 - n0 + kPiece - 1) / kPiece;
   for (int t = threadIdx.x; t < (r.hi - r.lo) * pieces; t += blockDim.x) {
@@ -470,7 +479,7 @@ __device__ __forceinline__ bool tile_rows(const RowsProduct& p, int R, int64_t i
   if (find_rows(p, item, R, counts, r, total)) return true;
   constexpr int kWide = Wide<WA>::kCols / (GLU ? 2 : 1);
   if (p.zero_rest && rest_rows(p, item - total, R, r))
-    zero_rows<E>(p.out, p.out_stride, r, n0, min(n0 + kWide, p.N));
+    zero_rows<E>(p, r, n0, min(n0 + kWide, p.N));
   return false;
 }
 
@@ -554,7 +563,7 @@ __global__ __launch_bounds__(kSWaves* kWave) void rows_stream(RowsProduct p, int
   int64_t total = 0;
   if (!find_rows(p, id / cols, 16, counts, r, total)) {
     if (p.zero_rest && rest_rows(p, id / cols - total, 16, r))
-      zero_rows<E>(p.out, p.out_stride, r, n0, min(n0 + (GLU ? 16 : 32), p.N));
+      zero_rows<E>(p, r, n0, min(n0 + (GLU ? 16 : 32), p.N));
     return;
   }
   const int lane = threadIdx.x & 63;
@@ -650,10 +659,18 @@ __global__ __launch_bounds__(kSWaves* kWave) void rows_stream(RowsProduct p, int
     }
     float h[4];
     swiglu(y[0], y[1], h);
-    store((E*)p.out, p.out_stride, n, h);
+    if (p.out_f32)
+      store((float*)p.out, p.out_stride, n, h);
+    else
+      store((E*)p.out, p.out_stride, n, h);
   } else {
-    store((E*)p.out, p.out_stride, n, y[0]);
-    store((E*)p.out, p.out_stride, n + 16, y[1]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (p.out_f32)
+        store((float*)p.out, p.out_stride, n + 16 * s, y[s]);
+      else
+        store((E*)p.out, p.out_stride, n + 16 * s, y[s]);
+    }
   }
 }
 

@@ -51,7 +51,7 @@ def _products(a, b, offsets, index, index_div, M, N, swiglu, out, zero, keep):
         M, N, K, G, dtype_of(a, "a"), swiglu, across, zero, a.shape[0], a.data_ptr(), stride,
         None if index is None else index.data_ptr(), index_div, offsets.data_ptr(), b.data_ptr(),
         down, group, out.data_ptr(), out.stride(0) if M > 1 else N,
-        None if pre is None else pre.data_ptr(), 2 * N), stream_of(a))
+        None if pre is None else pre.data_ptr(), 2 * N, dtype_of(out, "out")), stream_of(a))
     if st != B.MOE_OK:
         raise B.MoeError(st, "moe_grouped_matmul")
     return pre
@@ -115,11 +115,13 @@ class _Matmul(torch.autograd.Function):
         da = db = None
         if ctx.needs_input_grad[0]:
             K = b.shape[2]
-            da = torch.empty((M, K), dtype=a.dtype, device=a.device)
+            # a token's rows are summed before they are rounded
+            rows = torch.float32 if order is not None else a.dtype
+            da = torch.empty((M, K), dtype=rows, device=a.device)
             _products(dz, (b, not across, down, group), offsets, None, 1, M, K, False, da, True,
                       False)
             if order is not None:
-                da = _gather(da, order, None)[0]
+                da = _gather(da, order, None)[0].to(a.dtype)
         if ctx.needs_input_grad[1]:
             if across:
                 db = _outer(a, index, div, dz, None, 1, offsets, M).transpose(1, 2)

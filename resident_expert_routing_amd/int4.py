@@ -78,8 +78,13 @@ class Int4Weight:
                                  f"{unit * t.element_size()} bytes")
         self.codes, self.scale, self.zero = codes, scale, zero
         far = lambda t: 0 if t is None or not self.G else t.stride(0) if self.G > 1 else t.numel()
-        self._args = (self.group, codes.data_ptr(), far(codes), scale.data_ptr(), far(scale),
-                      SCALES[scale.dtype], None if zero is None else zero.data_ptr(), far(zero))
+        self._far = far(codes), far(scale), far(zero)
+
+    def _args(self):
+        """The matrices' part of moe_int4_matmul's arguments."""
+        codes, scale, zero = self.codes, self.scale, self.zero
+        return (self.group, codes.data_ptr(), self._far[0], scale.data_ptr(), self._far[1],
+                SCALES[scale.dtype], None if zero is None else zero.data_ptr(), self._far[2])
 
     @property
     def device(self) -> torch.device:
@@ -244,7 +249,7 @@ def matmul(a: torch.Tensor, w: Int4Weight, *, offsets: torch.Tensor | None = Non
     _matmul(a, B.Int4MatmulArgs(
         M, N, w.K, G, 1 if swiglu else 0, rows, a.data_ptr(), stride, adt,
         None if index is None else index.data_ptr(), int(index_div),
-        None if offsets is None else offsets.data_ptr(), *w._args, out.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), *w._args(), out.data_ptr(),
         out.stride(0) if M > 1 else N, od))
     if given:
         _written(out)

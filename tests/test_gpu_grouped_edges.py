@@ -427,3 +427,21 @@ def test_layer(T, H, E, k, I, S, resident):
         with pytest.raises(ValueError):
             R.layer_step_grouped(buf, wrong, args[0], None, args[1], hist, ex)
         assert torch.equal(hist, before)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("counts,N,K", [([1, 0, 2], 40, 96), ([70, 20], 33, 65), ([300, 4, 90] * 20, 520, 64),
+                                        ([300, 4, 90] * 20, 517, 67)])
+def test_rows_left_in_float32(counts, N, K, dtype):
+    """An out of float32 holds what the rounded one is rounded from, in every form."""
+    from resident_expert_routing_amd import grouped
+    for across in (False, True):
+        a, b, offsets, _ = case(counts, N, K, dtype, swiglu=False)
+        if across:
+            b = b.transpose(1, 2).contiguous().transpose(1, 2)
+        M = a.shape[0]
+        wide = torch.full((M, N), 9.0, device="cuda")
+        grouped._products(a, grouped._matrices(b), offsets, None, 1, M, N, False, wide, True, False)
+        assert torch.equal(wide.to(dtype), grouped.matmul(a, b, offsets))
+        ref = Reference(a, b, offsets, None, M, False, FP32)
+        assert within(wide, ref.out, ref.out_tol)

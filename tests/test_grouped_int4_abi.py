@@ -22,6 +22,7 @@ E, U = B.MOE_EINVAL, B.MOE_EUNSUPPORTED
     (dict(b_across=1, b_stride=63), E), (dict(b_across=1, swiglu=1, b_stride=127), E),
     (dict(pre=FAKE, pre_stride=128), E), (dict(swiglu=1, pre=FAKE, pre_stride=127), E),
     (dict(swiglu=1, pre=FAKE + 2, pre_stride=128), E),
+    (dict(out_dtype=1), E), (dict(out_dtype=3), E), (dict(out_dtype=2, out=FAKE + 2), E),
     (dict(N=(1 << 24) + 1, out_stride=1 << 25), U), (dict(K=(1 << 24) + 1, a_stride=1 << 25), U),
     (dict(M=(1 << 30) + 1, a_rows=(1 << 30) + 1), U), (dict(G=8193), U),
     (dict(M=WIDE), U), (dict(N=WIDE + 64), U), (dict(index_div=WIDE), U),
