@@ -814,8 +814,10 @@ int moe_grouped_matmul(const moe_grouped_matmul_args* args, hipStream_t stream);
  *          offsets [G+1] int32, cut to [0, M].
  * Output : out [G][L][R], rows out_stride elements apart, groups out_group_stride; must
  *          not overlap an input.
- * Errors : as moe_grouped_matmul.  M = 0 is valid and writes zeros (left and right may
- *          then be NULL).
+ * Workspace: moe_grouped_outer_ws_bytes(M, L, R, G, dtype) bytes, 16-byte aligned (0 for most
+ *          shapes: only few small matrices over many rows need one; at most 8 MB).
+ * Errors : as moe_grouped_matmul, and MOE_EWORKSPACE.  M = 0 is valid and writes zeros (left
+ *          and right may then be NULL).
  */
 typedef struct moe_grouped_outer_args {
   int M, L, R, G, dtype;
@@ -832,7 +834,11 @@ typedef struct moe_grouped_outer_args {
   void* out;
   size_t out_stride;
   size_t out_group_stride;
+  void* ws;
+  size_t ws_bytes;
 } moe_grouped_outer_args;
+
+size_t moe_grouped_outer_ws_bytes(int M, int L, int R, int G, int dtype);
 
 int moe_grouped_outer(const moe_grouped_outer_args* args, hipStream_t stream);
 

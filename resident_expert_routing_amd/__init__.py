@@ -13,7 +13,7 @@ from . import binding
 from .binding import (MOE_DT_BF16, MOE_DT_FP16, MOE_DT_FP32, MOE_OP_DEMAND, MOE_OP_EXPERTS, MOE_OP_HOT_PICK, MOE_OP_ROUTE, MoeError,
                       arena_load_slot, check, moe_combine, moe_combine_backward,
                       moe_demand_accumulate, moe_dispatch, moe_dispatch_backward,
-                      moe_experts_forward, moe_grouped_matmul, moe_grouped_outer,
+                      moe_experts_forward, moe_grouped_matmul, moe_grouped_outer, moe_grouped_outer_ws_bytes,
                       moe_hot_install, moe_hot_pick, moe_int4_code_bytes, moe_int4_matmul,
                       moe_int4_quantize, moe_int4_scale_count, moe_mxfp4_row_bytes, moe_int8_matmul,
                       moe_int8_quantize, moe_int8_row_bytes, moe_positions, moe_replan, moe_route,
@@ -27,7 +27,8 @@ __all__ = ["binding", "MOE_DT_BF16", "MOE_DT_FP16", "MOE_DT_FP32", "MOE_OP_DEMAN
            "MoeError", "arena_load_slot", "check", "moe_combine",
            "moe_combine_backward", "moe_demand_accumulate", "moe_dispatch",
            "moe_dispatch_backward", "moe_int8_matmul", "moe_int8_quantize", "moe_int8_row_bytes",
-           "moe_positions", "moe_grouped_matmul", "moe_grouped_outer", "moe_swiglu_backward",
+           "moe_positions", "moe_grouped_matmul", "moe_grouped_outer", "moe_grouped_outer_ws_bytes",
+           "moe_swiglu_backward",
            "moe_int4_code_bytes", "moe_int4_scale_count", "moe_int4_quantize", "moe_int4_matmul",
            "moe_experts_forward", "moe_hot_install", "moe_hot_pick", "moe_mxfp4_row_bytes", "moe_replan", "moe_route", "moe_slot_bytes",
            "moe_slot_sections", "moe_status_string", "moe_test_mfma_loop", "moe_test_mxfp4_probe",

@@ -51,7 +51,8 @@ EXPORTS = ("moe_status_string", "moe_mxfp4_row_bytes", "moe_act_row_bytes", "moe
            "moe_history_save", "moe_history_load", "moe_boot_plan", "moe_history_scale",
            "moe_positions", "moe_dispatch", "moe_dispatch_backward", "moe_combine",
            "moe_combine_backward", "moe_int8_row_bytes", "moe_int8_quantize", "moe_int8_matmul",
-           "moe_grouped_matmul", "moe_grouped_outer", "moe_swiglu_backward",
+           "moe_grouped_matmul", "moe_grouped_outer", "moe_grouped_outer_ws_bytes",
+           "moe_swiglu_backward",
            "moe_int4_code_bytes", "moe_int4_scale_count", "moe_int4_quantize", "moe_int4_matmul",
            "arena_load_slot", "moe_hot_pick", "moe_hot_install", "moe_replan", "moe_test_mxfp4_probe",
            "moe_test_stream_read", "moe_test_mfma_loop")
@@ -133,7 +134,8 @@ class GroupedOuterArgs(ctypes.Structure):
                 ("right_stride", ctypes.c_size_t), ("right_index", ctypes.c_void_p),
                 ("right_div", ctypes.c_int), ("offsets", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("out_stride", ctypes.c_size_t),
-                ("out_group_stride", ctypes.c_size_t)]
+                ("out_group_stride", ctypes.c_size_t), ("ws", ctypes.c_void_p),
+                ("ws_bytes", ctypes.c_size_t)]
 
 
 class Int4MatmulArgs(ctypes.Structure):
@@ -232,6 +234,8 @@ def load() -> ctypes.CDLL:
     lib.moe_grouped_matmul.restype = i
     lib.moe_grouped_outer.argtypes = [ctypes.POINTER(GroupedOuterArgs), vp]
     lib.moe_grouped_outer.restype = i
+    lib.moe_grouped_outer_ws_bytes.argtypes = [i, i, i, i, i]
+    lib.moe_grouped_outer_ws_bytes.restype = sz
     lib.moe_swiglu_backward.argtypes = [i, i, i, vp, sz, vp, sz, vp, sz, vp]
     lib.moe_swiglu_backward.restype = i
     lib.moe_test_mxfp4_probe.argtypes = [i, vp, vp, vp, vp, vp, vp]
@@ -530,15 +534,21 @@ def moe_grouped_matmul(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, a
 
 def moe_grouped_outer(M, L, R, G, dtype, left_rows, right_rows, left, left_stride, left_index,
                       left_div, right, right_stride, right_index, right_div, offsets, out,
-                      out_stride, out_group_stride, stream=None) -> int:
+                      out_stride, out_group_stride, ws=None, ws_bytes=0, stream=None) -> int:
     if not fits(M, L, R, G, dtype, left_rows, right_rows, left_div, right_div):
         return MOE_EUNSUPPORTED
     args = GroupedOuterArgs(int(M), int(L), int(R), int(G), int(dtype), int(left_rows),
                             int(right_rows), _ptr(left), int(left_stride), _ptr(left_index),
                             int(left_div), _ptr(right), int(right_stride), _ptr(right_index),
                             int(right_div), _ptr(offsets), _ptr(out), int(out_stride),
-                            int(out_group_stride))
+                            int(out_group_stride), _ptr(ws), int(ws_bytes))
     return int(load().moe_grouped_outer(ctypes.byref(args), _stream(stream)))
+
+
+def moe_grouped_outer_ws_bytes(M: int, L: int, R: int, G: int, dtype: int) -> int:
+    if not fits(M, L, R, G, dtype):
+        return 0
+    return int(load().moe_grouped_outer_ws_bytes(int(M), int(L), int(R), int(G), int(dtype)))
 
 
 def moe_swiglu_backward(M, N, dtype, pre, pre_stride, dout, dout_stride, dpre, dpre_stride,

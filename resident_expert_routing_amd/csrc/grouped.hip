@@ -128,6 +128,9 @@ int outer_status(const moe_grouped_outer_args* a) {
   if (a->out_stride < (size_t)a->R ||
       (a->G > 1 && a->out_group_stride < (size_t)(a->L - 1) * a->out_stride + (size_t)a->R))
     return MOE_EINVAL;
+  const size_t need = moe_grouped_outer_ws_bytes(a->M, a->L, a->R, a->G, a->dtype);
+  if (a->ws_bytes < need) return MOE_EWORKSPACE;
+  if (need && (!a->ws || !aligned(a->ws, 16))) return MOE_EINVAL;
   if (a->M == 0) return MOE_OK;  // every group is empty: zeros
   if (!a->left || !a->right || !aligned(a->left, e) || !aligned(a->right, e) ||
       !aligned(a->left_index, 4) || !aligned(a->right_index, 4))
@@ -159,6 +162,12 @@ extern "C" MOE_EXPORT int moe_grouped_matmul(const moe_grouped_matmul_args* a,
   return launch_rows_product<float>(p, a->b_across, a->swiglu, stream);
 }
 
+extern "C" MOE_EXPORT size_t moe_grouped_outer_ws_bytes(int M, int L, int R, int G, int dtype) {
+  if (M <= 0 || L <= 0 || R <= 0 || G <= 0 || dtype_bytes(dtype) == 0) return 0;
+  const int splits = outer_splits(M, L, R, G, dtype);
+  return splits > 1 ? (size_t)splits * (size_t)G * (size_t)L * (size_t)R * 4 : 0;
+}
+
 extern "C" MOE_EXPORT int moe_grouped_outer(const moe_grouped_outer_args* a, hipStream_t stream) {
   const int s = outer_status(a);
   if (s != MOE_OK) return s;
@@ -170,6 +179,8 @@ extern "C" MOE_EXPORT int moe_grouped_outer(const moe_grouped_outer_args* a, hip
   p.left_div = a->left_div, p.right_div = a->right_div;
   p.left_stride = a->left_stride, p.right_stride = a->right_stride;
   p.out_stride = a->out_stride, p.out_group_stride = a->out_group_stride;
+  p.splits = a->M > 0 ? outer_splits(a->M, a->L, a->R, a->G, a->dtype) : 1;
+  p.sums = p.splits > 1 ? (float*)a->ws : nullptr;
   if (a->dtype == MOE_DT_BF16) return launch_outer_product<Bf16>(p, stream);
   if (a->dtype == MOE_DT_FP16) return launch_outer_product<Fp16>(p, stream);
   return launch_outer_product<float>(p, stream);

@@ -37,6 +37,8 @@ struct OuterProduct {
   void* out;
   const int32_t *left_index, *right_index, *offsets;
   size_t left_stride, right_stride, out_stride, out_group_stride;  // elements
+  int splits;   // parts of each group's rows, with sums of their own
+  float* sums;  // [splits][G][L][R], or null for one part
 };
 
 template <typename E>
@@ -786,7 +788,12 @@ __global__ __launch_bounds__(Wide<WA>::kThreads, 2) void outer_tiles(OuterProduc
   const int64_t group = item / down;
   if (col >= across || group >= p.G) return;
   const int g = (int)group, l0 = (int)(item % down) * kRows, r0 = col * kCols;
-  const int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+  int lo = clamp_row(p.offsets[g], p.M), hi = clamp_row(p.offsets[g + 1], p.M);
+  if (p.sums && hi > lo) {
+    const int part = ((hi - lo + p.splits - 1) / p.splits + kC - 1) / kC * kC;
+    lo = (int)min((int64_t)hi, lo + (int64_t)blockIdx.y * part);
+    hi = min(hi, lo + part);
+  }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WA, wn = wave % WA;
 
@@ -834,22 +841,60 @@ __global__ __launch_bounds__(Wide<WA>::kThreads, 2) void outer_tiles(OuterProduc
                                                       from_right, acc);
   }
   barrier();
-  E* out = (E*)p.out + (size_t)g * p.out_group_stride;
   constexpr int kMine = kBytes / Wide<WA>::kWaves;
-  store_rows<E, MF, 4, false, kMine>(
-      smem + wave * kMine, [&](int f, int s, int e) { return acc[f][s][e]; },
-      [&](int row, int c) {
-        const int l = l0 + wm * MF * 16 + row, n = r0 + wn * 64 + c * kPiece;
-        return Dst<E>{out + (size_t)l * p.out_stride + n, l < p.L ? p.R - n : 0, false};
-      });
+  auto leave = [&](auto* to, size_t stride) {
+    using O = std::remove_pointer_t<decltype(to)>;
+    store_rows<O, MF, 4, false, kMine>(
+        smem + wave * kMine, [&](int f, int s, int e) { return acc[f][s][e]; },
+        [&](int row, int c) {
+          const int l = l0 + wm * MF * 16 + row;
+          const int n = r0 + wn * 64 + c * (16 / (int)sizeof(O));
+          return Dst<O>{to + (size_t)l * stride + n, l < p.L ? p.R - n : 0, false};
+        });
+  };
+  if constexpr (WA == kSmall)
+    if (p.sums)
+      return leave(p.sums + ((size_t)blockIdx.y * p.G + g) * ((size_t)p.L * p.R), (size_t)p.R);
+  leave((E*)p.out + (size_t)g * p.out_group_stride, p.out_stride);
 }
+
+// The parts' sums, in order, rounded once.
+template <typename E>
+__global__ __launch_bounds__(256) void outer_sum(OuterProduct p) {
+  const int64_t all = (int64_t)p.G * p.L * p.R;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    float v = p.sums[i];
+    for (int s = 1; s < p.splits; ++s) v += p.sums[s * all + i];
+    const int64_t row = i / p.R;
+    ((E*)p.out)[(size_t)(row / p.L) * p.out_group_stride + (size_t)(row % p.L) * p.out_stride +
+                (size_t)(i % p.R)] = from_f32<E>(v);
+  }
+}
+
+// Tiles of n x n, whether they are few, and into how many parts a group's rows are then cut:
+// enough for two workgroups a CU, of 512 rows at least, counted for groups of equal sizes (two
+// groups of 16384 rows, 256 x 192: 24 tiles).
+inline int64_t outer_tiles_of(int L, int R, int G, int n) {
+  return (int64_t)G * ((L + n - 1) / n) * ((R + n - 1) / n);
+}
+inline bool few_outer_tiles(int L, int R, int G, int dtype) {
+  return outer_tiles_of(L, R, G, 64 * (dtype == MOE_DT_FP32 ? kOuter<float> : kOuter<Bf16>)) <
+         kFewTiles;
+}
+inline int outer_splits(int M, int L, int R, int G, int dtype) {
+  if (!few_outer_tiles(L, R, G, dtype)) return 1;
+  const int64_t want = 512 / outer_tiles_of(L, R, G, 64), most = M / (512 * (int64_t)G);
+  const int64_t n = want < most ? want : most;
+  return n < 2 ? 1 : n > 64 ? 64 : (int)n;
+}
+
 
 template <typename E, int INDEXED>
 void launch_outer_tiles(const OuterProduct& p, hipStream_t stream) {
   const bool dma = whole_pieces<E>(p.left, p.left_stride, 0, p.L) &&
                    whole_pieces<E>(p.right, p.right_stride, 0, p.R);
-  auto tiles_of = [&](int n) { return (int64_t)p.G * ((p.L + n - 1) / n) * ((p.R + n - 1) / n); };
   constexpr int WA = kOuter<E>;
+  auto tiles_of = [&](int n) { return outer_tiles_of(p.L, p.R, p.G, n); };
   const bool few = tiles_of(64 * WA) < kFewTiles;
   const int side = few ? 64 : 64 * WA, down = (p.L + side - 1) / side, across = (p.R + side - 1) / side;
   // Blocks of tiles for each XCD, whose L2 then serves each operand's columns several times,
@@ -867,13 +912,17 @@ void launch_outer_tiles(const OuterProduct& p, hipStream_t stream) {
     const unsigned grid = (unsigned)(tiles - first < kMaxGrid ? tiles - first : kMaxGrid);
     if (few)
       outer_tiles<E, kSmall, 2, false, INDEXED>
-          <<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, down, across, blocks, first);
+          <<<dim3(grid, p.sums ? p.splits : 1), Wide<kSmall>::kThreads, 0, stream>>>(p, down, across, blocks, first);
     else if (dma)
       outer_tiles<E, WA, 2 * WA, true, INDEXED>
           <<<grid, Wide<WA>::kThreads, 0, stream>>>(p, down, across, blocks, first);
     else
       outer_tiles<E, WA, 2 * WA, false, INDEXED>
           <<<grid, Wide<WA>::kThreads, 0, stream>>>(p, down, across, blocks, first);
+  }
+  if (p.sums) {
+    const int64_t want = ((int64_t)p.G * p.L * p.R + 255) / 256;
+    outer_sum<E><<<(unsigned)(want < 4096 ? want : 4096), 256, 0, stream>>>(p);
   }
 }
 

@@ -65,10 +65,13 @@ def _outer(left, left_index, left_div, right, right_index, right_div, offsets, M
     L, R, G = left.shape[1], right.shape[1], offsets.numel() - 1
     out = torch.empty((G, L, R), dtype=left.dtype, device=left.device)
     at = lambda t: None if t is None else t.data_ptr()
+    dt = dtype_of(left, "left")
+    need = _lib.moe_grouped_outer_ws_bytes(M, L, R, G, dt)
+    ws = torch.empty(need, dtype=torch.uint8, device=left.device) if need else None
     st = _lib.moe_grouped_outer(B.GroupedOuterArgs(
-        M, L, R, G, dtype_of(left, "left"), left.shape[0], right.shape[0], left.data_ptr(), ls,
+        M, L, R, G, dt, left.shape[0], right.shape[0], left.data_ptr(), ls,
         at(left_index), left_div, right.data_ptr(), rs, at(right_index), right_div,
-        offsets.data_ptr(), out.data_ptr(), R, L * R), stream_of(left))
+        offsets.data_ptr(), out.data_ptr(), R, L * R, at(ws), need), stream_of(left))
     if st != B.MOE_OK:
         raise B.MoeError(st, "moe_grouped_outer")
     return out

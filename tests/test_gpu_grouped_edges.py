@@ -445,3 +445,24 @@ def test_rows_left_in_float32(counts, N, K, dtype):
         assert torch.equal(wide.to(dtype), grouped.matmul(a, b, offsets))
         ref = Reference(a, b, offsets, None, M, False, FP32)
         assert within(wide, ref.out, ref.out_tol)
+
+
+@pytest.mark.parametrize("dtype,N,K", [(BF16, 128, 192), (FP16, 70, 130), (FP32, 100, 64), (FP32, 33, 70)])
+@pytest.mark.parametrize("across", [False, True])
+def test_long_groups_of_small_matrices(dtype, N, K, across):
+    """The rows of a group are summed in parts, through a workspace."""
+    from resident_expert_routing_amd import binding as B
+    from resident_expert_routing_amd import grouped
+    counts = [5000, 0, 9001, 3]
+    a, b, offsets, d = case(counts, N, K, dtype, seed=2)
+    M = a.shape[0]
+    assert B.moe_grouped_outer_ws_bytes(M, N, K, 4, grouped.dtype_of(a, "a")) > 0
+    if across:
+        b = b.transpose(1, 2).contiguous().transpose(1, 2)
+    d[14004:] = float("nan")                              # rows of no group
+    a, b = a.requires_grad_(), b.detach().requires_grad_()
+    ref = Reference(a.detach(), b.detach(), offsets, None, M, False, dtype, d)
+    db, = torch.autograd.grad(grouped.matmul(a, b, offsets), b, d)
+    assert within(db, ref.db, ref.db_tol)
+    again, = torch.autograd.grad(grouped.matmul(a, b, offsets), b, d)
+    assert torch.equal(db, again)

@@ -46,6 +46,9 @@ def test_grouped_matmul_refusals(kw, code):
     (dict(L=(1 << 24) + 1), U), (dict(R=(1 << 24) + 1), U), (dict(G=8193), U),
     (dict(M=(1 << 30) + 1), U), (dict(L=WIDE), U), (dict(right_div=WIDE), U),
     (dict(M=0, out=None), E),  # zeros are still to be written
+    (dict(M=30000, left_rows=30000, right_rows=30000), B.MOE_EWORKSPACE),
+    (dict(M=30000, left_rows=30000, right_rows=30000, ws=None, ws_bytes=1 << 30), E),
+    (dict(M=30000, left_rows=30000, right_rows=30000, ws=FAKE + 8, ws_bytes=1 << 30), E),
 ])
 def test_grouped_outer_refusals(kw, code):
     a = dict(M=8, L=64, R=100, G=2, dtype=0, left_rows=8, right_rows=8, left=FAKE, left_stride=64,
@@ -102,6 +105,17 @@ def test_int4_quantize_refusals(kw, code):
     a = dict(w=FAKE, N=8, K=100, w_stride=100, dtype=0, group=128, codes=FAKE, scale=FAKE,
              scale_dtype=0)
     assert B.moe_int4_quantize(**(a | kw)) == code
+
+
+def test_outer_workspace():
+    """Only few small matrices over many rows need one, and it stays small."""
+    need = B.moe_grouped_outer_ws_bytes
+    assert need(30000, 64, 100, 2, 0) == 29 * 2 * 64 * 100 * 4
+    assert need(8, 64, 100, 2, 0) == 0 and need(1 << 20, 4096, 4096, 64, 0) == 0
+    assert need(0, 64, 100, 2, 0) == 0 and need(WIDE, 64, 100, 2, 0) == 0
+    for L, R, G in ((64, 64, 1), (700, 900, 3), (65, 4000, 2), (1, 1, 500), (512, 512, 7)):
+        for dt in range(3):
+            assert need(1 << 30, L, R, G, dt) <= 9 << 20
 
 
 def test_int4_sizes():
