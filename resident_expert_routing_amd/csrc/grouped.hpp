@@ -360,6 +360,8 @@ struct Live {
   uint8_t row[kMostRows];  // 1: computed, 2: set to zero, 0: left
 };
 
+// ONCE: these are all rows of their group, so b is read by this workgroup alone and passes
+// the caches by (16384 rows over 166 groups, down: 610 us against 601).
 template <typename E, bool ACROSS, bool GLU, int WA, int MF, int S, bool DMA, bool ONCE>
 __device__ __forceinline__ void rows_tile(const RowsProduct& p, const Rows& r, int n0,
                                           uint8_t* smem, Live& live) {
@@ -512,6 +514,8 @@ __global__ __launch_bounds__(Wide<kLarge>::kThreads, 2) void rows_tiles(RowsProd
       rows_tile<E, ACROSS, GLU, WA, 2, 3, true, true>(p, r, n0, smem, live);
     else if (rows <= 64)
       rows_tile<E, ACROSS, GLU, WA, 2, 3, true, false>(p, r, n0, smem, live);
+    else if (rows <= 128 && r.all)
+      rows_tile<E, ACROSS, GLU, WA, 4, 3, true, true>(p, r, n0, smem, live);
     else if (rows <= 128)
       rows_tile<E, ACROSS, GLU, WA, 4, 3, true, false>(p, r, n0, smem, live);
     else if (rows <= 192)
