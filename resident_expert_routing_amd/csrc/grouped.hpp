@@ -534,19 +534,21 @@ __global__ __launch_bounds__(Wide<kLarge>::kThreads, 2) void rows_tiles(RowsProd
   }
 }
 
-// Products of few tiles: 64 rows by 64 columns, two waves.
-template <typename E, bool ACROSS, bool GLU>
+// Products of few tiles: 64 rows by 64 columns, two waves; with direct loads three stages
+// ahead, since what each of the few workgroups has under way bounds them (4 rows over 8
+// groups, K 4096, N 1024, b across: 58 us through registers, one stage ahead, against 33).
+template <typename E, bool ACROSS, bool GLU, bool DMA>
 __global__ __launch_bounds__(Wide<kSmall>::kThreads, 2) void rows_small(RowsProduct p, int cols,
                                                                        int64_t first) {
-  constexpr int WA = kSmall;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (64 + Wide<WA>::kCols) * kStep];
+  constexpr int WA = kSmall, S = DMA ? 4 : 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * (64 + Wide<WA>::kCols) * kStep];
   __shared__ Live live;
   __shared__ int counts[Wide<WA>::kWaves];
   const int64_t id = first + blockIdx.x;
   const int n0 = (int)(id % cols) * (Wide<WA>::kCols / (GLU ? 2 : 1));
   Rows r;
   if (!tile_rows<E, WA, GLU>(p, 64, id / cols, n0, counts, r)) return;
-  rows_tile<E, ACROSS, GLU, WA, 2, 2, false, false>(p, r, n0, smem, live);
+  rows_tile<E, ACROSS, GLU, WA, 2, S, DMA, false>(p, r, n0, smem, live);
 }
 
 // Streaming form, for few rows in few groups, b along its rows: a workgroup takes 32 rows of b
@@ -722,7 +724,10 @@ void launch_rows_tiles(const RowsProduct& p, bool dma, hipStream_t stream) {
     const int64_t all = (max_items(p.M, p.G, 64) + (p.zero_rest ? 2 : 0)) * scols;
     for (int64_t first = 0; first < all; first += kMaxGrid) {
       const unsigned grid = (unsigned)(all - first < kMaxGrid ? all - first : kMaxGrid);
-      rows_small<E, ACROSS, GLU><<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, scols, first);
+      if (dma)
+        rows_small<E, ACROSS, GLU, true><<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, scols, first);
+      else
+        rows_small<E, ACROSS, GLU, false><<<grid, Wide<kSmall>::kThreads, 0, stream>>>(p, scols, first);
     }
     return;
   }
