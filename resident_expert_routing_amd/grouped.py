@@ -213,14 +213,27 @@ class GroupedExperts:
     and to the weights of the sum."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor):
-        S, two_i, H = gate_up.shape
-        if two_i % 2 or tuple(down.shape) != (S, H, two_i // 2):
+        gpu_tensor(gate_up, "gate_up")
+        gpu_tensor(down, "down")
+        if gate_up.dim() != 3 or gate_up.shape[1] % 2 or tuple(down.shape) != \
+                (gate_up.shape[0], gate_up.shape[2], gate_up.shape[1] // 2):
             raise ValueError(f"down {list(down.shape)} does not fit gate_up {list(gate_up.shape)}")
         self.gate_up, self.down = gate_up, down
-        self.S, self.I, self.H = S, two_i // 2, H
+        self.S, self.I, self.H = down.shape[0], down.shape[2], down.shape[1]
+        self._check_matrices()
+
+    def _check_matrices(self) -> None:
+        gpu_tensor(self.down, "down", gpu_tensor(self.gate_up, "gate_up").get_device())
+        dtype_of(self.gate_up, "gate_up")
+        if self.down.dtype != self.gate_up.dtype:
+            raise ValueError(f"gate_up is {self.gate_up.dtype}, down {self.down.dtype}")
 
     def check(self, x, T: int) -> None:
-        """Refuses token rows that are not [T, H] of the experts' type and device."""
+        """Refuses token rows that are not [T, H] of the experts' type and device, matrices
+        that differ in either (a parameter's may change after it was given), and tangents."""
+        self._check_matrices()
+        if forward_ad._current_level >= 0:
+            no_tangent("GroupedExperts", x, self.gate_up, self.down)
         gpu_tensor(x, "x", self.gate_up.get_device())
         if x.dtype != self.gate_up.dtype or tuple(x.shape) != (T, self.H):
             raise ValueError(f"x must be {self.gate_up.dtype} [{T}, {self.H}], not {x.dtype} "

@@ -332,6 +332,8 @@ def _layer_step(buf: LayerBuffers, x, w_router, bias, expert_slot, hist_row, exp
     """Routes with demand and runs `experts` on the bucketing, after the checks that keep
     what does not fit from being counted."""
     experts.check(x, buf.T)
+    if buf.perm.get_device() != x.get_device():
+        raise ValueError(f"buffers on {buf.perm.device}, x on {x.device}")
     if x.dtype != torch.bfloat16 or not x.is_contiguous():
         raise ValueError("x must be contiguous bfloat16 rows")
     if (experts.S, experts.H) != (buf.S, buf.H):

@@ -466,3 +466,38 @@ def test_long_groups_of_small_matrices(dtype, N, K, across):
     assert within(db, ref.db, ref.db_tol)
     again, = torch.autograd.grad(grouped.matmul(a, b, offsets), b, d)
     assert torch.equal(db, again)
+
+
+def test_experts_that_do_not_fit():
+    """Matrices of two types or places, or with a tangent, and buffers elsewhere are refused
+    before the demand is counted, also where they came to differ after they were given."""
+    from test_gpu_int8 import routed
+    from resident_expert_routing_amd import grouped
+    from resident_expert_routing_amd import runtime as R
+    buf, x, (wg, wu, wd), args = routed(8, 64, 8, 2, 32, 6, 6, 0)
+    gu, dn = torch.cat([wg, wu], 1).to(BF16), wd.to(BF16)
+    for bad in ((gu, dn.float()), (gu.float(), dn), (gu, dn.to(FP16)), (gu, dn.cpu()), (gu.cpu(), dn),
+                (gu.cpu(), dn.cpu()), (gu.int(), dn.int()), (gu[0], dn), (gu, dn[0]),
+                (gu, dn.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            grouped.GroupedExperts(*bad)
+    hist = torch.zeros(8, dtype=torch.float64, device="cuda")
+    step = lambda ex, buf=buf: R.layer_step_grouped(buf, x, args[0], None, args[1], hist, ex)
+    for which in range(2):
+        pair = [torch.nn.Parameter(t.clone()) for t in (gu, dn)]
+        ex = grouped.GroupedExperts(*pair)
+        for new in (lambda t: t.float(), lambda t: t.cpu()):
+            keep = pair[which].data
+            pair[which].data = new(keep)
+            with pytest.raises(ValueError):
+                step(ex)
+            pair[which].data = keep
+        with forward_ad.dual_level():
+            pair[which] = forward_ad.make_dual(pair[which].detach(), torch.ones_like(pair[which]))
+            with pytest.raises(ValueError, match="tangent"):
+                step(grouped.GroupedExperts(*pair))
+    ex = grouped.GroupedExperts(gu, dn)
+    with pytest.raises(ValueError):
+        step(ex, R.LayerBuffers(8, 64, 8, 2, 32, 6, torch.device("cpu")))
+    assert not hist.any()
+    assert step(ex).shape == x.shape and hist.any()
