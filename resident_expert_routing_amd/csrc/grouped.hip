@@ -23,7 +23,8 @@ constexpr int kMaxRows = 1 << 30;
 //   dg = d * u * (s + v * (1 - s)),  du = d * v,  s = 1 / (1 + exp(-g)), v = g * s
 // s from exp(-|g|), which cannot overflow.  Below kLow, where 1 - s is 1 in float32, exp(g)
 // is applied as two factors exp(g / 2), so that a gradient that is still a normal number
-// keeps its value to g = -174.  Bound by memory.
+// keeps its value to g = -174: d * u meets them first, or where float32 does not hold it
+// (then both are above 1) each of d and u one of them.  Bound by memory.
 template <typename E>
 __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const float* pre,
                                                             size_t pre_stride, const E* dout,
@@ -68,7 +69,10 @@ __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const 
       const float gf = g[i], uf = u[i], df = to_f32<E>(d.e[i]);
       const float h = __expf(0.5f * gf);
       if (gf < kLow) {
-        dg.e[i] = from_f32<E>((df * h) * (uf * (1.0f + gf) * h));
+        const float both = df * uf;
+        const float value = fabsf(both) < __builtin_inff() ? (both * h) * ((1.0f + gf) * h)
+                                                           : (df * h) * ((uf * h) * (1.0f + gf));
+        dg.e[i] = from_f32<E>(value);
         du.e[i] = from_f32<E>((df * h) * (gf * h));
       }
     }

@@ -501,3 +501,42 @@ def test_experts_that_do_not_fit():
         step(ex, R.LayerBuffers(8, 64, 8, 2, 32, 6, torch.device("cpu")))
     assert not hist.any()
     assert step(ex).shape == x.shape and hist.any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_low_gates(dtype):
+    """Gates from -64 to -173, in a product and in its gradient, with ups and gradients so large
+    that the value is a normal number: it keeps it."""
+    from resident_expert_routing_amd import grouped
+    f = torch.finfo(dtype)
+    g = -torch.arange(64, 174, device="cuda").float()
+    n = g.numel()
+    # exp's argument 1.25 |g| units of 2^-24; the exponentials, reciprocal and products 12
+    f32 = (1.25 * g.double().abs() + 12) * 2.0 ** -24
+    small = f.smallest_normal * 1.01
+    checked = 0
+    for u, d in ((1e38, 1.0), (3e38, 0.5), (1e19, 1e19), (0.25, 3e38), (1e-2, 1e38), (-1e38, 1e-2)):
+        us, ds = torch.full((n,), u, device="cuda"), torch.full((1, n), d, device="cuda").to(dtype)
+        gd, ud, dd = g.double(), us.double(), ds.double()
+        e = torch.exp(gd)
+        s = e / (1 + e)
+        want = torch.cat([dd * ud * (s + gd * s / (1 + e)), dd * gd * s], 1)
+        got = grouped._swiglu_backward(ds, torch.cat([g, us])[None]).double()
+        tol = want.abs() * (f32.repeat(2) + f.eps / 2 * 1.0001)
+        normal = (want.abs() >= small) & (want.abs() <= f.max / 1.01)
+        print(f"u {u} d {d}: {int(normal[:, :n].sum())} and {int(normal[:, n:].sum())} normal values, "
+              f"worst {float(((got - want).abs() / tol)[normal].nan_to_num(9).max()):.3f}", flush=True)
+        assert ((got - want).abs() <= tol)[normal].all()
+        checked += int(normal.sum())
+    assert checked > 3 * n
+    # the product itself: gates and ups that are one number each
+    up = 2.0 ** 127 * 1.5
+    a = torch.stack([g, torch.ones_like(g)], 1).to(dtype)
+    b = torch.tensor([[[1.0, 0.0], [0.0, up]]], device="cuda").to(dtype)
+    y = grouped.matmul(a, b, torch.tensor([0, n], dtype=torch.int32, device="cuda"), swiglu=True)
+    ad = a.double()
+    e = torch.exp(ad[:, 0])
+    want = ad[:, 0] * e / (1 + e) * float(b[0, 1, 1])
+    ok = (want.abs() >= small) & (want.abs() <= f.max / 1.01)
+    tol = want.abs() * (f32 + f.eps / 2 * 1.0001)
+    assert int(ok.sum()) > n // 2 and ((y[:, 0].double() - want).abs() <= tol)[ok].all()
