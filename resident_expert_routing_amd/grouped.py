@@ -26,6 +26,7 @@ from .rows import (RowOrder, _gather, combine, dtype_of, gpu_tensor, no_tangent,
                    row_major, stream_of)
 
 _lib = B.load()
+_MOST = 1 << 24  # contraction of a product; the gradients' products have b's rows there
 
 
 def _matrices(b: torch.Tensor):
@@ -190,6 +191,8 @@ def matmul(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, *,
                              "under torch.no_grad()")
         if a.requires_grad and index is not None:
             raise ValueError("the gradient of rows named by index needs `order`")
+        if wide > _MOST or (a.requires_grad and order is not None and order.k > B.MOE_MAX_K):
+            raise B.MoeError(B.MOE_EUNSUPPORTED, "the gradient of grouped products")
         return _Matmul.apply(a, b, offsets, order, index, int(index_div), M, N, bool(swiglu))
     given = out is not None
     if not given:

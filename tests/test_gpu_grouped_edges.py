@@ -540,3 +540,27 @@ def test_low_gates(dtype):
     ok = (want.abs() >= small) & (want.abs() <= f.max / 1.01)
     tol = want.abs() * (f32 + f.eps / 2 * 1.0001)
     assert int(ok.sum()) > n // 2 and ((y[:, 0].double() - want).abs() <= tol)[ok].all()
+
+
+def test_a_recorded_call_has_a_gradient():
+    """What the gradient's products could not take is refused when the call is recorded."""
+    from resident_expert_routing_amd import binding as B
+    from resident_expert_routing_amd import grouped, rows
+    a = torch.ones(3, 1, dtype=BF16, device="cuda", requires_grad=True)
+    b = torch.ones(1, (1 << 24) + 2, 1, dtype=BF16, device="cuda")
+    offsets = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    with torch.no_grad():
+        assert grouped.matmul(a, b, offsets, swiglu=True).shape == (3, (1 << 23) + 1)
+    with pytest.raises(B.MoeError):
+        grouped.matmul(a, b, offsets, swiglu=True)
+    k = B.MOE_MAX_K + 1                     # more picks than a token's sum takes
+    perm = torch.arange(3 * k, dtype=torch.int32, device="cuda")
+    order = rows.RowOrder(perm, 3, k, perm.view(3, k))
+    offsets[1] = 3 * k
+    with torch.no_grad():
+        assert grouped.matmul(a, b[:, :8], offsets, order=order).shape == (3 * k, 8)
+    with pytest.raises(B.MoeError):
+        grouped.matmul(a, b[:, :8], offsets, order=order)
+    leaf = b[:, :8].clone().requires_grad_()
+    y = grouped.matmul(a.detach(), leaf, offsets, order=order)
+    assert (torch.autograd.grad(y, leaf, torch.ones_like(y))[0] == 3 * k).all()
