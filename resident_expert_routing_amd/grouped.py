@@ -9,7 +9,7 @@
 fp32; sums are float32), and gradients go to both (moe_grouped_matmul, moe_grouped_outer,
 moe_swiglu_backward).  A call that is recorded keeps copies of the offsets and of the
 order, which the next moe_route may write over, and with SwiGLU the products before it in
-float32; rows and matrices are kept as they are.
+float32; rows are kept as they are for the matrices' gradient, matrices for the rows'.
 There is no forward-mode derivative: tensors that carry a tangent are refused.  Calls run
 on the current stream of their tensors' device and synchronise nothing.  A gradient
 captured into a graph is taken with torch.autograd.grad, or with no graph made outside the
@@ -97,10 +97,17 @@ class _Matmul(torch.autograd.Function):
         out = torch.empty((M, N), dtype=a.dtype, device=a.device)
         keep = order.kept() if order is not None else None
         idx = keep.perm if keep is not None else index
-        pre = _products(a, _matrices(b), offsets, idx, index_div, M, N, swiglu, out, True, swiglu)
-        ctx.order, ctx.index_div, ctx.sizes = keep, index_div, (M, N, swiglu)
-        ctx.save_for_backward(a, b, offsets.clone(),
-                              index.clone() if index is not None else None, pre)
+        taken = _matrices(b)
+        pre = _products(a, taken, offsets, idx, index_div, M, N, swiglu, out, True, swiglu)
+        # each gradient reads the other operand, a's the places of a token's rows and b's the
+        # rows' names
+        da, db = ctx.needs_input_grad[:2]
+        named = None if not db else keep.perm if keep is not None else \
+            index.clone() if index is not None else None
+        ctx.save_for_backward(a if db else None, b if da else None, offsets.clone(), named,
+                              keep.pos if da and keep is not None else None, pre)
+        ctx.sizes = M, N, a.shape[1], swiglu, index_div, taken[1]
+        ctx.tokens = (order.T, order.k) if order is not None else None
         return out
 
     @staticmethod
@@ -109,28 +116,24 @@ class _Matmul(torch.autograd.Function):
             raise RuntimeError("grouped products have no second derivative: take their gradient "
                                "without create_graph")
         no_tangent("the gradient of grouped products", grad)
-        a, b, offsets, index, pre = ctx.saved_tensors
-        order, div = ctx.order, ctx.index_div
-        M, N, swiglu = ctx.sizes
-        if order is not None:
-            index = order.perm
+        a, b, offsets, named, pos, pre = ctx.saved_tensors
+        M, N, K, swiglu, div, across = ctx.sizes
         dz = _swiglu_backward(grad, pre) if swiglu else grad
-        b, across, down, group = _matrices(b)
         da = db = None
         if ctx.needs_input_grad[0]:
-            K = b.shape[2]
+            b, across, down, group = _matrices(b)
             # a token's rows are summed before they are rounded
-            rows = torch.float32 if order is not None else a.dtype
-            da = torch.empty((M, K), dtype=rows, device=a.device)
+            rows = torch.float32 if ctx.tokens is not None else grad.dtype
+            da = torch.empty((M, K), dtype=rows, device=grad.device)
             _products(dz, (b, not across, down, group), offsets, None, 1, M, K, False, da, True,
                       False)
-            if order is not None:
-                da = _gather(da, order, None)[0].to(a.dtype)
+            if ctx.tokens is not None:
+                da = _gather(da, RowOrder.of(None, pos, *ctx.tokens), None)[0].to(grad.dtype)
         if ctx.needs_input_grad[1]:
             if across:
-                db = _outer(a, index, div, dz, None, 1, offsets, M).transpose(1, 2)
+                db = _outer(a, named, div, dz, None, 1, offsets, M).transpose(1, 2)
             else:
-                db = _outer(dz, None, 1, a, index, div, offsets, M)
+                db = _outer(dz, None, 1, a, named, div, offsets, M)
         return da, db, None, None, None, None, None, None, None
 
 

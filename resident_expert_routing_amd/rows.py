@@ -126,10 +126,17 @@ class RowOrder:
         """The order in tensors of its own."""
         if self.own:
             return self
-        order = object.__new__(RowOrder)
-        order.T, order.k, order.device, order.own = self.T, self.k, self.device, True
         both = torch.cat((self.pos.view(-1), self.perm.view(-1)))
-        order.pos, order.perm = both.view(2, self.T, self.k).unbind()
+        pos, perm = both.view(2, self.T, self.k).unbind()
+        return RowOrder.of(perm, pos, self.T, self.k)
+
+    @staticmethod
+    def of(perm, pos, T: int, k: int) -> "RowOrder":
+        """An order of tensors that nobody else writes; perm may be None for a call that
+        reads pos alone."""
+        order = object.__new__(RowOrder)
+        order.T, order.k, order.device, order.own = T, k, pos.get_device(), True
+        order.pos, order.perm = pos, perm
         return order
 
 

@@ -564,3 +564,55 @@ def test_a_recorded_call_has_a_gradient():
     leaf = b[:, :8].clone().requires_grad_()
     y = grouped.matmul(a.detach(), leaf, offsets, order=order)
     assert (torch.autograd.grad(y, leaf, torch.ones_like(y))[0] == 3 * k).all()
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_what_a_gradient_does_not_read_may_change(swiglu):
+    """Rows may be written over where only their own gradient is wanted, and matrices likewise;
+    what the wanted gradient reads is refused."""
+    from resident_expert_routing_amd import grouped
+    a, b, offsets, d = case([10, 0, 25], 24, 16, FP32, swiglu=swiglu)
+    b1 = b.clone().requires_grad_()
+    want = torch.autograd.grad(grouped.matmul(a.requires_grad_(), b1, offsets, swiglu=swiglu), [a, b1], d)
+    a = a.detach()
+    x, w = a.clone().requires_grad_(), b.clone()
+    inner = x * 1
+    y = grouped.matmul(inner, w, offsets, swiglu=swiglu)
+    inner.add_(1)
+    assert torch.equal(torch.autograd.grad(y, x, d)[0], want[0])
+    y = grouped.matmul(x * 1, w, offsets, swiglu=swiglu)
+    w.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        torch.autograd.grad(y, x, d)
+    x, w = a.clone(), b.clone().requires_grad_()
+    y = grouped.matmul(x, w, offsets, swiglu=swiglu)
+    with torch.no_grad():
+        w.add_(1)
+    assert torch.equal(torch.autograd.grad(y, w, d)[0], want[1])
+    y = grouped.matmul(x, w, offsets, swiglu=swiglu)
+    x.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        torch.autograd.grad(y, w, d)
+
+
+def test_hooks_see_all_that_is_kept():
+    """Everything that a recorded call keeps for its gradient passes through torch's hooks for
+    saved tensors, the order too, and may come back from elsewhere."""
+    from resident_expert_routing_amd import grouped, rows
+    gen = torch.Generator().manual_seed(8)
+    T, k = 50, 2
+    perm, offsets = (t.cuda() for t in bucketing([30, 50, 20], gen))
+    a = torch.randn(T, 32, generator=gen).to(BF16).cuda().requires_grad_()
+    b = torch.randn(3, 16, 32, generator=gen).to(BF16).cuda().requires_grad_()
+    d = torch.randn(T * k, 16, generator=gen).to(BF16).cuda()
+    order = rows.RowOrder(perm, T, k)
+    seen = []
+    def pack(t):
+        seen.append(t.data_ptr())
+        return t.cpu()
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t.cuda()):
+        y = grouped.matmul(a, b, offsets, order=order)
+    assert {t.data_ptr() for t in (a, b, order.pos, order.perm)} <= set(seen)
+    want = torch.autograd.grad(grouped.matmul(a, b, offsets, order=order), [a, b], d)
+    for g, w in zip(torch.autograd.grad(y, [a, b], d), want):
+        assert torch.equal(g, w)
