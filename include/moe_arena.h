@@ -761,13 +761,15 @@ int moe_int8_matmul(const moe_int8_matmul_args* args, hipStream_t stream);
  * MOE_DT_FP32.  fp32 products are float32 products.  silu is within (1.25 |v| + 8) * 2^-24 of its value down to v = -174,
  * below which it is 0.
  *   r = p, or with index: index[p] / index_div (moe_route's perm and k name the token
- *   of a row).  Nothing is computed for rows whose r is outside [0, a_rows), nor for
- *   rows in no group (before offsets[0], from offsets[G] on): with zero_rest they are
+ *   of a row).  Nothing is computed for rows whose r is outside [0, a_rows), nor with pos
+ *   for those whose assignment has another row (index[p] in [0, M) and pos[index[p]] != p:
+ *   the earlier row of an assignment named twice, as in moe_dispatch), nor for rows in no group (before offsets[0], from offsets[G] on): with zero_rest they are
  *   set to zero, without it left as they were.  Offsets have to ascend; they are cut
  *   to [0, M].
  * Inputs : a [a_rows][K], rows a_stride elements apart; offsets [G+1] int32; b: for
  *          each group N (2N) rows of K elements b_stride apart, or with b_across K rows
- *          of N (2N); groups b_group_stride elements apart (0: all groups share one).
+ *          of N (2N); groups b_group_stride elements apart (0: all groups share one); pos
+ *          [M] int32 (nullable, with index only): what moe_positions makes of index.
  * Outputs: out, rows out_stride elements apart (>= N); with swiglu pre (nullable), the
  *          products z before SwiGLU, float [M][2N], rows pre_stride apart, for
  *          moe_swiglu_backward (rounded to 16 bits they would double the error of the
@@ -776,7 +778,7 @@ int moe_int8_matmul(const moe_int8_matmul_args* args, hipStream_t stream);
  *          overlap an input or the other.  Everything may start at any element.
  * Errors : MOE_EINVAL for null or misaligned pointers (the element's size; 4 bytes for
  *          int32), a bad size, stride, dtype or flag, index without index_div >= 1,
- *          fewer rows of a than M without index, or pre without swiglu;
+ *          fewer rows of a than M without index, pos without index, or pre without swiglu;
  *          MOE_EUNSUPPORTED for N or K > 2^24, M > 2^30 or G > MOE_MAX_S.
  *          M = 0 is valid and does nothing.  No workspace.
  * The gradient of a is this call too: da[p] = sum_n dz[p][n] * b[g][n] has dz for a and
@@ -799,6 +801,7 @@ typedef struct moe_grouped_matmul_args {
   float* pre;
   size_t pre_stride;
   int out_dtype;
+  const int32_t* pos;
 } moe_grouped_matmul_args;
 
 int moe_grouped_matmul(const moe_grouped_matmul_args* args, hipStream_t stream);
@@ -808,8 +811,10 @@ int moe_grouped_matmul(const moe_grouped_matmul_args* args, hipStream_t stream);
  *   out[g][l][r] = sum over offsets[g] <= p < offsets[g+1] of left[pl][l] * right[pr][r]
  * with float32 sums over ascending p in a fixed order and one rounding; a group without
  * rows gets zeros.  pl = p, or left_index[p] / left_div; pr likewise (at
- * most one operand has an index); a row p for which it is outside its array adds nothing.  With left = dz and right = a this is the
- * gradient of b [N][K]; the other way round, that of b [K][N].
+ * most one operand has an index); a row p for which it is outside its array adds nothing, nor
+ * one that pos ([M], nullable, with an index only) excludes as in moe_grouped_matmul.  With
+ * left = dz and right = a this is the gradient of b [N][K]; the other way round, that of
+ * b [K][N].
  * Inputs : left [left_rows][L], right [right_rows][R], rows their strides apart;
  *          offsets [G+1] int32, cut to [0, M].
  * Output : out [G][L][R], rows out_stride elements apart, groups out_group_stride; must
@@ -836,6 +841,7 @@ typedef struct moe_grouped_outer_args {
   size_t out_group_stride;
   void* ws;
   size_t ws_bytes;
+  const int32_t* pos;
 } moe_grouped_outer_args;
 
 size_t moe_grouped_outer_ws_bytes(int M, int L, int R, int G, int dtype);

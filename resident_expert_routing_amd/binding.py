@@ -122,7 +122,7 @@ class GroupedMatmulArgs(ctypes.Structure):
                 ("b_stride", ctypes.c_size_t), ("b_group_stride", ctypes.c_size_t),
                 ("out", ctypes.c_void_p), ("out_stride", ctypes.c_size_t),
                 ("pre", ctypes.c_void_p), ("pre_stride", ctypes.c_size_t),
-                ("out_dtype", ctypes.c_int)]
+                ("out_dtype", ctypes.c_int), ("pos", ctypes.c_void_p)]
 
 
 class GroupedOuterArgs(ctypes.Structure):
@@ -135,7 +135,7 @@ class GroupedOuterArgs(ctypes.Structure):
                 ("right_div", ctypes.c_int), ("offsets", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("out_stride", ctypes.c_size_t),
                 ("out_group_stride", ctypes.c_size_t), ("ws", ctypes.c_void_p),
-                ("ws_bytes", ctypes.c_size_t)]
+                ("ws_bytes", ctypes.c_size_t), ("pos", ctypes.c_void_p)]
 
 
 class Int4MatmulArgs(ctypes.Structure):
@@ -520,7 +520,7 @@ def moe_int8_matmul(M, N, K, G, swiglu, a_rows, a, a_stride, a_scale, index, ind
 
 def moe_grouped_matmul(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, a, a_stride, index,
                        index_div, offsets, b, b_stride, b_group_stride, out, out_stride, pre=None,
-                       pre_stride=0, out_dtype=None, stream=None) -> int:
+                       pre_stride=0, out_dtype=None, pos=None, stream=None) -> int:
     out_dtype = dtype if out_dtype is None else out_dtype
     if not fits(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, index_div, out_dtype):
         return MOE_EUNSUPPORTED
@@ -528,20 +528,21 @@ def moe_grouped_matmul(M, N, K, G, dtype, swiglu, b_across, zero_rest, a_rows, a
                              int(b_across), int(zero_rest), int(a_rows), _ptr(a), int(a_stride),
                              _ptr(index), int(index_div), _ptr(offsets), _ptr(b), int(b_stride),
                              int(b_group_stride), _ptr(out), int(out_stride), _ptr(pre),
-                             int(pre_stride), int(out_dtype))
+                             int(pre_stride), int(out_dtype), _ptr(pos))
     return int(load().moe_grouped_matmul(ctypes.byref(args), _stream(stream)))
 
 
 def moe_grouped_outer(M, L, R, G, dtype, left_rows, right_rows, left, left_stride, left_index,
                       left_div, right, right_stride, right_index, right_div, offsets, out,
-                      out_stride, out_group_stride, ws=None, ws_bytes=0, stream=None) -> int:
+                      out_stride, out_group_stride, ws=None, ws_bytes=0, pos=None,
+                      stream=None) -> int:
     if not fits(M, L, R, G, dtype, left_rows, right_rows, left_div, right_div):
         return MOE_EUNSUPPORTED
     args = GroupedOuterArgs(int(M), int(L), int(R), int(G), int(dtype), int(left_rows),
                             int(right_rows), _ptr(left), int(left_stride), _ptr(left_index),
                             int(left_div), _ptr(right), int(right_stride), _ptr(right_index),
                             int(right_div), _ptr(offsets), _ptr(out), int(out_stride),
-                            int(out_group_stride), _ptr(ws), int(ws_bytes))
+                            int(out_group_stride), _ptr(ws), int(ws_bytes), _ptr(pos))
     return int(load().moe_grouped_outer(ctypes.byref(args), _stream(stream)))
 
 

@@ -110,6 +110,7 @@ int matmul_status(const moe_grouped_matmul_args* a) {
   if (!a->a || !a->b || !a->out || !a->offsets || a->a_rows == 0) return MOE_EINVAL;
   if (a->index ? a->index_div < 1 : a->a_rows < a->M) return MOE_EINVAL;
   if (a->pre && !a->swiglu) return MOE_EINVAL;
+  if (!aligned(a->pos, 4) || (a->pos && !a->index)) return MOE_EINVAL;
   if (!aligned(a->a, e) || !aligned(a->b, e) || !aligned(a->out, o) || !aligned(a->pre, 4) ||
       !aligned(a->offsets, 4) || !aligned(a->index, 4))
     return MOE_EINVAL;
@@ -140,6 +141,7 @@ int outer_status(const moe_grouped_outer_args* a) {
       !aligned(a->left_index, 4) || !aligned(a->right_index, 4))
     return MOE_EINVAL;
   if (a->left_index && a->right_index) return MOE_EINVAL;
+  if (!aligned(a->pos, 4) || (a->pos && !a->left_index && !a->right_index)) return MOE_EINVAL;
   if (a->left_index ? a->left_div < 1 : a->left_rows < a->M) return MOE_EINVAL;
   if (a->right_index ? a->right_div < 1 : a->right_rows < a->M) return MOE_EINVAL;
   if (a->left_stride < (size_t)a->L || a->right_stride < (size_t)a->R) return MOE_EINVAL;
@@ -156,7 +158,7 @@ extern "C" MOE_EXPORT int moe_grouped_matmul(const moe_grouped_matmul_args* a,
   p.M = a->M, p.N = a->N, p.K = a->K, p.G = a->G;
   p.a_rows = a->a_rows, p.index_div = a->index_div;
   p.a = a->a, p.b = a->b, p.out = a->out, p.pre = a->pre;
-  p.index = a->index, p.offsets = a->offsets;
+  p.index = a->index, p.pos = a->pos, p.offsets = a->offsets;
   p.a_stride = a->a_stride, p.b_stride = a->b_stride, p.b_group_stride = a->b_group_stride;
   p.out_stride = a->out_stride, p.pre_stride = a->pre_stride;
   p.zero_rest = a->zero_rest;
@@ -178,7 +180,7 @@ extern "C" MOE_EXPORT int moe_grouped_outer(const moe_grouped_outer_args* a, hip
   OuterProduct p{};
   p.M = a->M, p.L = a->L, p.R = a->R, p.G = a->G;
   p.left = a->left, p.right = a->right, p.out = a->out, p.offsets = a->offsets;
-  p.left_index = a->left_index, p.right_index = a->right_index;
+  p.left_index = a->left_index, p.right_index = a->right_index, p.pos = a->pos;
   p.left_rows = a->left_rows, p.right_rows = a->right_rows;
   p.left_div = a->left_div, p.right_div = a->right_div;
   p.left_stride = a->left_stride, p.right_stride = a->right_stride;

@@ -26,6 +26,7 @@ struct RowsProduct {
   void* out;
   float* pre;  // the products before SwiGLU, [M][2N], or null
   const int32_t *index, *offsets;
+  const int32_t* pos;  // the row of each of M assignments, or null: the only one that index names
   size_t a_stride, b_stride, b_group_stride, out_stride, pre_stride;  // elements
   bool zero_rest;  // rows that nothing is computed for become zero
   bool out_f32;    // out is float32 whatever the element type
@@ -36,6 +37,7 @@ struct OuterProduct {
   const void *left, *right;
   void* out;
   const int32_t *left_index, *right_index, *offsets;
+  const int32_t* pos;  // as in RowsProduct, for the operand that has an index
   size_t left_stride, right_stride, out_stride, out_group_stride;  // elements
   int splits;   // parts of each group's rows, with sums of their own
   float* sums;  // [splits][G][L][R], or null for one part
@@ -45,6 +47,22 @@ template <typename E>
 int launch_rows_product(const RowsProduct& p, bool across, bool glu, hipStream_t stream);
 template <typename E>
 int launch_outer_product(const OuterProduct& p, hipStream_t stream);
+
+// The assignment that row m has of `index`; -1 for none, or with pos for one whose row is
+// another.
+__device__ __forceinline__ int named_at(const int32_t* index, const int32_t* pos, int M, int m) {
+  const int r = index[m];
+  if (!pos || (unsigned)r >= (unsigned)M) return r < 0 ? -1 : r;
+  return pos[r] == m ? r : -1;
+}
+__device__ __forceinline__ int source_row(const RowsProduct& p, int m) {
+  int r = m;
+  if (p.index) {
+    r = named_at(p.index, p.pos, p.M, m);
+    r = r < 0 ? -1 : r / p.index_div;
+  }
+  return (unsigned)r < (unsigned)p.a_rows ? r : -1;
+}
 
 // acc += products of 16 x 16 fragments over 64 bytes of contraction, sums in float32.
 // A lane holds 16 bytes of row (lane & 15) from byte 16 * (lane >> 4) on; it gets rows
@@ -816,7 +834,7 @@ __global__ __launch_bounds__(Wide<WA>::kThreads, 2) void outer_tiles(OuterProduc
       const int div = INDEXED == kLeft ? p.left_div : p.right_div;
       const int rows = INDEXED == kLeft ? p.left_rows : p.right_rows;
       for (int t = threadIdx.x; t < n; t += kThreads) {
-        int r = index[m0 + t];
+        int r = named_at(index, p.pos, p.M, m0 + t);
         r = r < 0 ? -1 : r / div;
         table[t] = (unsigned)r < (unsigned)rows ? r : -1;
       }

@@ -42,7 +42,7 @@ def _matrices(b: torch.Tensor):
 
 
 @on_its_device
-def _products(a, b, offsets, index, index_div, M, N, swiglu, out, zero, keep):
+def _products(a, b, offsets, index, index_div, M, N, swiglu, out, zero, keep, pos=None):
     """out [M, N], and with `keep` the products before SwiGLU; b as _matrices has it."""
     b, across, down, group = b
     a, stride = row_major(a)
@@ -52,14 +52,15 @@ def _products(a, b, offsets, index, index_div, M, N, swiglu, out, zero, keep):
         M, N, K, G, dtype_of(a, "a"), swiglu, across, zero, a.shape[0], a.data_ptr(), stride,
         None if index is None else index.data_ptr(), index_div, offsets.data_ptr(), b.data_ptr(),
         down, group, out.data_ptr(), out.stride(0) if M > 1 else N,
-        None if pre is None else pre.data_ptr(), 2 * N, dtype_of(out, "out")), stream_of(a))
+        None if pre is None else pre.data_ptr(), 2 * N, dtype_of(out, "out"),
+        None if pos is None else pos.data_ptr()), stream_of(a))
     if st != B.MOE_OK:
         raise B.MoeError(st, "moe_grouped_matmul")
     return pre
 
 
 @on_its_device
-def _outer(left, left_index, left_div, right, right_index, right_div, offsets, M):
+def _outer(left, left_index, left_div, right, right_index, right_div, offsets, M, pos=None):
     """[G, L, R]: the sums of left[p] x right[p] over each group's rows."""
     left, ls = row_major(left)
     right, rs = row_major(right)
@@ -72,7 +73,7 @@ def _outer(left, left_index, left_div, right, right_index, right_div, offsets, M
     st = _lib.moe_grouped_outer(B.GroupedOuterArgs(
         M, L, R, G, dt, left.shape[0], right.shape[0], left.data_ptr(), ls,
         at(left_index), left_div, right.data_ptr(), rs, at(right_index), right_div,
-        offsets.data_ptr(), out.data_ptr(), R, L * R, at(ws), need), stream_of(left))
+        offsets.data_ptr(), out.data_ptr(), R, L * R, at(ws), need, at(pos)), stream_of(left))
     if st != B.MOE_OK:
         raise B.MoeError(st, "moe_grouped_outer")
     return out
@@ -96,16 +97,14 @@ class _Matmul(torch.autograd.Function):
     def forward(ctx, a, b, offsets, order, index, index_div, M, N, swiglu):
         out = torch.empty((M, N), dtype=a.dtype, device=a.device)
         keep = order.kept() if order is not None else None
-        idx = keep.perm if keep is not None else index
+        idx, pos = (keep.perm, keep.pos) if keep is not None else (index, None)
         taken = _matrices(b)
-        pre = _products(a, taken, offsets, idx, index_div, M, N, swiglu, out, True, swiglu)
-        # each gradient reads the other operand, a's the places of a token's rows and b's the
-        # rows' names
+        pre = _products(a, taken, offsets, idx, index_div, M, N, swiglu, out, True, swiglu, pos)
+        # each gradient reads the other operand, and b's the rows' names
         da, db = ctx.needs_input_grad[:2]
         named = None if not db else keep.perm if keep is not None else \
             index.clone() if index is not None else None
-        ctx.save_for_backward(a if db else None, b if da else None, offsets.clone(), named,
-                              keep.pos if da and keep is not None else None, pre)
+        ctx.save_for_backward(a if db else None, b if da else None, offsets.clone(), named, pos, pre)
         ctx.sizes = M, N, a.shape[1], swiglu, index_div, taken[1]
         ctx.tokens = (order.T, order.k) if order is not None else None
         return out
@@ -131,9 +130,9 @@ class _Matmul(torch.autograd.Function):
                 da = _gather(da, RowOrder.of(None, pos, *ctx.tokens), None)[0].to(grad.dtype)
         if ctx.needs_input_grad[1]:
             if across:
-                db = _outer(a, named, div, dz, None, 1, offsets, M).transpose(1, 2)
+                db = _outer(a, named, div, dz, None, 1, offsets, M, pos).transpose(1, 2)
             else:
-                db = _outer(dz, None, 1, a, named, div, offsets, M)
+                db = _outer(dz, None, 1, a, named, div, offsets, M, pos)
         return da, db, None, None, None, None, None, None, None
 
 
@@ -147,7 +146,8 @@ def matmul(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, *,
     axis (a transposed view of [G, K, N] is taken as it lies; other layouts are copied).
     swiglu: b holds 2N rows, gate then up, and out = silu(gate) * up.  The rows of a: r = p;
     with `order` (rows.RowOrder of T*k assignments) the token row perm[p] // k, and a has
-    T rows; with `index` (int32 [M]) r = index[p] // index_div.  Gradients go to a and b;
+    T rows (the earlier row of an assignment that it names twice has none, as in
+    rows.dispatch); with `index` (int32 [M]) r = index[p] // index_div.  Gradients go to a and b;
     that of rows named by `index` has to be taken with `order`, which knows each token's
     rows.  Rows of out that nothing is computed for (in no group, or whose index is
     negative) are zero; in an `out` of the caller's, [M, N] with contiguous rows, which is
@@ -170,13 +170,13 @@ def matmul(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, *,
         raise ValueError(f"b {list(b.shape)}: swiglu needs an even number of rows, and K and N "
                          "are at least 1")
     N = wide // 2 if swiglu else wide
-    M, own_index = rows, None
+    M, own_index, pos = rows, None, None
     if order is not None:
         if index is not None:
             raise ValueError("order or index, not both")
         if order.device != dev or rows != order.T:
             raise ValueError(f"a must hold the order's {order.T} token rows, on its device")
-        M, own_index, index_div = order.T * order.k, order.perm, order.k
+        M, own_index, pos, index_div = order.T * order.k, order.perm, order.pos, order.k
     elif index is not None:
         if gpu_tensor(index, "index", dev).dtype != torch.int32:
             raise ValueError("index must be int32")
@@ -206,7 +206,7 @@ def matmul(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, *,
         if (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
             raise ValueError("the rows of out must be contiguous and apart")
     _products(a, _matrices(b), offsets, own_index, int(index_div), M, N, bool(swiglu), out,
-              not given, False)
+              not given, False, pos)
     if given and not out.is_inference():
         torch.autograd.graph.increment_version([out])
     return out

@@ -616,3 +616,41 @@ def test_hooks_see_all_that_is_kept():
     want = torch.autograd.grad(grouped.matmul(a, b, offsets, order=order), [a, b], d)
     for g, w in zip(torch.autograd.grad(y, [a, b], d), want):
         assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("swiglu,across", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("dtype,counts,N,K", [
+    (BF16, [9, 0, 11], 24, 40),                                   # the streaming form, or small tiles
+    (FP16, [70, 3, 67], 72, 136), (FP32, [70, 3, 67], 41, 35),    # small tiles
+    (BF16, [300, 4, 90, 1, 129] * 20, 300, 72)])                  # large tiles
+def test_an_assignment_named_twice(counts, N, K, swiglu, across, dtype):
+    """As in dispatch: the earlier row of an assignment that the order names twice is zero, and
+    has no part in a gradient."""
+    from resident_expert_routing_amd import grouped, rows
+    k, G = 2, len(counts)
+    gen = torch.Generator().manual_seed(9)
+    perm, offsets = bucketing(counts, gen, tail=sum(counts) % 2)
+    M = perm.numel()
+    early = torch.arange(0, M // 2, 3)
+    perm[early] = perm[M // 2 + early // 2]
+    perm[M // 2 - 1] = M                                          # names nothing
+    index = torch.where((perm < 0) | (perm >= M), -1, perm // k)
+    holes = index.clone()
+    holes[early] = -1
+    a = torch.randn(M // k, K, generator=gen).to(dtype).cuda().requires_grad_()
+    b = (torch.randn(G, 2 * N if swiglu else N, K, generator=gen) * K ** -0.5).to(dtype).cuda()
+    if across:
+        b = b.transpose(1, 2).contiguous().transpose(1, 2)
+    b = b.detach().requires_grad_()
+    d = torch.randn(M, N, generator=gen).to(dtype).cuda()
+    perm, offsets, holes = perm.cuda(), offsets.cuda(), holes.cuda()
+    ref = Reference(a.detach(), b.detach(), offsets, holes, M, swiglu, dtype, d, token_sum=True)
+    order = rows.RowOrder(perm, M // k, k)
+    y = grouped.matmul(a, b, offsets, order=order, swiglu=swiglu)
+    assert within(y.detach(), ref.out, ref.out_tol) and not y[holes < 0].any()
+    with torch.no_grad():
+        assert torch.equal(grouped.matmul(a, b, offsets, order=order, swiglu=swiglu), y)
+    d[holes < 0] = float("nan")
+    da, db = torch.autograd.grad(y, [a, b], d)
+    assert within(da, ref.da, ref.da_tol)
+    assert within(db, ref.db, ref.db_tol)

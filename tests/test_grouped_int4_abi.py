@@ -150,3 +150,20 @@ def test_layout_of_matrices():
     assert grouped._matrices(b[:, :, :7])[1:] == (False, 20, 160)
     for odd in (b[:, :, ::2], b.permute(1, 2, 0)[:, ::2], b[:, :1].expand(3, 8, 20)):
         assert grouped._matrices(odd)[0].is_contiguous()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(pos=FAKE), E), (dict(pos=FAKE + 2, index=FAKE, index_div=1), E),
+    (dict(pos=FAKE + 2, index=FAKE, index_div=1, M=0), B.MOE_OK)])
+def test_positions_go_with_an_index(kw, code):
+    a = dict(M=8, N=64, K=100, G=2, dtype=0, swiglu=0, b_across=0, zero_rest=0, a_rows=8, a=FAKE,
+             a_stride=100, index=None, index_div=0, offsets=FAKE, b=FAKE, b_stride=100,
+             b_group_stride=6400, out=FAKE, out_stride=64)
+    assert B.moe_grouped_matmul(**(a | kw)) == code
+    o = dict(M=8, L=64, R=100, G=2, dtype=0, left_rows=8, right_rows=8, left=FAKE, left_stride=64,
+             left_index=None, left_div=1, right=FAKE, right_stride=100, right_index=None,
+             right_div=1, offsets=FAKE, out=FAKE, out_stride=100, out_group_stride=6400)
+    for side in ("left", "right"):
+        as_here = {"pos": "pos", "index": f"{side}_index", "index_div": f"{side}_div"}
+        names = {as_here[k]: v for k, v in kw.items() if k != "M"}
+        assert B.moe_grouped_outer(**(o | names)) == E
