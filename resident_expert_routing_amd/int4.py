@@ -55,8 +55,7 @@ class Int4Weight:
             raise ValueError(f"scales are bfloat16 or float16, not {scale.dtype}")
         lead = tuple(codes.shape[:-4])
         if scale.dim() != len(lead) + 3 or tuple(scale.shape[:-2]) != (*lead, blocks) or \
-                scale.shape[-1] != 16 or _up(K, 128) // max(scale.shape[-2], 1) not in GROUPS or \
-                _up(K, 128) % scale.shape[-2]:
+                scale.shape[-1] != 16 or all(scale.shape[-2] * g != _up(K, 128) for g in GROUPS):
             raise ValueError(f"scale {list(scale.shape)} does not fit groups of 32, 64 or 128 "
                              f"weights of {list(lead)} matrices {N} x {K}")
         if zero is not None and (gpu_tensor(zero, "zero", dev).dtype != torch.uint8

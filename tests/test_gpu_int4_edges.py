@@ -318,3 +318,11 @@ def test_up_rows_inside_a_tile():
         assert within(got[lo:hi], y, tol)
     rows = ex.rows(x, offsets, perm, 1)
     assert rows.shape == (6, H) and torch.isfinite(rows).all()
+
+
+def test_scales_that_are_no_groups():
+    from resident_expert_routing_amd import int4
+    w, _, _ = made(0, 32, 128, zeros=False)
+    for n in (0, 3, 8):
+        with pytest.raises(ValueError):
+            int4.Int4Weight(w.codes, torch.empty(2, n, 16, dtype=BF16, device="cuda"), N=32, K=128)
