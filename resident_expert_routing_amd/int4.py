@@ -170,7 +170,8 @@ def pack(codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = N
          group: int = 128) -> Int4Weight:
     """An Int4Weight of codes 0..15 that exist already: codes uint8 [.., N, K], scale (bf16 or
     fp16) and zero (uint8, or None: 8) [.., N, ceil(K / group)].  For loading: elementary
-    torch operations, matrix by matrix."""
+    torch operations, matrix by matrix.  There is no gradient: scales that want one, or carry
+    a tangent, are refused."""
     dev = gpu_tensor(codes, "codes").get_device()
     gpu_tensor(scale, "scale", dev)
     *lead, N, K = codes.shape
@@ -182,6 +183,7 @@ def pack(codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = N
     if zero is not None and (gpu_tensor(zero, "zero", dev).shape != scale.shape
                              or zero.dtype != torch.uint8):
         raise ValueError("zero must be uint8 of scale's shape")
+    _no_gradient("int4.pack", scale)
     out = Int4Weight.empty(*codes.shape, group=group, zeros=zero is not None,
                            scale_dtype=scale.dtype, device=codes.device)
     for g in range(out.G) if out.G else (None,):

@@ -326,3 +326,16 @@ def test_scales_that_are_no_groups():
     for n in (0, 3, 8):
         with pytest.raises(ValueError):
             int4.Int4Weight(w.codes, torch.empty(2, n, 16, dtype=BF16, device="cuda"), N=32, K=128)
+
+
+def test_pack_has_no_gradient():
+    """Scales that want a gradient, or carry a tangent, are refused; under no_grad they pass."""
+    from resident_expert_routing_amd import int4
+    codes = torch.randint(0, 16, (16, 128), dtype=torch.uint8, device="cuda")
+    scale = torch.rand(16, 2, device="cuda").to(BF16).requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        int4.pack(codes, scale, group=64)
+    with torch.no_grad():
+        assert not int4.pack(codes, scale, group=64).scale.requires_grad
+    with forward_ad.dual_level(), pytest.raises(ValueError, match="tangent"):
+        int4.pack(codes, forward_ad.make_dual(scale.detach(), scale.detach()), group=64)
