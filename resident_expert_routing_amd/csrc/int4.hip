@@ -496,7 +496,8 @@ __global__ __launch_bounds__(kWave) void quantize_tiles(const E* w, int N, int K
     lo = fminf(lo, __shfl_xor(lo, d, 64)), hi = fmaxf(hi, __shfl_xor(hi, d, 64));
     bad |= __shfl_xor(bad, d, 64);
   }
-  const float want = zero ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+  float want = zero ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+  if (!(want < __builtin_inff())) want = (0.5f * hi - 0.5f * lo) / 7.5f;  // hi - lo overflowed
   uint16_t bits = scale_dtype == MOE_DT_BF16 ? from_f32<Bf16>(want).bits : from_f32<Fp16>(want).bits;
   float s = scale_dtype == MOE_DT_BF16 ? bf16_to_f32(bits) : to_f32<Fp16>(Fp16{bits});
   if (bad || !(s < __builtin_inff())) {

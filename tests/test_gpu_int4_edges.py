@@ -339,3 +339,27 @@ def test_pack_has_no_gradient():
         assert not int4.pack(codes, scale, group=64).scale.requires_grad
     with forward_ad.dual_level(), pytest.raises(ValueError, match="tangent"):
         int4.pack(codes, forward_ad.make_dual(scale.detach(), scale.detach()), group=64)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantize_of_the_largest_numbers(group, dtype):
+    """Weights whose range float32 does not hold, but whose scale its type does."""
+    from resident_expert_routing_amd import int4
+    gen = torch.Generator().manual_seed(6)
+    w = ((torch.rand(20, 256, generator=gen) * 2 - 1) * torch.finfo(dtype).max).to(dtype).cuda()
+    for zeros in (False, True):
+        q = int4.quantize(w, group, zeros=zeros)
+        v = w.double().view(20, -1, group)
+        lo, hi = v.amin(2), v.amax(2)
+        assert (hi - lo).max() > torch.finfo(FP32).max
+        want = (hi - lo) / 15 if zeros else torch.maximum(hi, -lo) / 7
+        scale = q.scale.double().transpose(1, 2).reshape(-1, q.scale.shape[1])[:20]
+        assert ((scale - want).abs() <= want * (2.0 ** -8 + 2.0 ** -22)).all()
+        # half a step, and with a zero point its own rounding and the scale's of 15 steps
+        step = scale.unsqueeze(2) * ((1 + 15 * 2.0 ** -8 if zeros else 0.5 + 8 * 2.0 ** -8) + 1e-5)
+        # steps times scale in float64: seven steps of a scale that was rounded up may pass
+        # float32's largest number by that rounding, 2^-9
+        steps = int4.Int4Weight(q.codes, torch.ones_like(q.scale), q.zero, N=20, K=256).dequantize()
+        got = steps.double().view(20, -1, group) * scale.unsqueeze(2)
+        assert ((got - v).abs() <= step).all()
