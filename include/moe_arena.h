@@ -905,7 +905,8 @@ int moe_int4_quantize(const void* w, int N, int K, size_t w_stride, int dtype, i
  * scale over the groups, and one rounding to out_dtype.  For 16-bit activations a group's
  * sum is taken of a * (16 + code) and corrected, so its error is that of a float32 sum of
  * magnitudes up to 31 |a|; values of a above 2^110 may overflow.  fp32 activations are three
- * bf16 parts whose sum they are exactly, against code - zero.
+ * bf16 parts whose sum they are (exactly from 2^-102 up, below that to within 2^-126), against
+ * code - zero; infinite ones are infinite.
  *   G, offsets, index, index_div, and which rows of out are left as they were: as in
  *   moe_int8_matmul.  Made for few rows of each group: weights are read and widened again for
  *   every 16 or 32 rows of a group.

@@ -123,18 +123,21 @@ struct Acts {
     if constexpr (kParts == 1) {
       v[0] = raw[0];
     } else {
-      uint16_t b[3][8];
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float x = __int_as_float(raw[i / 4][i % 4]);
+      for (int i = 0; i < 8; ++i) x[i] = __int_as_float(raw[i / 4][i % 4]);
 #pragma unroll
-        for (int t = 0; t < 3; ++t) {
-          b[t][i] = from_f32<Bf16>(x).bits;
-          x -= bf16_to_f32(b[t][i]);
+      for (int t = 0; t < 3; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[t][j] = (int)__builtin_amdgcn_perm(__float_as_uint(x[2 * j + 1]),
+                                               __float_as_uint(x[2 * j]), 0x07060302u);
+#pragma unroll
+        for (int i = 0; i < 8 && t < 2; ++i) {
+          const float cut = __uint_as_float(__float_as_uint(x[i]) & 0xFFFF0000u);
+          x[i] = t == 0 && x[i] == cut ? 0.0f : x[i] - cut;
         }
       }
-#pragma unroll
-      for (int t = 0; t < 3; ++t) __builtin_memcpy(&v[t], b[t], 16);
     }
   }
 };

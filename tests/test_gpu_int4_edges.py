@@ -363,3 +363,100 @@ def test_quantize_of_the_largest_numbers(group, dtype):
         steps = int4.Int4Weight(q.codes, torch.ones_like(q.scale), q.zero, N=20, K=256).dequantize()
         got = steps.double().view(20, -1, group) * scale.unsqueeze(2)
         assert ((got - v).abs() <= step).all()
+
+
+def agree(got, want, tol):
+    """Where want is a number, within tol; the same infinities and NaN elsewhere."""
+    fine = torch.isfinite(want)
+    got = got.double()
+    assert torch.equal(fine, torch.isfinite(got))
+    assert torch.equal(want.isnan(), got.isnan())
+    inf = ~fine & ~want.isnan()
+    assert torch.equal(want[inf], got[inf])
+    worst = ((got - want).abs() / tol.clamp_min(1e-300))[fine]
+    assert worst.numel() == 0 or float(worst.max()) <= 1, float(worst.max())
+
+
+@pytest.mark.parametrize("dtype", [FP32])
+@pytest.mark.parametrize("group,zeros,swiglu,K", [(128, False, False, 384), (64, True, False, 200),
+                                                  (32, True, True, 650)])
+@pytest.mark.parametrize("at", range(len(FORMS)))
+def test_infinities(at, group, zeros, swiglu, K, dtype):
+    """An infinite activation gives the definition's infinities, and NaN only where the weight is
+    zero or another infinity meets it; other rows' results do not change by a bit."""
+    from resident_expert_routing_amd import int4
+    counts, N, _ = FORMS[at]
+    N = N // 2 + 7 if swiglu else N
+    w, (exact, sc), gen = made(len(counts), 2 * N if swiglu else N, K, group, zeros, seed=at)
+    perm, offsets = bucketing(counts, gen)
+    M = perm.numel()
+    a = torch.randn(M, K, generator=gen).to(dtype)
+    bad = a.clone()
+    inf = float("inf")
+    rows = torch.randperm(M, generator=gen)[:max(1, M // 3)]
+    for i, r in enumerate(rows.tolist()):
+        at_k = torch.randint(0, K, (2,), generator=gen)
+        for n, v in ((0, (inf, -inf, inf, float("nan"))[i % 4]),
+                     (1, (a[r, at_k[1]], a[r, at_k[1]], -inf, 1.0)[i % 4])):
+            bad[r, at_k[n]] = v
+    perm, offsets = perm.cuda(), offsets.cuda()
+    call = lambda x: int4.matmul(x.cuda(), w, offsets=offsets, index=perm, swiglu=swiglu,
+                                 out_dtype=FP32)
+    got, clean = call(bad), call(a)
+    touched = torch.zeros(M, dtype=torch.bool)
+    touched[rows] = True
+    same = ~touched.cuda()[perm.long()]
+    assert torch.equal(got[same], clean[same])
+    x = bad.cuda().double()
+    for g, lo, hi in spans(offsets):
+        xs = x[perm[lo:hi].long()]
+        # products one by one: a library's may meet an infinity with a zero of its own
+        y = torch.stack([(r * exact[g]).sum(1) for r in xs])
+        e = 2 * (K + 16) * 2.0 ** -23 * torch.stack(
+            [(r.abs().nan_to_num(0, 0, 0) * 31 * sc[g]).sum(1) for r in xs])
+        if swiglu:
+            gt, up, eg, eu = y[:, :N], y[:, N:], e[:, :N], e[:, N:]
+            y = gt / (1 + torch.exp(-gt)) * up
+            low = gt == -inf                        # -inf * 0
+            y = torch.where(low, torch.full_like(y, float("nan")), y)
+            s = torch.sigmoid(gt)
+            e = 1.1 * eg * (up.abs() + eu) + (gt * s).abs() * eu + \
+                (1.25 * gt.abs() + 12) * 2.0 ** -24 * y.abs()
+            e = e.nan_to_num(0, 0, 0)
+        agree(got[lo:hi], y, e + 2.0 ** -24 * y.abs().nan_to_num(0, 0, 0) + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", [FP32])
+@pytest.mark.parametrize("group,zeros", [(128, False), (64, True), (32, False)])
+def test_large_and_small_activations(group, zeros, dtype):
+    """Up to the type's largest number and down to 2^-100, against weights of -1, 0 and 1 steps:
+    sums that float32 holds are right."""
+    from resident_expert_routing_amd import int4
+    gen = torch.Generator().manual_seed(3)
+    N, K, rows = 40, 300, 24
+    n = -(-K // group)
+    zero = torch.randint(1, 15, (N, n), dtype=torch.uint8, generator=gen)
+    base = zero.repeat_interleave(group, 1)[:, :K] if zeros else torch.full((N, K), 8, dtype=torch.uint8)
+    codes = (base.int() + torch.randint(-1, 2, (N, K), generator=gen)).to(torch.uint8).cuda()
+    scale = (torch.rand(N, n, generator=gen) + 0.5).mul(2.0 ** -10).to(BF16).cuda()
+    zero = zero.cuda() if zeros else None
+    w = int4.pack(codes, scale, zero, group=group)
+    exact, sc = values(codes, scale, zero, group)
+    big = torch.finfo(dtype).max
+    a = torch.randn(rows, K, generator=gen).clamp(-4, 4)
+    for r in range(rows):
+        if r < 8:                       # one of the largest among ordinary ones
+            a[r, 11 * r + 5] = big * (-1) ** r
+        elif r < 16:                    # all large: sums of at most 128 of them
+            a[r] *= 2.0 ** (117 + (r - 8) // 2 % 2)
+        else:
+            a[r] *= 2.0 ** -100
+    a = a.to(dtype).cuda()
+    got = int4.matmul(a, w, out_dtype=FP32)
+    want = a.double() @ exact.t().contiguous()
+    tol = (K + 16) * 2.0 ** -22 * (a.double().abs() @ sc.t().contiguous()) * (
+        torch.ones(rows, 1, dtype=torch.float64, device="cuda"))
+    tol[16:] *= 31                      # 16-bit activations there: of a (16 + code), corrected
+    tol[:16] += 2.0 ** -20 * want[:16].abs()
+    assert torch.isfinite(want.float()).all()
+    agree(got, want, tol + 2.0 ** -133)
