@@ -904,9 +904,10 @@ int moe_int4_quantize(const void* w, int N, int K, size_t w_stride, int dtype, i
  * with float32 sums of exact products, within each group of weights first, then with its
  * scale over the groups, and one rounding to out_dtype.  For 16-bit activations a group's
  * sum is taken of a * (16 + code) and corrected, so its error is that of a float32 sum of
- * magnitudes up to 31 |a|; values of a above 2^110 may overflow.  fp32 activations are three
- * bf16 parts whose sum they are (exactly from 2^-102 up, below that to within 2^-126), against
- * code - zero; infinite ones are infinite.
+ * magnitudes up to 31 |a|; a result that is no number this way (an infinite activation, or
+ * one above 2^110) is computed again of a * (code - zero), as fp32 activations are from the
+ * start.  Those are three bf16 parts whose sum they are (exactly from 2^-102 up, below that to
+ * within 2^-126).  Infinities and NaN of a touch their own row only.
  *   G, offsets, index, index_div, and which rows of out are left as they were: as in
  *   moe_int8_matmul.  Made for few rows of each group: weights are read and widened again for
  *   every 16 or 32 rows of a group.

@@ -9,7 +9,8 @@
 // with the second sum from the same instruction against ones, and only finished group
 // sums meet the scales, all in float32.  16 is the smallest offset that lets all sixteen
 // codes share an exponent, so the subtraction costs about two bits of float32; activations
-// of 32 bits, whose result would show that, take c - z itself, with more instructions.
+// of 32 bits, whose result would show that, take c - z itself, with more instructions, and so
+// do sums of the others that end as no number.
 #include <type_traits>
 
 #include "groups.hpp"
@@ -159,13 +160,17 @@ __device__ __forceinline__ void store_out(const Int4Args& p, int m, int n, const
     store4<float>(p, m, n, y);
 }
 
-// Eight codes less their zero point: small integers, exact in bf16.
+// Eight codes less their zero point: small integers, exact in both types.
+template <bool HALF>
 __device__ __forceinline__ i32x4 centered(uint32_t w, float zero) {
   i32x4 v;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float lo = (float)(w >> (4 * j) & 15u) - zero, hi = (float)(w >> (16 + 4 * j) & 15u) - zero;
-    v[j] = (int)__builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+    if constexpr (HALF)
+      v[j] = (int)(from_f32<Fp16>(lo).bits | (uint32_t)from_f32<Fp16>(hi).bits << 16);
+    else
+      v[j] = (int)__builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
   }
   return v;
 }
@@ -208,29 +213,39 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
   const Widen<HALF> widen;
   const int first = n0 + wn * (GLU ? NT / 2 : NT) * 16;  // the wave's first column of out
 
-  const uint8_t* codes[NT];
-  const uint16_t* scale[NT];
-  const uint8_t* zero[NT];
+  // where lane l reads
+  struct Sources {
+    const uint8_t* codes[NT];
+    const uint16_t* scale[NT];
+    const uint8_t* zero[NT];
+    const E* arow[MT];
+  };
   const bool zeros = p.zero != nullptr;
+  auto sources = [&](int l) {
+    Sources from;
+    const int col = l & 15, quad = l >> 4;
 #pragma unroll
-  for (int s = 0; s < NT; ++s) {
-    const bool up = GLU && s >= NT / 2;
-    const int row =
-        min(first + 16 * (up ? s - NT / 2 : s) + (up ? p.N : 0) + col, p.rows - 1);
-    const size_t block = (size_t)(row / kBlock) * p.chunks;
-    codes[s] = p.codes + (size_t)r.g * p.codes_group_stride + block * kTileBytes +
-               row % kBlock * (kCodes / 2) + 16 * quad;
-    const size_t at = block * QUADS * kBlock + row % kBlock;
-    scale[s] = p.scale + (size_t)r.g * p.scale_group_stride + at;
-    // without zero points any bytes are read in their place, those of the scales
-    zero[s] = zeros ? p.zero + (size_t)r.g * p.zero_group_stride + at : (const uint8_t*)scale[s];
-  }
-  const E* arow[MT];
+    for (int s = 0; s < NT; ++s) {
+      const bool up = GLU && s >= NT / 2;
+      const int row =
+          min(first + 16 * (up ? s - NT / 2 : s) + (up ? p.N : 0) + col, p.rows - 1);
+      const size_t block = (size_t)(row / kBlock) * p.chunks;
+      from.codes[s] = p.codes + (size_t)r.g * p.codes_group_stride + block * kTileBytes +
+                      row % kBlock * (kCodes / 2) + 16 * quad;
+      const size_t at = block * QUADS * kBlock + row % kBlock;
+      from.scale[s] = p.scale + (size_t)r.g * p.scale_group_stride + at;
+      // without zero points any bytes are read in their place, those of the scales
+      from.zero[s] = zeros ? p.zero + (size_t)r.g * p.zero_group_stride + at
+                           : (const uint8_t*)from.scale[s];
+    }
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int src = source_row(p, min(r.lo + 16 * t + col, r.hi - 1));
-    arow[t] = (const E*)p.a + (size_t)max(src, 0) * p.a_stride + 8 * quad;
-  }
+    for (int t = 0; t < MT; ++t) {
+      const int src = source_row(p, min(r.lo + 16 * t + col, r.hi - 1));
+      from.arow[t] = (const E*)p.a + (size_t)max(src, 0) * p.a_stride + 8 * quad;
+    }
+    return from;
+  };
+  const Sources from = sources(lane);
   i32x4 ones;
 #pragma unroll
   for (int i = 0; i < 4; ++i) ones[i] = HALF ? 0x3C003C00 : 0x3F803F80;
@@ -243,14 +258,14 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
   const uint32_t is_bf16 = p.scale_dtype == MOE_DT_BF16 ? ~0u : 0u;
   constexpr uint32_t kOffset = kExact ? 0 : 16;
   const uint32_t given = zeros ? 0xFFu : 0u, offset = zeros ? kOffset : kOffset + 8;
-  auto load_codes = [&](i32x4 (&w)[NT], int c) {
+  auto load_codes = [&](const Sources& from, i32x4 (&w)[NT], int c) {
 #pragma unroll
-    for (int s = 0; s < NT; ++s) w[s] = __builtin_nontemporal_load((const i32x4*)(codes[s] + (size_t)c * kTileBytes));
+    for (int s = 0; s < NT; ++s) w[s] = __builtin_nontemporal_load((const i32x4*)(from.codes[s] + (size_t)c * kTileBytes));
   };
-  auto load_side = [&](Side& w, int group) {  // of groups group .. + 3
+  auto load_side = [&](const Sources& from, Side& w, int group) {  // of groups group .. + 3
     const size_t at = (size_t)min(group + quad, p.chunks * QUADS - 1) * kBlock;
 #pragma unroll
-    for (int s = 0; s < NT; ++s) w.s[s] = scale[s][at], w.z[s] = zero[s][at];
+    for (int s = 0; s < NT; ++s) w.s[s] = from.scale[s][at], w.z[s] = from.zero[s][at];
   };
   f32x4 acc[MT][NT] = {}, dot[MT][NT], sum[MT];
   // products of quarter j of a tile; the first of a group of weights starts its sums
@@ -260,7 +275,7 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
     i32x4 wide[NT];
 #pragma unroll
     for (int s = 0; s < NT; ++s)
-      wide[s] = kExact ? centered(word[s][j], (float)(side[s][q] >> 16)) : widen(word[s][j]);
+      wide[s] = kExact ? centered<HALF>(word[s][j], (float)(side[s][q] >> 16)) : widen(word[s][j]);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       i32x4 v[Acts<E>::kParts];
@@ -274,12 +289,15 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
       }
     }
   };
+  auto scale_of = [&](uint32_t side) {
+    const uint32_t bits = side & 0xFFFFu;
+    const float half = to_f32<Fp16>(Fp16{(uint16_t)bits});
+    return __uint_as_float((bits << 16 & is_bf16) | (__float_as_uint(half) & ~is_bf16));
+  };
   auto finish = [&](const uint32_t (&side)[NT][4], int q) {  // a group's sums
 #pragma unroll
     for (int s = 0; s < NT; ++s) {
-      const uint32_t bits = side[s][q] & 0xFFFFu;
-      const float half = to_f32<Fp16>(Fp16{(uint16_t)bits});
-      const float sc = __uint_as_float((bits << 16 & is_bf16) | (__float_as_uint(half) & ~is_bf16));
+      const float sc = scale_of(side[s][q]);
       const float off = (float)(side[s][q] >> 16);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -314,11 +332,11 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
     auto load_acts = [&](Acts<E> (&to)[MT], int step) {
       const int k = lo * kCodes + 32 * min(step, last);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) to[t].load(arow[t] + k);
+      for (int t = 0; t < MT; ++t) to[t].load(from.arow[t] + k);
     };
 #pragma unroll
-    for (int u = 0; u < kCodesAhead; ++u) load_codes(w[u], min(lo + u, hi - 1));
-    load_side(next, lo * QUADS);
+    for (int u = 0; u < kCodesAhead; ++u) load_codes(from, w[u], min(lo + u, hi - 1));
+    load_side(from, next, lo * QUADS);
 #pragma unroll
     for (int u = 0; u < kActsAhead; ++u) load_acts(x[u], u);
     for (int c0 = lo; c0 < hi; c0 += 4) {
@@ -327,10 +345,10 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
       for (int u = 0; u < 4; ++u) {
         const int c = c0 + u;
         if (c >= hi) break;
-        load_codes(w[(u + kCodesAhead) % kRing], min(c + kCodesAhead, hi - 1));
+        load_codes(from, w[(u + kCodesAhead) % kRing], min(c + kCodesAhead, hi - 1));
         if (u % kRun == 0) {
           spread_side(next, side);
-          load_side(next, (c + kRun) * QUADS);
+          load_side(from, next, (c + kRun) * QUADS);
         }
         uint32_t word[NT][4];
         words(w[u % kRing], word);
@@ -349,8 +367,8 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
     i32x4 w[NT];
     Side s;
     uint32_t word[NT][4], side[NT][4];
-    load_codes(w, full);
-    load_side(s, full * QUADS);
+    load_codes(from, w, full);
+    load_side(from, s, full * QUADS);
     words(w, word);
     spread_side(s, side);
 #pragma unroll
@@ -358,12 +376,75 @@ __device__ __forceinline__ void int4_tile(const Int4Args& p, const Rows& r, int 
       const int k = full * kCodes + 32 * j;
       Acts<E> x[MT];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) x[t].load_head(arow[t] + k, p.K - k - 8 * quad);
+      for (int t = 0; t < MT; ++t) x[t].load_head(from.arow[t] + k, p.K - k - 8 * quad);
       // a group that begins behind the row has no scale: its weights are padding
       const int q = j / (4 / QUADS);
       multiply(word, side, q, j, x);
       if ((j + 1) % (4 / QUADS) == 0 && full * kCodes + q * (kCodes / QUADS) < p.K)
         finish(side, q);
+    }
+  }
+
+  // Sums that are no numbers once more, of codes less their zero points: of a * (16 + c) and
+  // their correction an infinite activation, or one so large that 31 of it are, makes a NaN
+  // where the definition has an infinity or a number.  Other sums keep what they are.
+  if constexpr (!kExact) {
+    bool fine = true;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int s = 0; s < NT; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fine = fine && fabsf(acc[t][s][i]) < __builtin_inff();
+    if (__builtin_expect(!__all(fine), 0)) {
+      // addresses of its own: kept over the main loop, the first ones cost it a wave a SIMD
+      int l = lane;
+      asm("" : "+v"(l));
+      const Sources from = sources(l);
+      f32x4 again[MT][NT] = {};
+      const int end = wk == WK - 1 ? p.chunks : hi;
+#pragma unroll 1
+      for (int c = lo; c < end; ++c) {
+        i32x4 w[NT];
+        Side near;
+        uint32_t word[NT][4], side[NT][4];
+        load_codes(from, w, c);
+        load_side(from, near, c * QUADS);
+        words(w, word);
+        spread_side(near, side);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = c * kCodes + 32 * j, q = j / (4 / QUADS);
+          const bool fresh = j % (4 / QUADS) == 0, last = (j + 1) % (4 / QUADS) == 0;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            Acts<E> x;
+            i32x4 v[1];
+            x.load_head(from.arow[t] + k, p.K - k - 8 * quad);
+            x.parts(v);
+#pragma unroll
+            for (int s = 0; s < NT; ++s)
+              dot[t][s] = mma<HALF>(v[0], centered<HALF>(word[s][j], (float)(side[s][q] >> 16) - 16.0f),
+                                    fresh ? f32x4{} : dot[t][s]);
+          }
+          if (last && c * kCodes + q * (kCodes / QUADS) < p.K) {
+#pragma unroll
+            for (int s = 0; s < NT; ++s)
+#pragma unroll
+              for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  again[t][s][i] = fmaf(scale_of(side[s][q]), dot[t][s][i], again[t][s][i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(fabsf(acc[t][s][i]) < __builtin_inff())) acc[t][s][i] = again[t][s][i];
     }
   }
 

@@ -377,7 +377,7 @@ def agree(got, want, tol):
     assert worst.numel() == 0 or float(worst.max()) <= 1, float(worst.max())
 
 
-@pytest.mark.parametrize("dtype", [FP32])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("group,zeros,swiglu,K", [(128, False, False, 384), (64, True, False, 200),
                                                   (32, True, True, 650)])
 @pytest.mark.parametrize("at", range(len(FORMS)))
@@ -426,7 +426,7 @@ def test_infinities(at, group, zeros, swiglu, K, dtype):
         agree(got[lo:hi], y, e + 2.0 ** -24 * y.abs().nan_to_num(0, 0, 0) + 1e-30)
 
 
-@pytest.mark.parametrize("dtype", [FP32])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("group,zeros", [(128, False), (64, True), (32, False)])
 def test_large_and_small_activations(group, zeros, dtype):
     """Up to the type's largest number and down to 2^-100, against weights of -1, 0 and 1 steps:
