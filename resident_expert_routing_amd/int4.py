@@ -54,15 +54,16 @@ class Int4Weight:
         if scale.dtype not in SCALES:
             raise ValueError(f"scales are bfloat16 or float16, not {scale.dtype}")
         lead = tuple(codes.shape[:-4])
-        if scale.dim() != len(lead) + 3 or tuple(scale.shape[:-2]) != (*lead, blocks) or \
-                scale.shape[-1] != 16 or all(scale.shape[-2] * g != _up(K, 128) for g in GROUPS):
+        groups = scale.shape[-2] if scale.dim() == len(lead) + 3 else 0
+        if groups < 1 or tuple(scale.shape[:-2]) != (*lead, blocks) or scale.shape[-1] != 16 or \
+                chunks * 128 % groups or chunks * 128 // groups not in GROUPS:
             raise ValueError(f"scale {list(scale.shape)} does not fit groups of 32, 64 or 128 "
                              f"weights of {list(lead)} matrices {N} x {K}")
         if zero is not None and (gpu_tensor(zero, "zero", dev).dtype != torch.uint8
                                  or zero.shape != scale.shape):
             raise ValueError("zero must be uint8 of scale's shape")
         _no_gradient("Int4Weight", scale)
-        self.group = _up(K, 128) // scale.shape[-2]
+        self.group = chunks * 128 // groups
         self.N, self.K, self.G = int(N), int(K), (lead[0] if lead else 0)
         for t, what, unit, inner in ((codes, "codes", 16, 4), (scale, "scale", 4, 3),
                                      (zero, "zero", 4, 3)):
