@@ -24,7 +24,12 @@ constexpr int kMaxRows = 1 << 30;
 // s from exp(-|g|), which cannot overflow.  Below kLow, where 1 - s is 1 in float32, exp(g)
 // is applied as two factors exp(g / 2), so that a gradient that is still a normal number
 // keeps its value to g = -174: d * u meets them first, or where float32 does not hold it
-// (then both are above 1) each of d and u one of them.  Bound by memory.
+// (then both are above 1) each of d and u one of them.  Bound by memory (32768 rows of 2048
+// bf16, 0.94 GB: 147 us).
+// The result is rounded to the element type, since both gradients' products take it as an
+// operand of the matrix instruction: with their own rounding the gradients of a bf16 step are
+// off by 2.35e-3 of the norm, without it by 1.66e-3 (float32 torch); two parts of 16 bits would
+// double both products.  In fp16 values past 65504 are infinite.
 template <typename E>
 __global__ __launch_bounds__(256) void swiglu_backward_rows(int M, int N, const float* pre,
                                                             size_t pre_stride, const E* dout,

@@ -900,7 +900,8 @@ __global__ __launch_bounds__(256) void outer_sum(OuterProduct p) {
 
 // Tiles of n x n, whether they are few, and into how many parts a group's rows are then cut:
 // enough for two workgroups a CU, of 512 rows at least, counted for groups of equal sizes (two
-// groups of 16384 rows, 256 x 192: 24 tiles).
+// groups of 16384 rows, 256 x 192: 24 tiles).  Few are counted without the rows, so moderate
+// matrices over many rows take the small tiles too (eight groups of 1024 x 1024: 128 large ones).
 inline int64_t outer_tiles_of(int L, int R, int G, int n) {
   return (int64_t)G * ((L + n - 1) / n) * ((R + n - 1) / n);
 }

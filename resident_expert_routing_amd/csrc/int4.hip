@@ -528,8 +528,9 @@ void launch_form(const Int4Args& p, int group, hipStream_t stream) {
 // (8 groups of one row: 24 us in the first form, 20 with four waves), all eight of them
 // where even then CUs would be left without a workgroup (one token, 8.4 MB: 6.1 us).  Groups
 // of more rows take tiles of 32, for which weights are widened once (8192 rows over 166
-// groups: 790 us against 961; 2048 rows: 501 against 443); tiles of 64 do not fit the
-// registers (1005).
+// groups: 790 us against 961; 2048 rows: 501 against 443), where groups and columns alone are
+// a workgroup for every CU: tiles of rows are not counted, so dense products and few long
+// groups stay at 16 rows.  Tiles of 64 do not fit the registers (1005).
 template <typename E, bool GLU>
 void launch_matmul(const Int4Args& p, int group, hipStream_t stream) {
   using Few = Form<1, 2, 8, 1>;

@@ -257,7 +257,7 @@ class Int8Experts:
         [T*k, H] (as many rows as perm has), row p from token perm[p] // k; rows
         that are in no slot are undefined.  The second products' inputs are
         rounded to inner_dtype before they are quantised: bf16, half the bytes of
-        float32 and off by at most 2^-9 of a value where the 8-bit step is 2^-7 of
+        float32 and off by at most 2^-8 of a value where the 8-bit step is 2^-7 of
         the row's largest, whatever x's type; float32 leaves the one rounding to 8
         bits (fp16 overflows at 65504)."""
         self.check(x, x.shape[0], out_dtype, inner_dtype)

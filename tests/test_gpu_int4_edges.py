@@ -359,7 +359,7 @@ def test_quantize_of_the_largest_numbers(group, dtype):
         # half a step, and with a zero point its own rounding and the scale's of 15 steps
         step = scale.unsqueeze(2) * ((1 + 15 * 2.0 ** -8 if zeros else 0.5 + 8 * 2.0 ** -8) + 1e-5)
         # steps times scale in float64: seven steps of a scale that was rounded up may pass
-        # float32's largest number by that rounding, 2^-9
+        # float32's largest number by that rounding, 2^-8
         steps = int4.Int4Weight(q.codes, torch.ones_like(q.scale), q.zero, N=20, K=256).dequantize()
         got = steps.double().view(20, -1, group) * scale.unsqueeze(2)
         assert ((got - v).abs() <= step).all()
