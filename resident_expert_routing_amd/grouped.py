@@ -219,8 +219,6 @@ class GroupedExperts:
     and to the weights of the sum."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor):
-        gpu_tensor(gate_up, "gate_up")
-        gpu_tensor(down, "down")
         if gate_up.dim() != 3 or gate_up.shape[1] % 2 or tuple(down.shape) != \
                 (gate_up.shape[0], gate_up.shape[2], gate_up.shape[1] // 2):
             raise ValueError(f"down {list(down.shape)} does not fit gate_up {list(gate_up.shape)}")
@@ -229,15 +227,18 @@ class GroupedExperts:
         self._check_matrices()
 
     def _check_matrices(self) -> None:
-        gpu_tensor(self.down, "down", gpu_tensor(self.gate_up, "gate_up").get_device())
-        dtype_of(self.gate_up, "gate_up")
-        if self.down.dtype != self.gate_up.dtype:
-            raise ValueError(f"gate_up is {self.gate_up.dtype}, down {self.down.dtype}")
+        gate_up, down = self.gate_up, self.down
+        dtype_of(gate_up, "gate_up")
+        if down.dtype != gate_up.dtype or down.device != gate_up.device:
+            raise ValueError(f"gate_up is {gate_up.dtype} on {gate_up.device}, down {down.dtype} on "
+                             f"{down.device}")
 
     def check(self, x, T: int) -> None:
         """Refuses token rows that are not [T, H] of the experts' type and device, matrices
-        that differ in either (a parameter's may change after it was given), and tangents."""
+        that are not on a GPU or differ in either (a model's parameters may be moved or cast
+        after they were given), and tangents."""
         self._check_matrices()
+        gpu_tensor(self.gate_up, "gate_up")
         if forward_ad._current_level >= 0:
             no_tangent("GroupedExperts", x, self.gate_up, self.down)
         gpu_tensor(x, "x", self.gate_up.get_device())

@@ -477,7 +477,7 @@ def test_experts_that_do_not_fit():
     buf, x, (wg, wu, wd), args = routed(8, 64, 8, 2, 32, 6, 6, 0)
     gu, dn = torch.cat([wg, wu], 1).to(BF16), wd.to(BF16)
     for bad in ((gu, dn.float()), (gu.float(), dn), (gu, dn.to(FP16)), (gu, dn.cpu()), (gu.cpu(), dn),
-                (gu.cpu(), dn.cpu()), (gu.int(), dn.int()), (gu[0], dn), (gu, dn[0]),
+                (gu.int(), dn.int()), (gu[0], dn), (gu, dn[0]),
                 (gu, dn.transpose(1, 2))):
         with pytest.raises(ValueError):
             grouped.GroupedExperts(*bad)
@@ -496,11 +496,20 @@ def test_experts_that_do_not_fit():
             pair[which] = forward_ad.make_dual(pair[which].detach(), torch.ones_like(pair[which]))
             with pytest.raises(ValueError, match="tangent"):
                 step(grouped.GroupedExperts(*pair))
+    with pytest.raises(ValueError, match="GPU"):
+        step(grouped.GroupedExperts(gu.cpu(), dn.cpu()))
     ex = grouped.GroupedExperts(gu, dn)
     with pytest.raises(ValueError):
         step(ex, R.LayerBuffers(8, 64, 8, 2, 32, 6, torch.device("cpu")))
     assert not hist.any()
-    assert step(ex).shape == x.shape and hist.any()
+    want = step(ex)
+    assert want.shape == x.shape and hist.any()
+    # a model may be made on the host and moved as a whole
+    pair = [torch.nn.Parameter(t.cpu()) for t in (gu, dn)]
+    ex = grouped.GroupedExperts(*pair)
+    for t in pair:
+        t.data = t.data.cuda()
+    assert torch.equal(step(ex), want)
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
